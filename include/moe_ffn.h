@@ -424,6 +424,218 @@ int moe_quantize_token_blocks(const void* src, int ld, int src_rows, const int32
 int moe_quantize_act_rows(const void* src, int rows, int cols, uint8_t* codes, int32_t* exps,
                           void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Around the layer: the router with its balance loss, the gradient of the
+ * gates, the norms before and after the block, and the optimizer of the
+ * layer's weights.  Rows of a matrix argument are `ld` elements apart (ld >=
+ * its columns), the elements of a row lie side by side.
+ * ------------------------------------------------------------------------- */
+#define MOE_DEV_BAD_LOGIT 16   /* a router row in use holds NaN or +infinity (it is routed nowhere) */
+
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* A top-k router over E experts.  dtype (MOE_F32 or MOE_BF16): the logits'.
+ * With s the score's logarithm, s_e = l_e (softmax) or log sigmoid(l_e):
+ *   P_te = exp(s_te) / sum_i exp(s_ti),
+ *   gate of a chosen expert = scale * P_te / (sum of P over the chosen) when
+ *   renorm != 0, else scale * P_te (softmax) or scale * sigmoid(l_te).
+ * The chosen experts are the k largest logits, the lower index among equals
+ * (-0 equals 0), in descending order. */
+typedef struct {
+  int E, k;
+  int dtype;
+  int score;
+  int renorm;
+  float scale;
+} moe_router;
+
+/* Workspace of moe_router_forward for T tokens; 0 for invalid arguments. */
+size_t moe_router_workspace_size(const moe_router* R, int T);
+
+/* Routing of T tokens and the losses that balance it.
+ *   logits [T][E], rows ld apart.  An expert whose logit is -infinity is never
+ *     chosen; with fewer than k others the remaining ids are -1, gates 0.
+ *   token_mask [T] (nullable): 0 = padding.  A padding row, whatever it holds,
+ *     and a row of -infinities alone are routed nowhere (ids -1, gates 0) and
+ *     enter no sum; so is a row in use with NaN or +infinity, which also sets
+ *     MOE_DEV_BAD_LOGIT in *status_dev.
+ *   topk_ids [T][k], gates [T][k] fp32: what moe_route_stats and moe_forward take.
+ *   counts [E]: c_e, (token, slot) pairs routed to e.  prob_sum [E]: sum_t P_te.
+ *   live [1]: n, the rows that are routed.
+ *   losses [2]: balance = E / (k n^2) * sum_e c_e prob_sum_e (1 when both are
+ *     even), z = 1/n sum_t (log sum_e exp(l_te))^2; 0 when n = 0.
+ * Sums over tokens are made in a fixed order: the same call gives the same bits.
+ * Errors: MOE_ERR_ARG for E < 1, k < 1, k > E, ld < E, T < 0, an unknown dtype
+ *   or score, a scale that is not finite or a null pointer;
+ *   MOE_ERR_UNSUPPORTED for E > 1024, k > 32 or T * k >= 2^31;
+ *   MOE_ERR_WORKSPACE for a missing, misaligned or short workspace. */
+int moe_router_forward(const moe_router* R, const void* logits, int ld,
+                       const uint8_t* token_mask, int T, int32_t* topk_ids, float* gates,
+                       int32_t* counts, float* prob_sum, int32_t* live, float* losses,
+                       int32_t* status_dev, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of the logits.
+ *   topk_ids, counts, live: moe_router_forward's, on the same logits and mask.
+ *   dlogp [T][k] fp32 (nullable): p * dL/dp of each gate p, its gradient in log
+ *     form, as moe_backward_gates and moe_gate_grad give it; read where the id
+ *     is in [0, E).
+ *   dlosses [2] (device, nullable): dL/dbalance and dL/dz.
+ *   dlogits [T][E], rows ld_out apart, the logits' dtype; rows that are routed
+ *     nowhere receive zeros.  It may be the logits themselves (ld_out = ld).
+ * With h = dlogp put on the chosen experts, H its sum, b and z the two of
+ * dlosses, g_e = b E c_e / (k n^2) and q the chosen experts' renormalised gates:
+ *   ds_e = h_e - H q_e (renorm), h_e - H P_e (softmax) or h_e (sigmoid)
+ *          + P_e (g_e - sum_i P_i g_i),
+ *   dl_e = ds_e (sigmoid: times sigmoid(-l_e)) + 2 z / n lse(l) softmax(l)_e.
+ * No gate is divided by, so a gate that is 0 has a gradient like any other.
+ * Errors: as moe_router_forward, without a workspace. */
+int moe_router_backward(const moe_router* R, const void* logits, int ld,
+                        const uint8_t* token_mask, int T, const int32_t* topk_ids,
+                        const float* dlogp, const int32_t* counts, const int32_t* live,
+                        const float* dlosses, void* dlogits, int ld_out, void* stream);
+
+/* Gate gradients in log form from the layer's saved rows: since dU = dA SiLU(G)
+ * and D = p dy, the contribution p O of a row has
+ *   p * dL/dp = <dy, p O> = <dA, SiLU(G) U> = <dU, U>.
+ *   z [slots][2*d_ff]: z_save, rows [G, U]; dz the same of [dG, dU], dtype
+ *   MOE_F32 or MOE_BF16; row_to_slot [rows] (an entry outside [0, slots): 0).
+ *   dlogp [rows] fp32.
+ * Errors: MOE_ERR_ARG for negative rows or slots, d_ff < 1, a bad dtype or a
+ *   null pointer; MOE_ERR_UNSUPPORTED when d_ff is not a multiple of 64. */
+int moe_gate_grad(const void* z, const void* dz, int dtype, const int32_t* row_to_slot, int rows,
+                  int slots, int d_ff, float* dlogp, void* stream);
+
+/* moe_backward, and the gate gradients of its rows: dlogp [T][k] fp32 receives
+ * p_tj * dL/dp_tj (moe_gate_grad on the rows [dG, dU] inside the workspace, as
+ * they are before the token-axis requantization); 0 where topk_ids < 0. */
+int moe_backward_gates(const moe_layer* L, const void* x, const float* gates, const void* dy,
+                       const void* z_save, const int32_t* topk_ids, int T, int k, int beta,
+                       int P, int s, const int32_t* counts, const int32_t* block_offsets,
+                       const int32_t* row_to_slot, const int32_t* slot_to_row,
+                       const int32_t* owner, const int32_t* block_worker, void* dx, float* dw1,
+                       float* dw2, float* dlogp, int32_t* status_dev, void* ws, size_t ws_bytes,
+                       int exec_flags, void* const* stage_events, uint64_t* timeline,
+                       void* stream);
+
+/* Norm of T rows of d features, with a gate and a residual scale around it.
+ * rms(v) = sqrt(mean(v^2) + eps); dtype (MOE_F32 or MOE_BF16) is the rows',
+ * w [d] is of w_dtype (MOE_F32 or the rows'); the gate g is none (1), one
+ * number per token (gate [T]) or per feature (gate [d]), fp32; alpha a constant.
+ *   before the block:  r = x + alpha g u,  n = w r / rms(r)
+ *   after the block:   out = x + alpha g w y / rms(y)
+ * Sums are fp32, over a row and over the tokens in a fixed order; r's rounding
+ * does not enter n.  An output may be the same memory as an input with the same
+ * row stride. */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_FEATURE = 2 } moe_gate_kind;
+typedef struct {
+  int T, d;
+  int dtype, w_dtype;
+  int gate_kind;
+  float alpha, eps;
+  const void* w;
+  const float* gate;
+} moe_norm;
+
+/* Workspace of the norms' backward passes; 0 for invalid arguments. */
+size_t moe_norm_workspace_size(int T, int d);
+
+/* Before the block.  u (nullable) [T][d]: what the residual stream takes up, r
+ * (nullable) the updated stream; without u, r is a copy of x and the gate must
+ * be none.  rstd [T] = 1 / rms(r), for the backward pass.
+ * Errors: MOE_ERR_ARG for d < 1, T < 0, eps <= 0 or not finite, alpha not
+ *   finite, a row stride below d, an unknown dtype or gate kind, a gate without
+ *   u or a null pointer; MOE_ERR_UNSUPPORTED for d > 16384 or a w_dtype that
+ *   is neither MOE_F32 nor dtype. */
+int moe_norm_in(const moe_norm* N, const void* x, int ldx, const void* u, int ldu, void* r,
+                int ldr, void* n, int ldn, float* rstd, void* stream);
+
+/* Its gradients.  dn [T][d]: of n; dr (nullable): what reaches r from elsewhere;
+ * r: the updated stream as stored; rstd: the forward's.
+ *   dx = dr + rstd (w dn - rhat mean(w dn rhat)), rhat = r rstd;  du = alpha g dx
+ *   dw = sum_t dn rhat;  dgate = alpha sum u dx over the features (token) or
+ *   the tokens (feature), like the gate, nullable with gate none.
+ * u and du (both or neither) as in the forward pass.  dw [d], dgate fp32. */
+int moe_norm_in_backward(const moe_norm* N, const void* dn, int lddn, const void* dr, int lddr,
+                         const void* r, int ldr, const void* u, int ldu, const float* rstd,
+                         void* dx, int lddx, void* du, int lddu, float* dw, float* dgate,
+                         void* ws, size_t ws_bytes, void* stream);
+
+/* After the block: y [T][d] its output, x the residual stream. */
+int moe_norm_out(const moe_norm* N, const void* y, int ldy, const void* x, int ldx, void* out,
+                 int ldout, float* rstd, void* stream);
+
+/* Its gradients, with dv = alpha g dout and yhat = y rstd (x's is dout itself):
+ *   dy = rstd (w dv - yhat mean(w dv yhat));  dw = sum_t dv yhat;
+ *   dgate = alpha sum dout w yhat. */
+int moe_norm_out_backward(const moe_norm* N, const void* dout, int lddo, const void* y, int ldy,
+                          const float* rstd, void* dy, int lddy, float* dw, float* dgate, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* AdamW over a list of tensors in one launch.  With t the step (1, 2, ...),
+ *   g = grad * grad_scale;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr wd) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32.  A tensor of n elements (n >= 0) has p in fp32 or bf16, optionally
+ * with an fp32 master copy that is updated and rounded to nearest into a bf16
+ * p; a bf16 p without one is rounded at random, so that steps below half a
+ * step of bf16 are kept on average.
+ * state_bits 32: m, v fp32.  state_bits 8: m and sqrt(v) as OCP e4m3 codes in
+ * blocks of MOE_ADAMW_BLOCK elements, each block with one fp32 scale (m_scale,
+ * v_scale [ceil(n / MOE_ADAMW_BLOCK)]): value = code * scale, scale = (largest
+ * finite magnitude of the block) / 448.  Codes are rounded at random: rounded
+ * to nearest, a state whose change per step is below half a code step would
+ * never move.  A block whose magnitudes are all below 2^-100 is stored as
+ * zeros; a state that is not finite becomes the NaN code of its element alone.
+ * Start with zero codes and zero scales.
+ * The random word of element i of the list's tensor j at step t is
+ *   mix(i G + mix(seed + t G + j C3)),  mix(x): x ^= x >> 16; x *= C2; x ^= x >> 15
+ * modulo 2^32 (G = 0x9E3779B9, C2 = 0x6A09E667, C3 = 0xBB67AE85): its low 16
+ * bits round m, its high ones v, the high ones of its product with C3 p. */
+#define MOE_ADAMW_BLOCK 128
+#define MOE_ADAMW_MAX_TENSORS 4096
+typedef struct {
+  void* p;
+  float* master;         /* NULL: none */
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;        /* state_bits 8 only */
+  float* v_scale;
+  int64_t n;
+  int p_dtype, g_dtype;  /* MOE_F32 or MOE_BF16 */
+} moe_adamw_tensor;
+
+/* A prepared list (host): made by moe_adamw_prepare, valid while its workspace and tensors are. */
+typedef struct {
+  const void* table;     /* device */
+  int tensors, state_bits;
+  uint32_t items;
+} moe_adamw_list;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;   /* 1 - beta is taken in double */
+  int step;                    /* >= 1; not read when step_dev is given */
+  uint32_t seed;
+  const int32_t* step_dev;     /* device, nullable: the step, for captured graphs */
+  const float* lr_dev;         /* device, nullable: the learning rate instead of lr */
+  const float* grad_scale;     /* device, nullable: 1 */
+} moe_adamw_hyper;
+
+size_t moe_adamw_workspace_size(int tensors);
+
+/* Writes the list's table into ws on `stream`; *out (host) is what moe_adamw takes.
+ * Errors: MOE_ERR_ARG for a count outside [0, MOE_ADAMW_MAX_TENSORS], a null or
+ *   misaligned pointer of a tensor with n > 0, an unknown dtype, a master of a
+ *   tensor that is not bf16, or memory that two of the buffers written or a
+ *   buffer written and a gradient share; MOE_ERR_UNSUPPORTED for state_bits
+ *   other than 8 or 32 or above 2^43 elements; MOE_ERR_WORKSPACE. */
+int moe_adamw_prepare(const moe_adamw_tensor* tensors, int count, int state_bits,
+                      moe_adamw_list* out, void* ws, size_t ws_bytes, void* stream);
+
+/* One step on every tensor of the list.
+ * Errors: MOE_ERR_ARG for a null list, beta1 or beta2 outside [0, 1), eps <= 0,
+ *   step < 1 (without step_dev) or a lr or weight_decay that is not finite. */
+int moe_adamw(const moe_adamw_list* list, const moe_adamw_hyper* h, void* stream);
+
 /* Timing helpers so a caller without a HIP binding can time the stages:
  * create / destroy a hipEvent_t, and the milliseconds between two recorded
  * events (waits for `b`). */

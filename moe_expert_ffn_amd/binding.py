@@ -20,6 +20,10 @@ MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0, -1
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 PLAN_FWD, PLAN_BWD, PLAN_QUOTA = 0, 1, 2
 DEV_BAD_EXPERT, DEV_BAD_PLAN, DEV_BAD_OWNER, DEV_WAIT_TIMEOUT = 1, 2, 4, 8
+DEV_BAD_LOGIT = 16
+SCORES = {"softmax": 0, "sigmoid": 1}         # moe_score
+GATE_NONE, GATE_TOKEN, GATE_FEATURE = 0, 1, 2  # moe_gate_kind
+ADAMW_BLOCK = 128                             # MOE_ADAMW_BLOCK
 EXEC_TWO_PHASE = 1              # MOE_EXEC_TWO_PHASE
 EXEC_SPLIT_SHIFT = 8            # MOE_EXEC_SPLIT(n1) = n1 << 8
 EXEC_FP8_ACT = 2                # MOE_EXEC_FP8_ACT
@@ -43,7 +47,11 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_max_slots", "moe_max_blocks
            "moe_plan_gate",
            "moe_predict_cost", "moe_predict_split", "moe_quantize_token_blocks",
            "moe_quantize_act_rows", "moe_forward",
-           "moe_backward",
+           "moe_backward", "moe_backward_gates", "moe_gate_grad",
+           "moe_router_workspace_size", "moe_router_forward", "moe_router_backward",
+           "moe_norm_workspace_size", "moe_norm_in", "moe_norm_in_backward", "moe_norm_out",
+           "moe_norm_out_backward",
+           "moe_adamw_workspace_size", "moe_adamw_prepare", "moe_adamw",
            "moe_event_create", "moe_event_destroy", "moe_event_record", "moe_event_elapsed_ms",
            "moe_device_info"]
 
@@ -57,6 +65,36 @@ class Layer(ctypes.Structure):
                 ("act_dtype", ctypes.c_int), ("w_dtype", ctypes.c_int),
                 ("w1", ctypes.c_void_p), ("w2", ctypes.c_void_p),
                 ("w1_scale", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p)]
+
+
+class Router(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int), ("k", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("score", ctypes.c_int), ("renorm", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class Norm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("d", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("w_dtype", ctypes.c_int), ("gate_kind", ctypes.c_int), ("alpha", ctypes.c_float),
+                ("eps", ctypes.c_float), ("w", ctypes.c_void_p), ("gate", ctypes.c_void_p)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("master", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("p_dtype", ctypes.c_int),
+                ("g_dtype", ctypes.c_int)]
+
+
+class AdamwList(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("tensors", ctypes.c_int),
+                ("state_bits", ctypes.c_int), ("items", ctypes.c_uint32)]
+
+
+class AdamwHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("step", ctypes.c_int), ("seed", ctypes.c_uint32), ("step_dev", ctypes.c_void_p),
+                ("lr_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -104,6 +142,35 @@ def load():
     lib.moe_backward.restype = _I
     lib.moe_backward.argtypes = ([ctypes.POINTER(Layer), _P, _P, _P, _P, _P, _I, _I, _I, _I, _I]
                                  + [_P] * 10 + [_P, _SZ, _I, _P, _P, _P])
+    lib.moe_backward_gates.restype = _I
+    lib.moe_backward_gates.argtypes = ([ctypes.POINTER(Layer)] + [_P] * 5 + [_I] * 5
+                                       + [_P] * 11 + [_P, _SZ, _I, _P, _P, _P])
+    lib.moe_gate_grad.restype = _I
+    lib.moe_gate_grad.argtypes = [_P, _P, _I, _P, _I, _I, _I, _P, _P]
+    R, N = ctypes.POINTER(Router), ctypes.POINTER(Norm)
+    lib.moe_router_workspace_size.restype = _SZ
+    lib.moe_router_workspace_size.argtypes = [R, _I]
+    lib.moe_router_forward.restype = _I
+    lib.moe_router_forward.argtypes = [R, _P, _I, _P, _I] + [_P] * 7 + [_P, _SZ, _P]
+    lib.moe_router_backward.restype = _I
+    lib.moe_router_backward.argtypes = [R, _P, _I, _P, _I] + [_P] * 6 + [_I, _P]
+    lib.moe_norm_workspace_size.restype = _SZ
+    lib.moe_norm_workspace_size.argtypes = [_I, _I]
+    lib.moe_norm_in.restype = _I
+    lib.moe_norm_in.argtypes = [N] + [_P, _I] * 4 + [_P, _P]
+    lib.moe_norm_in_backward.restype = _I
+    lib.moe_norm_in_backward.argtypes = [N] + [_P, _I] * 4 + [_P] + [_P, _I] * 2 + [_P, _P, _P, _SZ, _P]
+    lib.moe_norm_out.restype = _I
+    lib.moe_norm_out.argtypes = [N] + [_P, _I] * 3 + [_P, _P]
+    lib.moe_norm_out_backward.restype = _I
+    lib.moe_norm_out_backward.argtypes = [N] + [_P, _I] * 2 + [_P] + [_P, _I] + [_P, _P, _P, _SZ, _P]
+    lib.moe_adamw_workspace_size.restype = _SZ
+    lib.moe_adamw_workspace_size.argtypes = [_I]
+    lib.moe_adamw_prepare.restype = _I
+    lib.moe_adamw_prepare.argtypes = [ctypes.POINTER(AdamwTensor), _I, _I, ctypes.POINTER(AdamwList),
+                                      _P, _SZ, _P]
+    lib.moe_adamw.restype = _I
+    lib.moe_adamw.argtypes = [ctypes.POINTER(AdamwList), ctypes.POINTER(AdamwHyper), _P]
     lib.moe_event_create.argtypes = [ctypes.POINTER(_P)]
     lib.moe_event_destroy.argtypes = [_P]
     lib.moe_event_record.argtypes = [_P, _P]
@@ -421,7 +488,8 @@ def forward(layer: Layer, x, gates, topk_ids, beta, P, rs, block_worker, y, z_sa
 
 def backward(layer: Layer, x, gates, dy, z_save, topk_ids, beta, P, s, rs, owner, block_worker,
              dx, dw1, dw2, ws, status, events=None, timeline=None, two_phase=False, split=0,
-             fp8_act=False):
+             fp8_act=False, dlogp=None):
+    """moe_backward; with dlogp [T][k] fp32, moe_backward_gates (the gate gradients too)."""
     _require_device(x, gates, dy, z_save, topk_ids, owner, block_worker, dx, dw1, dw2, ws, status,
                     timeline)
     _expect_timeline(timeline)
@@ -440,13 +508,325 @@ def backward(layer: Layer, x, gates, dy, z_save, topk_ids, beta, P, s, rs, owner
     _expect(status, torch.int32, 1, "status")
     wsp, wsn = _aligned(ws)
     ev = None if events is None else (ctypes.c_void_p * len(events))(*events)
-    _check(load().moe_backward(ctypes.byref(layer), _ptr(x), _ptr(gates), _ptr(dy), _ptr(z_save),
-                               _ptr(topk_ids), T, k, beta, P, s, _ptr(rs["counts"]),
-                               _ptr(rs["block_offsets"]), _ptr(rs["row_to_slot"]),
-                               _ptr(rs["slot_to_row"]), _ptr(owner), _ptr(block_worker), _ptr(dx),
-                               _ptr(dw1), _ptr(dw2), _ptr(status), wsp, wsn,
-                               exec_flags(two_phase, split, fp8_act), ev, _ptr(timeline),
-                               _stream()))
+    args = [ctypes.byref(layer), _ptr(x), _ptr(gates), _ptr(dy), _ptr(z_save), _ptr(topk_ids), T, k,
+            beta, P, s, _ptr(rs["counts"]), _ptr(rs["block_offsets"]), _ptr(rs["row_to_slot"]),
+            _ptr(rs["slot_to_row"]), _ptr(owner), _ptr(block_worker), _ptr(dx), _ptr(dw1),
+            _ptr(dw2)]
+    rest = [_ptr(status), wsp, wsn, exec_flags(two_phase, split, fp8_act), ev, _ptr(timeline),
+            _stream()]
+    if dlogp is None:
+        _check(load().moe_backward(*args, *rest))
+    else:
+        _require_device(dlogp)
+        _expect(dlogp, torch.float32, T * k, "dlogp")
+        _check(load().moe_backward_gates(*args, _ptr(dlogp), *rest))
+
+
+# ---- around the layer: router, gate gradients, norms, optimizer ---------------
+
+def _here(*ts):
+    """Every tensor given is on the current device, whose stream the call uses."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise MoeError("all buffers must be tensors on the current device")
+
+
+def _rows(t, T, cols, dtype, name):
+    """Row stride of a [T][cols] matrix whose rows' elements lie side by side."""
+    if t.dtype != dtype:
+        raise MoeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols:
+        raise MoeError(f"{name}: expected {(T, cols)}, got {tuple(t.shape)}")
+    if T == 0 or (T == 1 and (cols <= 1 or t.stride(1) == 1)):
+        return cols
+    ld = t.stride(0)
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise MoeError(f"{name}: strides {tuple(t.stride())} are not those of rows of {cols}")
+    return ld
+
+
+def _vector(t, n, dtype, name):
+    if t.dtype != dtype or t.numel() < n or not t.is_contiguous():
+        raise MoeError(f"{name}: expected {n} contiguous elements of {dtype}, got "
+                       f"{tuple(t.shape)} of {t.dtype}")
+
+
+def _dtype_code(dtype, name):
+    if dtype == torch.float32:
+        return MOE_F32
+    if dtype == torch.bfloat16:
+        return MOE_BF16
+    raise MoeError(f"{name}: unsupported element type {dtype}")
+
+
+def make_router(E, k, dtype=torch.float32, score="softmax", renorm=True, scale=1.0) -> Router:
+    """A top-k router of logits [T][E] of this dtype (moe_router)."""
+    if score not in SCORES:
+        raise MoeError(f"score {score!r}: one of {sorted(SCORES)}")
+    r = Router(E, k, _dtype_code(dtype, "logits"), SCORES[score], int(bool(renorm)), scale)
+    if load().moe_router_workspace_size(ctypes.byref(r), 0) == 0:
+        raise MoeError(f"router of E={E}, k={k}, scale={scale} is not supported")
+    return r
+
+
+def alloc_router(router: Router, T, device):
+    f32, i32 = dict(dtype=torch.float32, device=device), dict(dtype=torch.int32, device=device)
+    return {"topk_ids": torch.empty((T, router.k), **i32), "gates": torch.empty((T, router.k), **f32),
+            "counts": torch.empty(router.E, **i32), "prob_sum": torch.empty(router.E, **f32),
+            "live": torch.empty(1, **i32), "losses": torch.empty(2, **f32)}
+
+
+def router_workspace(router: Router, T, device) -> torch.Tensor:
+    n = int(load().moe_router_workspace_size(ctypes.byref(router), T))
+    if n == 0:
+        raise MoeError("moe_router_workspace_size rejected the sizes")
+    return torch.empty(n + 256, dtype=torch.uint8, device=device)
+
+
+def _router_args(router, logits, mask):
+    if logits.dim() != 2:
+        raise MoeError(f"logits: expected [T][E], got {tuple(logits.shape)}")
+    T = logits.shape[0]
+    dt = torch.float32 if router.dtype == MOE_F32 else torch.bfloat16
+    ld = _rows(logits, T, router.E, dt, "logits")
+    if mask is not None:
+        if mask.dtype not in (torch.uint8, torch.bool):
+            raise MoeError(f"mask: expected uint8 or bool, got {mask.dtype}")
+        _vector(mask, T, mask.dtype, "mask")
+    return T, ld, dt
+
+
+def router_forward(router: Router, logits, out: dict, ws, status, mask=None):
+    """Routes logits [T][E] into out (alloc_router): ids, gates, counts, prob_sum, live, losses."""
+    _here(logits, mask, ws, status, *out.values())
+    T, ld, _ = _router_args(router, logits, mask)
+    _vector(out["topk_ids"], T * router.k, torch.int32, "topk_ids")
+    _vector(out["gates"], T * router.k, torch.float32, "gates")
+    _vector(out["counts"], router.E, torch.int32, "counts")
+    _vector(out["prob_sum"], router.E, torch.float32, "prob_sum")
+    _vector(out["live"], 1, torch.int32, "live")
+    _vector(out["losses"], 2, torch.float32, "losses")
+    _vector(status, 1, torch.int32, "status")
+    _vector(ws, 1, torch.uint8, "ws")
+    wsp, wsn = _aligned(ws)
+    _check(load().moe_router_forward(
+        ctypes.byref(router), _ptr(logits), ld, _ptr(mask), T, _ptr(out["topk_ids"]),
+        _ptr(out["gates"]), _ptr(out["counts"]), _ptr(out["prob_sum"]), _ptr(out["live"]),
+        _ptr(out["losses"]), _ptr(status), wsp, wsn, _stream()))
+    return out
+
+
+def router_backward(router: Router, logits, out: dict, dlogp, dlosses, dlogits, mask=None):
+    """dlogits [T][E] from dlogp [T][k] (log-form gate gradients) and dlosses [2], each nullable;
+    out: router_forward's on the same logits and mask."""
+    _here(logits, mask, dlogp, dlosses, dlogits, out["topk_ids"], out["counts"], out["live"])
+    T, ld, dt = _router_args(router, logits, mask)
+    ld_out = _rows(dlogits, T, router.E, dt, "dlogits")
+    _vector(out["topk_ids"], T * router.k, torch.int32, "topk_ids")
+    _vector(out["counts"], router.E, torch.int32, "counts")
+    _vector(out["live"], 1, torch.int32, "live")
+    if dlogp is not None:
+        _vector(dlogp, T * router.k, torch.float32, "dlogp")
+    if dlosses is not None:
+        _vector(dlosses, 2, torch.float32, "dlosses")
+    _check(load().moe_router_backward(
+        ctypes.byref(router), _ptr(logits), ld, _ptr(mask), T, _ptr(out["topk_ids"]), _ptr(dlogp),
+        _ptr(out["counts"]), _ptr(out["live"]), _ptr(dlosses), _ptr(dlogits), ld_out, _stream()))
+    return dlogits
+
+
+def gate_grad(z, dz, row_to_slot, dlogp):
+    """Log-form gate gradients <dU, U> of routed rows from rows [G, U] and [dG, dU] [slots][2 d_ff]."""
+    _here(z, dz, row_to_slot, dlogp)
+    if z.dim() != 2 or z.shape[1] % 2:
+        raise MoeError(f"z: expected [slots][2 d_ff], got {tuple(z.shape)}")
+    slots, two = z.shape
+    code = _dtype_code(z.dtype, "z")
+    _vector(z, z.numel(), z.dtype, "z")
+    _vector(dz, z.numel(), z.dtype, "dz")
+    rows = row_to_slot.numel()
+    _vector(row_to_slot, rows, torch.int32, "row_to_slot")
+    _vector(dlogp, rows, torch.float32, "dlogp")
+    _check(load().moe_gate_grad(_ptr(z), _ptr(dz), code, _ptr(row_to_slot), rows, slots, two // 2,
+                                _ptr(dlogp), _stream()))
+    return dlogp
+
+
+def norm_workspace(T, d, device) -> torch.Tensor:
+    n = int(load().moe_norm_workspace_size(T, d))
+    if n == 0:
+        raise MoeError("moe_norm_workspace_size rejected the sizes")
+    return torch.empty(n + 256, dtype=torch.uint8, device=device)
+
+
+def _norm_desc(rows, w, gate, alpha, eps, name):
+    """The moe_norm of rows [T][d] of the tensor `rows`, and their row stride."""
+    if rows.dim() != 2:
+        raise MoeError(f"{name}: expected [T][d], got {tuple(rows.shape)}")
+    T, d = rows.shape
+    code = _dtype_code(rows.dtype, name)
+    if w.dtype not in (torch.float32, rows.dtype):
+        raise MoeError(f"w: expected float32 or {rows.dtype}, got {w.dtype}")
+    if tuple(w.shape) != (d,) or not w.is_contiguous():
+        raise MoeError(f"w: expected {d} contiguous elements, got {tuple(w.shape)}")
+    kind = GATE_NONE
+    if gate is not None:
+        if tuple(gate.shape) == (T, 1):
+            kind = GATE_TOKEN
+        elif tuple(gate.shape) == (d,):
+            kind = GATE_FEATURE
+        else:
+            raise MoeError(f"gate: expected {(T, 1)} or {(d,)}, got {tuple(gate.shape)}")
+        _vector(gate, gate.numel(), torch.float32, "gate")
+    N = Norm(T, d, code, _dtype_code(w.dtype, "w"), kind, alpha, eps, w.data_ptr(),
+             None if gate is None else gate.data_ptr())
+    return N, T, d, _rows(rows, T, d, rows.dtype, name)
+
+
+def _opt_rows(t, T, d, dtype, name):
+    return (None, 0) if t is None else (_ptr(t), _rows(t, T, d, dtype, name))
+
+
+def norm_in(x, w, eps, n, rstd, u=None, gate=None, alpha=1.0, r=None):
+    """Before the block: r = x + alpha gate u, n = w r / rms(r); rstd [T] for the backward pass."""
+    _here(x, w, n, rstd, u, gate, r)
+    N, T, d, ldx = _norm_desc(x, w, gate, alpha, eps, "x")
+    _vector(rstd, T, torch.float32, "rstd")
+    _check(load().moe_norm_in(ctypes.byref(N), _ptr(x), ldx, *_opt_rows(u, T, d, x.dtype, "u"),
+                              *_opt_rows(r, T, d, x.dtype, "r"), _ptr(n),
+                              _rows(n, T, d, x.dtype, "n"), _ptr(rstd), _stream()))
+    return n
+
+
+def _norm_grads(T, d, gate, dw, dgate, ws):
+    _vector(dw, d, torch.float32, "dw")
+    if gate is not None and dgate is not None:
+        _vector(dgate, gate.numel(), torch.float32, "dgate")
+    _vector(ws, 1, torch.uint8, "ws")
+    return _aligned(ws)
+
+
+def norm_in_backward(dn, r, w, rstd, dx, dw, ws, dr=None, u=None, gate=None, alpha=1.0, du=None,
+                     dgate=None):
+    """Gradients of norm_in: dx (r's and x's), dw, and with u also du and dgate (shaped like gate)."""
+    _here(dn, r, w, rstd, dx, dw, ws, dr, u, gate, du, dgate)
+    N, T, d, ldr = _norm_desc(r, w, gate, alpha, 1.0, "r")
+    dt = r.dtype
+    _vector(rstd, T, torch.float32, "rstd")
+    wsp, wsn = _norm_grads(T, d, gate, dw, dgate, ws)
+    _check(load().moe_norm_in_backward(
+        ctypes.byref(N), _ptr(dn), _rows(dn, T, d, dt, "dn"), *_opt_rows(dr, T, d, dt, "dr"),
+        _ptr(r), ldr, *_opt_rows(u, T, d, dt, "u"), _ptr(rstd), _ptr(dx),
+        _rows(dx, T, d, dt, "dx"), *_opt_rows(du, T, d, dt, "du"), _ptr(dw), _ptr(dgate), wsp, wsn,
+        _stream()))
+    return dx
+
+
+def norm_out(y, x, w, eps, out, rstd, gate=None, alpha=1.0):
+    """After the block: out = x + alpha gate w y / rms(y); rstd [T] for the backward pass."""
+    _here(y, x, w, out, rstd, gate)
+    N, T, d, ldy = _norm_desc(y, w, gate, alpha, eps, "y")
+    _vector(rstd, T, torch.float32, "rstd")
+    _check(load().moe_norm_out(ctypes.byref(N), _ptr(y), ldy, _ptr(x),
+                               _rows(x, T, d, y.dtype, "x"), _ptr(out),
+                               _rows(out, T, d, y.dtype, "out"), _ptr(rstd), _stream()))
+    return out
+
+
+def norm_out_backward(dout, y, w, rstd, dy, dw, ws, gate=None, alpha=1.0, dgate=None):
+    """Gradients of norm_out: dy, dw and dgate (shaped like gate); x's is dout."""
+    _here(dout, y, w, rstd, dy, dw, ws, gate, dgate)
+    N, T, d, ldy = _norm_desc(y, w, gate, alpha, 1.0, "y")
+    _vector(rstd, T, torch.float32, "rstd")
+    wsp, wsn = _norm_grads(T, d, gate, dw, dgate, ws)
+    _check(load().moe_norm_out_backward(
+        ctypes.byref(N), _ptr(dout), _rows(dout, T, d, y.dtype, "dout"), _ptr(y), ldy, _ptr(rstd),
+        _ptr(dy), _rows(dy, T, d, y.dtype, "dy"), _ptr(dw), _ptr(dgate), wsp, wsn, _stream()))
+    return dy
+
+
+class PreparedAdamw:
+    """A prepared list of tensors (moe_adamw_prepare) and the tensors, which it keeps alive."""
+
+    def __init__(self, c_list, device, keep):
+        self.list, self.device, self.keep = c_list, device, keep
+
+
+def make_adamw(p, g, m, v, m_scale=None, v_scale=None, master=None) -> PreparedAdamw:
+    """Prepares AdamW over lists of contiguous tensors: parameters p, gradients g, states m and v
+    (float32, or uint8 e4m3 codes with m_scale and v_scale, one float32 per 128 elements), and
+    optionally master (a float32 copy, or None, for each bfloat16 parameter)."""
+    count = len(p)
+    lists = {"g": g, "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale, "master": master}
+    for name, ts in lists.items():
+        if ts is not None and len(ts) != count:
+            raise MoeError(f"{name}: expected {count} tensors, got {len(ts)}")
+    bits = 8 if m_scale is not None else 32
+    if (m_scale is None) != (v_scale is None):
+        raise MoeError("m_scale and v_scale go together")
+    state = torch.uint8 if bits == 8 else torch.float32
+    arr = (AdamwTensor * max(count, 1))()
+    keep = []
+    for i in range(count):
+        n = p[i].numel()
+        ts = [p[i], g[i], m[i], v[i]]
+        _vector(p[i], n, p[i].dtype, f"p[{i}]")
+        _vector(g[i], n, g[i].dtype, f"g[{i}]")
+        _vector(m[i], n, state, f"m[{i}]")
+        _vector(v[i], n, state, f"v[{i}]")
+        a = arr[i]
+        if bits == 8:
+            blocks = -(-n // ADAMW_BLOCK)
+            _vector(m_scale[i], blocks, torch.float32, f"m_scale[{i}]")
+            _vector(v_scale[i], blocks, torch.float32, f"v_scale[{i}]")
+            ts += [m_scale[i], v_scale[i]]
+            a.m_scale, a.v_scale = m_scale[i].data_ptr(), v_scale[i].data_ptr()
+        if master is not None and master[i] is not None:
+            _vector(master[i], n, torch.float32, f"master[{i}]")
+            ts.append(master[i])
+            a.master = master[i].data_ptr()
+        _here(*ts)
+        keep += ts
+        a.p, a.g, a.m, a.v, a.n = (p[i].data_ptr(), g[i].data_ptr(), m[i].data_ptr(),
+                                   v[i].data_ptr(), n)
+        a.p_dtype, a.g_dtype = _dtype_code(p[i].dtype, f"p[{i}]"), _dtype_code(g[i].dtype, f"g[{i}]")
+    device = torch.cuda.current_device()
+    size = int(load().moe_adamw_workspace_size(count))
+    if size == 0 and count:
+        raise MoeError("moe_adamw_workspace_size rejected the list")
+    ws = torch.empty(size + 256, dtype=torch.uint8, device="cuda")
+    wsp, wsn = _aligned(ws)
+    out = AdamwList()
+    _check(load().moe_adamw_prepare(arr, count, bits, ctypes.byref(out), wsp, wsn, _stream()))
+    return PreparedAdamw(out, device, keep + [ws])
+
+
+def adamw(prepared: PreparedAdamw, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1,
+          seed=0, grad_scale=None):
+    """One AdamW step on every tensor of the list.  step (from 1 on) is a number or an int32 tensor,
+    lr a number or a float32 tensor, grad_scale nothing or a float32 tensor: tensors are read when
+    the step runs, also in a captured graph."""
+    h = AdamwHyper(0.0, beta1, beta2, eps, weight_decay, 0, seed & 0xFFFFFFFF)
+    if isinstance(step, torch.Tensor):
+        _here(step)
+        _vector(step, 1, torch.int32, "step")
+        h.step_dev = step.data_ptr()
+    else:
+        h.step = step
+    if isinstance(lr, torch.Tensor):
+        _here(lr)
+        _vector(lr, 1, torch.float32, "lr")
+        h.lr_dev = lr.data_ptr()
+    else:
+        h.lr = lr
+    if grad_scale is not None:
+        _here(grad_scale)
+        _vector(grad_scale, 1, torch.float32, "grad_scale")
+        h.grad_scale = grad_scale.data_ptr()
+    if prepared.device != torch.cuda.current_device():
+        raise MoeError("the list was prepared on another device")
+    _check(load().moe_adamw(ctypes.byref(prepared.list), ctypes.byref(h), _stream()))
 
 
 class Events:

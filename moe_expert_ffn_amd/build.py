@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libmoe_ffn.so")
-SOURCES = ["route_plan.hip", "ffn.hip", "api.hip"]
+SOURCES = ["route_plan.hip", "ffn.hip", "router.hip", "norm.hip", "adamw.hip", "api.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",

@@ -2,6 +2,11 @@
 // carving and kernel launches.  No allocation, no host synchronisation.
 #include <hip/hip_runtime.h>
 
+#include <stdlib.h>
+
+#include <algorithm>
+#include <cmath>
+
 #include "internal.h"
 #include "moe_ffn.h"
 
@@ -281,14 +286,13 @@ int moe_forward(const moe_layer* L, const void* x, const float* gates, const int
                         timeline, (hipStream_t)stream);
 }
 
-int moe_backward(const moe_layer* L, const void* x, const float* gates, const void* dy,
-                 const void* z_save, const int32_t* topk_ids, int T, int k, int beta, int P,
+static int backward(const moe_layer* L, const void* x, const float* gates, const void* dy,
+                 const void* z_save, int T, int k, int beta, int P,
                  int s, const int32_t* counts, const int32_t* block_offsets,
                  const int32_t* row_to_slot, const int32_t* slot_to_row, const int32_t* owner,
                  const int32_t* block_worker, void* dx, float* dw1, float* dw2,
-                 int32_t* status_dev, void* ws, size_t ws_bytes, int exec_flags,
+                 float* dlogp, int32_t* status_dev, void* ws, size_t ws_bytes, int exec_flags,
                  void* const* stage_events, uint64_t* timeline, void* stream) {
-  (void)topk_ids;
   const int lc = check_layer(L, true);
   if (!exec_flags_ok(exec_flags)) return MOE_ERR_ARG;
   if (lc != MOE_OK) return lc;
@@ -307,8 +311,246 @@ int moe_backward(const moe_layer* L, const void* x, const float* gates, const vo
   if (!ws_ok(ws, ws_bytes, exec_layout(z, true).total)) return MOE_ERR_WORKSPACE;
   LayerPtrs Lp{L->w1, L->w2, L->w1_scale, L->w2_scale, L->act_dtype, L->w_dtype};
   return launch_backward(z, Lp, x, gates, dy, z_save, counts, block_offsets, row_to_slot,
-                         slot_to_row, owner, block_worker, dx, dw1, dw2, status_dev, (char*)ws,
+                         slot_to_row, owner, block_worker, dx, dw1, dw2, dlogp, status_dev, (char*)ws,
                          exec_flags, stage_events, timeline, (hipStream_t)stream);
+}
+
+int moe_backward(const moe_layer* L, const void* x, const float* gates, const void* dy,
+                 const void* z_save, const int32_t* topk_ids, int T, int k, int beta, int P,
+                 int s, const int32_t* counts, const int32_t* block_offsets,
+                 const int32_t* row_to_slot, const int32_t* slot_to_row, const int32_t* owner,
+                 const int32_t* block_worker, void* dx, float* dw1, float* dw2,
+                 int32_t* status_dev, void* ws, size_t ws_bytes, int exec_flags,
+                 void* const* stage_events, uint64_t* timeline, void* stream) {
+  (void)topk_ids;
+  return backward(L, x, gates, dy, z_save, T, k, beta, P, s, counts, block_offsets, row_to_slot,
+                  slot_to_row, owner, block_worker, dx, dw1, dw2, nullptr, status_dev, ws, ws_bytes,
+                  exec_flags, stage_events, timeline, stream);
+}
+
+int moe_backward_gates(const moe_layer* L, const void* x, const float* gates, const void* dy,
+                       const void* z_save, const int32_t* topk_ids, int T, int k, int beta,
+                       int P, int s, const int32_t* counts, const int32_t* block_offsets,
+                       const int32_t* row_to_slot, const int32_t* slot_to_row,
+                       const int32_t* owner, const int32_t* block_worker, void* dx, float* dw1,
+                       float* dw2, float* dlogp, int32_t* status_dev, void* ws, size_t ws_bytes,
+                       int exec_flags, void* const* stage_events, uint64_t* timeline,
+                       void* stream) {
+  (void)topk_ids;
+  if (T > 0 && !dlogp) return MOE_ERR_ARG;
+  return backward(L, x, gates, dy, z_save, T, k, beta, P, s, counts, block_offsets, row_to_slot,
+                  slot_to_row, owner, block_worker, dx, dw1, dw2, dlogp, status_dev, ws, ws_bytes,
+                  exec_flags, stage_events, timeline, stream);
+}
+
+static bool dtype_ok(int d) { return d == MOE_F32 || d == MOE_BF16; }
+
+static int check_router(const moe_router* R, int ld, int T) {
+  if (!R || R->E < 1 || R->k < 1 || R->k > R->E || T < 0 || ld < R->E || !dtype_ok(R->dtype) ||
+      (R->score != MOE_SCORE_SOFTMAX && R->score != MOE_SCORE_SIGMOID) || !std::isfinite(R->scale))
+    return MOE_ERR_ARG;
+  if (R->E > kMaxExperts || R->k > kRouterMaxK || (long long)T * R->k >= (1ll << 31))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_router_workspace_size(const moe_router* R, int T) {
+  if (!R || check_router(R, R->E, T) != MOE_OK) return 0;
+  return router_ws_bytes(T, R->E);
+}
+
+int moe_router_forward(const moe_router* R, const void* logits, int ld,
+                       const uint8_t* token_mask, int T, int32_t* topk_ids, float* gates,
+                       int32_t* counts, float* prob_sum, int32_t* live, float* losses,
+                       int32_t* status_dev, void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_router(R, ld, T);
+  if (rc != MOE_OK) return rc;
+  if ((T > 0 && (!logits || !topk_ids || !gates)) || !counts || !prob_sum || !live || !losses ||
+      !status_dev)
+    return MOE_ERR_ARG;
+  if (!ws_ok(ws, ws_bytes, router_ws_bytes(T, R->E))) return MOE_ERR_WORKSPACE;
+  return launch_router(*R, logits, ld, token_mask, T, topk_ids, gates, counts, prob_sum, live,
+                       losses, status_dev, ws, (hipStream_t)stream);
+}
+
+int moe_router_backward(const moe_router* R, const void* logits, int ld,
+                        const uint8_t* token_mask, int T, const int32_t* topk_ids,
+                        const float* dlogp, const int32_t* counts, const int32_t* live,
+                        const float* dlosses, void* dlogits, int ld_out, void* stream) {
+  const int rc = check_router(R, ld, T);
+  if (rc != MOE_OK) return rc;
+  if (ld_out < R->E || (T > 0 && (!logits || !topk_ids || !dlogits)) || !counts || !live)
+    return MOE_ERR_ARG;
+  return launch_router_bwd(*R, logits, ld, token_mask, T, topk_ids, dlogp, counts, live, dlosses,
+                           dlogits, ld_out, (hipStream_t)stream);
+}
+
+int moe_gate_grad(const void* z, const void* dz, int dtype, const int32_t* row_to_slot, int rows,
+                  int slots, int d_ff, float* dlogp, void* stream) {
+  if (rows < 0 || slots < 0 || d_ff < 1 || !dtype_ok(dtype)) return MOE_ERR_ARG;
+  if (d_ff % 64) return MOE_ERR_UNSUPPORTED;
+  if (rows > 0 && (!row_to_slot || !dlogp)) return MOE_ERR_ARG;
+  if (slots > 0 && (!z || !dz)) return MOE_ERR_ARG;
+  if (((uintptr_t)z | (uintptr_t)dz) & 15u) return MOE_ERR_ARG;
+  return launch_gate_grad(z, dz, dtype, row_to_slot, rows, slots, d_ff, dlogp,
+                          (hipStream_t)stream);
+}
+
+static int check_norm(const moe_norm* N) {
+  if (!N || N->d < 1 || N->T < 0 || !dtype_ok(N->dtype) || !(N->eps > 0.f) ||
+      !std::isfinite(N->eps) || !std::isfinite(N->alpha) || N->gate_kind < MOE_GATE_NONE ||
+      N->gate_kind > MOE_GATE_FEATURE || !N->w)
+    return MOE_ERR_ARG;
+  if (N->gate_kind == MOE_GATE_NONE
+          ? N->gate != nullptr
+          : !N->gate && (N->T > 0 || N->gate_kind == MOE_GATE_FEATURE))
+    return MOE_ERR_ARG;
+  if (N->d > kNormMaxD || (N->w_dtype != MOE_F32 && N->w_dtype != N->dtype))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t moe_norm_workspace_size(int T, int d) {
+  return T < 0 || d < 1 || d > kNormMaxD ? 0 : norm_ws_bytes(T, d);
+}
+
+int moe_norm_in(const moe_norm* N, const void* x, int ldx, const void* u, int ldu, void* r,
+                int ldr, void* n, int ldn, float* rstd, void* stream) {
+  const int rc = check_norm(N);
+  if (rc != MOE_OK) return rc;
+  if ((N->T > 0 && (!x || !n || !rstd)) || ldx < N->d || ldn < N->d || (u && ldu < N->d) ||
+      (r && ldr < N->d) || (N->T > 0 && !u && N->gate_kind != MOE_GATE_NONE))
+    return MOE_ERR_ARG;
+  return launch_norm(*N, false, {x, ldx}, {u, ldu}, {r, ldr}, {n, ldn}, rstd, (hipStream_t)stream);
+}
+
+int moe_norm_out(const moe_norm* N, const void* y, int ldy, const void* x, int ldx, void* out,
+                 int ldout, float* rstd, void* stream) {
+  const int rc = check_norm(N);
+  if (rc != MOE_OK) return rc;
+  if ((N->T > 0 && (!y || !x || !out || !rstd)) || ldx < N->d || ldy < N->d || ldout < N->d)
+    return MOE_ERR_ARG;
+  return launch_norm(*N, true, {x, ldx}, {y, ldy}, {nullptr, 0}, {out, ldout}, rstd,
+                     (hipStream_t)stream);
+}
+
+int moe_norm_in_backward(const moe_norm* N, const void* dn, int lddn, const void* dr, int lddr,
+                         const void* r, int ldr, const void* u, int ldu, const float* rstd,
+                         void* dx, int lddx, void* du, int lddu, float* dw, float* dgate,
+                         void* ws, size_t ws_bytes, void* stream) {
+  const int rc = check_norm(N);
+  if (rc != MOE_OK) return rc;
+  if ((N->T > 0 && (!dn || !r || !rstd || !dx)) || !dw || lddn < N->d || ldr < N->d ||
+      lddx < N->d || (dr && lddr < N->d) || (u && ldu < N->d) || (du && lddu < N->d) ||
+      (N->T > 0 && !u != !du) || (N->T > 0 && !u && N->gate_kind != MOE_GATE_NONE) ||
+      (N->gate_kind == MOE_GATE_NONE ? dgate != nullptr
+                                     : !dgate && (N->T > 0 || N->gate_kind == MOE_GATE_FEATURE)))
+    return MOE_ERR_ARG;
+  if (!ws_ok(ws, ws_bytes, norm_ws_bytes(N->T, N->d))) return MOE_ERR_WORKSPACE;
+  return launch_norm_bwd(*N, false, {dn, lddn}, {dr, lddr}, {r, ldr}, {u, ldu}, rstd, {dx, lddx},
+                         {du, lddu}, dw, dgate, ws, (hipStream_t)stream);
+}
+
+int moe_norm_out_backward(const moe_norm* N, const void* dout, int lddo, const void* y, int ldy,
+                          const float* rstd, void* dy, int lddy, float* dw, float* dgate, void* ws,
+                          size_t ws_bytes, void* stream) {
+  const int rc = check_norm(N);
+  if (rc != MOE_OK) return rc;
+  if ((N->T > 0 && (!dout || !y || !rstd || !dy)) || !dw || lddo < N->d || ldy < N->d ||
+      lddy < N->d ||
+      (N->gate_kind == MOE_GATE_NONE ? dgate != nullptr
+                                     : !dgate && (N->T > 0 || N->gate_kind == MOE_GATE_FEATURE)))
+    return MOE_ERR_ARG;
+  if (!ws_ok(ws, ws_bytes, norm_ws_bytes(N->T, N->d))) return MOE_ERR_WORKSPACE;
+  return launch_norm_bwd(*N, true, {dout, lddo}, {nullptr, 0}, {y, ldy}, {nullptr, 0}, rstd,
+                         {dy, lddy}, {nullptr, 0}, dw, dgate, ws, (hipStream_t)stream);
+}
+
+size_t moe_adamw_workspace_size(int tensors) {
+  return tensors < 0 || tensors > MOE_ADAMW_MAX_TENSORS ? 0 : adamw_ws_bytes(tensors);
+}
+
+namespace {
+struct Extent { uintptr_t at, end; int written; };
+
+// Every buffer of the list as a range; whether a written one shares memory with
+// another.  `ext` holds 7 * count entries.
+bool extents_apart(const moe_adamw_tensor* t, int count, int bits, Extent* ext) {
+  size_t m = 0;
+  auto put = [&](const void* p, size_t bytes, int written) {
+    if (p && bytes) ext[m++] = {(uintptr_t)p, (uintptr_t)p + bytes, written};
+  };
+  for (int i = 0; i < count; ++i) {
+    const size_t n = (size_t)t[i].n, blocks = (n + MOE_ADAMW_BLOCK - 1) / MOE_ADAMW_BLOCK;
+    put(t[i].p, n * (t[i].p_dtype == MOE_F32 ? 4 : 2), 1);
+    put(t[i].master, n * 4, 1);
+    put(t[i].g, n * (t[i].g_dtype == MOE_F32 ? 4 : 2), 0);
+    put(t[i].m, bits == 8 ? n : n * 4, 1);
+    put(t[i].v, bits == 8 ? n : n * 4, 1);
+    if (bits == 8) {
+      put(t[i].m_scale, blocks * 4, 1);
+      put(t[i].v_scale, blocks * 4, 1);
+    }
+  }
+  std::sort(ext, ext + m, [](const Extent& a, const Extent& b) { return a.at < b.at; });
+  uintptr_t end = 0, end_w = 0;      // furthest end of any, and of a written, earlier buffer
+  for (size_t i = 0; i < m; ++i) {
+    if (ext[i].at < (ext[i].written ? end : end_w)) return false;
+    end = std::max(end, ext[i].end);
+    if (ext[i].written) end_w = std::max(end_w, ext[i].end);
+  }
+  return true;
+}
+}  // namespace
+
+int moe_adamw_prepare(const moe_adamw_tensor* tensors, int count, int state_bits,
+                      moe_adamw_list* out, void* ws, size_t ws_bytes, void* stream) {
+  if (count < 0 || count > MOE_ADAMW_MAX_TENSORS || !out || (count > 0 && !tensors))
+    return MOE_ERR_ARG;
+  if (state_bits != 8 && state_bits != 32) return MOE_ERR_UNSUPPORTED;
+  long long total = 0;
+  for (int i = 0; i < count; ++i) {
+    const moe_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || !dtype_ok(t.p_dtype) || !dtype_ok(t.g_dtype)) return MOE_ERR_ARG;
+    if (t.n == 0) continue;
+    if (t.n > (1ll << 43) || (total += t.n) > (1ll << 43)) return MOE_ERR_UNSUPPORTED;
+    const uintptr_t pb = t.p_dtype == MOE_F32 ? 3 : 1, gb = t.g_dtype == MOE_F32 ? 3 : 1;
+    if (!t.p || !t.g || !t.m || !t.v || ((uintptr_t)t.p & pb) || ((uintptr_t)t.g & gb))
+      return MOE_ERR_ARG;
+    if (t.master && (t.p_dtype != MOE_BF16 || ((uintptr_t)t.master & 3))) return MOE_ERR_ARG;
+    if (state_bits == 8) {
+      if (!t.m_scale || !t.v_scale || (((uintptr_t)t.m_scale | (uintptr_t)t.v_scale) & 3))
+        return MOE_ERR_ARG;
+    } else if (((uintptr_t)t.m | (uintptr_t)t.v) & 3) {
+      return MOE_ERR_ARG;
+    }
+  }
+  if (!ws_ok(ws, ws_bytes, adamw_ws_bytes(count))) return MOE_ERR_WORKSPACE;
+  if (count > 0) {
+    Extent* ext = (Extent*)malloc(sizeof(Extent) * 7 * (size_t)count);
+    if (!ext) return MOE_ERR_HIP;
+    const bool apart = extents_apart(tensors, count, state_bits, ext);
+    free(ext);
+    if (!apart) return MOE_ERR_ARG;
+  }
+  uint32_t items = 0;
+  const int rc = launch_adamw_table(tensors, count, state_bits, &items, ws, (hipStream_t)stream);
+  if (rc != MOE_OK) return rc;
+  out->table = ws;
+  out->tensors = count;
+  out->state_bits = state_bits;
+  out->items = items;
+  return MOE_OK;
+}
+
+int moe_adamw(const moe_adamw_list* list, const moe_adamw_hyper* h, void* stream) {
+  if (!list || !h || list->tensors < 0 || (list->items > 0 && !list->table) ||
+      (list->state_bits != 8 && list->state_bits != 32))
+    return MOE_ERR_ARG;
+  if (!(h->beta1 >= 0 && h->beta1 < 1) || !(h->beta2 >= 0 && h->beta2 < 1) || !(h->eps > 0) ||
+      !std::isfinite(h->eps) || !std::isfinite(h->weight_decay) || (!h->lr_dev && !std::isfinite(h->lr)) || (!h->step_dev && h->step < 1))
+    return MOE_ERR_ARG;
+  return launch_adamw(*list, *h, (hipStream_t)stream);
 }
 
 int moe_event_create(void** ev) {

@@ -273,6 +273,7 @@ struct ExecArgs {
   int tl_phase;           //   this launch's phase row (a two-phase launch: its first phase)
   int32_t* flags;         // two-phase launches: finished first-phase items per (worker, row tile)
   int32_t* status;
+  float* dlogp;           // nullable: gate gradients in log form of the T * k routed rows
 };
 
 enum { PH_FC1 = 0, PH_FC2 = 1, PH_DA = 2, PH_DX = 3, PH_DW = 4 };
@@ -2474,6 +2475,15 @@ int launch_forward(const Sizes& z, const LayerPtrs& Lp, const void* x, const flo
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
+// Gate gradients from the saved [G, U] and dZ's rows, which bufA holds from dA's
+// epilogue until (with e4m3 weights) they are requantized for the weight gradients.
+static void gate_grads(const Sizes& z, const ExecArgs& a, int dtype, const int32_t* row_to_slot,
+                       hipStream_t st) {
+  if (a.dlogp)
+    (void)launch_gate_grad(a.z_save, a.bufA, dtype, row_to_slot, z.T * z.k, (int)z.max_slots,
+                           z.dff, a.dlogp, st);
+}
+
 // With e4m3 weights (FP8): D = p dy per slot is requantized along the tokens
 // and widened back to bf16 (dhat) before dA; dZ is requantized in place in
 // bufA once dX has used it; the weight gradients then read both as bf16.
@@ -2509,6 +2519,7 @@ static void run_backward_stream(const Sizes& z, ExecArgs& a, const int32_t* row_
     rec(ev, 2, st);
   }
   rec(ev, 3, st);
+  gate_grads(z, a, MOE_BF16, row_to_slot, st);
   if (z.T > 0)
     hipLaunchKernelGGL(k_combine<uint16_t>, combine_grid<uint16_t>(z.T, z.d), dim3(256), 0, st,
                        (const uint16_t*)a.bufO, row_to_slot, z.T, z.k, z.d, (uint16_t*)dx);
@@ -2543,6 +2554,7 @@ static void run_backward(const Sizes& z, ExecArgs& a, const int32_t* row_to_slot
   rec(ev, 2, st);
   hipLaunchKernelGGL((k_bwd_dx<T, C, FP8>), dim3(gx), dim3(C::NT), lds, st, a);
   rec(ev, 3, st);
+  gate_grads(z, a, sizeof(T) == 4 ? MOE_F32 : MOE_BF16, row_to_slot, st);
   if (z.T > 0)
     hipLaunchKernelGGL(k_combine<T>, combine_grid<T>(z.T, z.d), dim3(256), 0, st,
                        (const T*)a.bufO, row_to_slot, z.T, z.k, z.d, (T*)dx);
@@ -2559,7 +2571,7 @@ int launch_backward(const Sizes& z, const LayerPtrs& Lp, const void* x, const fl
                     const int32_t* boff, const int32_t* row_to_slot,
                     const int32_t* slot_to_row, const int32_t* owner,
                     const int32_t* block_worker, void* dx, float* dw1, float* dw2,
-                    int32_t* status, char* ws, int exec_flags, void* const* ev,
+                    float* dlogp, int32_t* status, char* ws, int exec_flags, void* const* ev,
                     uint64_t* timeline, hipStream_t st) {
   bool split = true;
   const int n1split = exec_split(exec_flags, z.P, &split);
@@ -2577,6 +2589,7 @@ int launch_backward(const Sizes& z, const LayerPtrs& Lp, const void* x, const fl
   a.x = x; a.gates = gates; a.slot_to_row = slot_to_row; a.row_to_slot = row_to_slot;
   a.z_save = const_cast<void*>(z_save);
   a.dy = dy; a.dw1 = dw1; a.dw2 = dw2; a.boff = boff;
+  a.dlogp = dlogp;
   a.timeline = timeline;
   a.status = status;
   if (Lp.act_dtype == MOE_F32) run_backward<float, SmallCfg>(z, a, row_to_slot, dx, dw1, dw2, ev, st);

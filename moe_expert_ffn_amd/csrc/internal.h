@@ -77,6 +77,32 @@ struct LayerPtrs {
   int act_dtype, w_dtype;
 };
 
+constexpr int kRouterMaxK = 32;
+size_t router_ws_bytes(int T, int E);
+int launch_router(const moe_router& R, const void* logits, int ld, const uint8_t* mask, int T,
+                  int32_t* ids, float* gates, int32_t* counts, float* psum, int32_t* live,
+                  float* losses, int32_t* status, void* ws, hipStream_t st);
+int launch_router_bwd(const moe_router& R, const void* logits, int ld, const uint8_t* mask, int T,
+                      const int32_t* ids, const float* dlogp, const int32_t* counts,
+                      const int32_t* live, const float* dlosses, void* dlogits, int ld_out,
+                      hipStream_t st);
+int launch_gate_grad(const void* z, const void* dz, int dtype, const int32_t* row_to_slot,
+                     int rows, int slots, int dff, float* dlogp, hipStream_t st);
+
+constexpr int kNormMaxD = 16384;
+struct NormRows { const void* p; int ld; };
+size_t norm_ws_bytes(int T, int d);
+int launch_norm(const moe_norm& N, bool out, NormRows x, NormRows u, NormRows r, NormRows n,
+                float* rstd, hipStream_t st);
+int launch_norm_bwd(const moe_norm& N, bool out, NormRows dn, NormRows dr, NormRows r, NormRows u,
+                    const float* rstd, NormRows dx, NormRows du, float* dw, float* dgate, void* ws,
+                    hipStream_t st);
+
+size_t adamw_ws_bytes(int tensors);
+int launch_adamw_table(const moe_adamw_tensor* t, int count, int bits, uint32_t* items, void* ws,
+                       hipStream_t st);
+int launch_adamw(const moe_adamw_list& l, const moe_adamw_hyper& h, hipStream_t st);
+
 int launch_forward(const Sizes& z, const LayerPtrs& L, const void* x, const float* gates,
                    const int32_t* counts, const int32_t* boff, const int32_t* row_to_slot,
                    const int32_t* slot_to_row, const int32_t* block_worker, void* y,
@@ -88,7 +114,7 @@ int launch_backward(const Sizes& z, const LayerPtrs& L, const void* x, const flo
                     const int32_t* boff, const int32_t* row_to_slot,
                     const int32_t* slot_to_row, const int32_t* owner,
                     const int32_t* block_worker, void* dx, float* dw1, float* dw2,
-                    int32_t* status, char* ws, int exec_flags, void* const* ev,
+                    float* dlogp, int32_t* status, char* ws, int exec_flags, void* const* ev,
                     uint64_t* timeline, hipStream_t st);
 
 int gemm_wg_per_cu();

@@ -1,0 +1,397 @@
+// Root-mean-square norms before and after a block, with its gate and residual
+// scale, and their gradients.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "lanes.h"
+
+namespace moe {
+
+struct NormArgs {
+  const void* x;       // before the block: the stream; after: the stream.  backward: r or y
+  const void* u;       // before: what the stream takes up (nullable); after: y
+  const void* w;
+  const float* gate;
+  const void* go;      // backward: the gradient of the output
+  const void* gr;      // backward: what reaches r from elsewhere (nullable)
+  void* r;             // forward: the updated stream (nullable).  backward: du
+  void* n;             // forward: the output.  backward: dx or dy
+  float* rstd;
+  float* dgate;
+  float* part_w;       // [workgroups][d] sums of dw, or dw itself with one workgroup
+  float* part_g;
+  size_t ldx, ldu, ldgo, ldgr, ldr, ldn;
+  int T, d, w32, kind;
+  float alpha, eps, inv_d;
+};
+
+template <typename T, int VE> MOE_DEV void load_f(const T* p, float* v) {
+  T raw[VE];
+  load_n<T, VE, (VE > 1)>(p, raw);
+#pragma unroll
+  for (int i = 0; i < VE; ++i) v[i] = elem_f(raw[i]);
+}
+template <typename T, int VE> MOE_DEV void store_f(T* p, const float* v) {
+  T raw[VE];
+#pragma unroll
+  for (int i = 0; i < VE; ++i) elem_set(raw[i], v[i]);
+  store_n<T, VE, (VE > 1)>(p, raw);
+}
+template <typename T, int VE> MOE_DEV void load_w(const NormArgs& a, int c, float* v) {
+  if (a.w32) load_f<float, VE>((const float*)a.w + c, v);
+  else load_f<T, VE>((const T*)a.w + c, v);
+}
+// alpha g for the columns from c on: g_row holds alpha (times the token's gate)
+template <int VE> MOE_DEV void load_g(const NormArgs& a, int c, float g_row, float* v) {
+  if (a.kind == MOE_GATE_FEATURE) {
+    load_f<float, VE>(a.gate + c, v);
+#pragma unroll
+    for (int i = 0; i < VE; ++i) v[i] *= g_row;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) v[i] = g_row;
+  }
+}
+
+// Sum over the NT threads of a row.  More than a wave: through LDS, `red` two
+// buffers used in turn, so one barrier per sum is enough.
+template <int NT> MOE_DEV float row_sum(float s, float (*red)[16], int turn) {
+  s = group_all<64>(s, OpAdd());
+  if constexpr (NT > 64) {
+    float* r = red[turn & 1];
+    if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NT / 64; ++i) s += r[i];
+  }
+  return s;
+}
+
+// NT threads take a row, KC pieces of VE elements each, which stay in
+// registers between the sum and the output: every row is read once.
+template <typename T, int VE, int NT, int KC, bool OUT>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(NormArgs a) {
+  constexpr int RPW = NT < 256 ? 256 / NT : 1;
+  __shared__ float red[2][16];
+  const int li = threadIdx.x % NT;
+  const size_t t = (size_t)blockIdx.x * RPW + threadIdx.x / NT;
+  if (t >= (size_t)a.T) return;                          // a whole wave
+  const float g_row = a.alpha * (a.kind == MOE_GATE_TOKEN ? a.gate[t] : 1.f);
+  const T* x = (const T*)a.x + t * a.ldx;
+  const T* u = (const T*)a.u + t * a.ldu;
+  float v[KC][VE], xs[OUT ? KC : 1][VE];
+  float s = 0.f;
+#pragma unroll
+  for (int q = 0; q < KC; ++q) {
+    const int c = (li + q * NT) * VE;
+#pragma unroll
+    for (int i = 0; i < VE; ++i) v[q][i] = 0.f;
+    if (c >= a.d) continue;
+    if constexpr (OUT) {
+      load_f<T, VE>(u + c, v[q]);
+      load_f<T, VE>(x + c, xs[q]);
+    } else {
+      load_f<T, VE>(x + c, v[q]);
+      if (a.u) {
+        float uu[VE], g[VE];
+        load_f<T, VE>(u + c, uu);
+        load_g<VE>(a, c, g_row, g);
+#pragma unroll
+        for (int i = 0; i < VE; ++i) v[q][i] += g[i] * uu[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VE; ++i) s += v[q][i] * v[q][i];
+  }
+  s = row_sum<NT>(s, red, 0);
+  const float rstd = 1.f / sqrtf(s * a.inv_d + a.eps);
+  if (li == 0) a.rstd[t] = rstd;
+#pragma unroll
+  for (int q = 0; q < KC; ++q) {
+    const int c = (li + q * NT) * VE;
+    if (c >= a.d) continue;
+    float w[VE], o[VE];
+    load_w<T, VE>(a, c, w);
+    if constexpr (OUT) {
+      float g[VE];
+      load_g<VE>(a, c, g_row, g);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) o[i] = xs[q][i] + g[i] * (v[q][i] * rstd * w[i]);
+    } else {
+      if (a.r) store_f<T, VE>((T*)a.r + t * a.ldr + c, v[q]);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) o[i] = v[q][i] * rstd * w[i];
+    }
+    store_f<T, VE>((T*)a.n + t * a.ldn + c, o);
+  }
+}
+
+// Backward: threads keep their columns' sums over the rows of a workgroup in
+// registers (dw, and FEAT: the gate's); the workgroups' sums are joined by
+// k_norm_cols, so the order of every sum is fixed by the grid.
+template <typename T, int VE, int NT, int KC, bool OUT, bool FEAT>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_bwd(NormArgs a) {
+  constexpr int RPW = NT < 256 ? 256 / NT : 1;
+  __shared__ float red[2][16];
+  __shared__ float join[RPW > 1 ? RPW : 1][RPW > 1 ? NT * VE : 1];
+  const int li = threadIdx.x % NT, rg = threadIdx.x / NT;
+  float dw[KC][VE], dg[FEAT ? KC : 1][VE];
+#pragma unroll
+  for (int q = 0; q < KC; ++q)
+#pragma unroll
+    for (int i = 0; i < VE; ++i) {
+      dw[q][i] = 0.f;
+      if constexpr (FEAT) dg[q][i] = 0.f;
+    }
+  int turn = 0;
+  const size_t step = (size_t)gridDim.x * RPW;
+  for (size_t t = (size_t)blockIdx.x * RPW + rg; t < (size_t)a.T; t += step) {
+    const float g_row = a.alpha * (a.kind == MOE_GATE_TOKEN ? a.gate[t] : 1.f);
+    const float rstd = a.rstd[t];
+    const T* x = (const T*)a.x + t * a.ldx;
+    const T* go = (const T*)a.go + t * a.ldgo;
+    float xh[KC][VE], p[KC][VE];       // x / rms, and the gradient of that
+    float s = 0.f;
+#pragma unroll
+    for (int q = 0; q < KC; ++q) {
+      const int c = (li + q * NT) * VE;
+      if (c >= a.d) continue;
+      float o[VE], w[VE];
+      load_f<T, VE>(x + c, xh[q]);
+      load_f<T, VE>(go + c, o);
+      load_w<T, VE>(a, c, w);
+      float g[VE];
+      if constexpr (OUT) load_g<VE>(a, c, g_row, g);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) {
+        xh[q][i] *= rstd;
+        float dv = o[i];
+        if constexpr (OUT) {
+          dv *= g[i];
+          if constexpr (FEAT) dg[q][i] += o[i] * (w[i] * xh[q][i]);
+        }
+        dw[q][i] += dv * xh[q][i];
+        p[q][i] = dv * w[i];
+        // after the block, a token's gate: the sum without it, which is also its gradient
+        s += (OUT && !FEAT ? o[i] * w[i] : p[q][i]) * xh[q][i];
+      }
+    }
+    s = row_sum<NT>(s, red, turn++);
+    if constexpr (OUT && !FEAT) {
+      if (a.kind == MOE_GATE_TOKEN && li == 0) a.dgate[t] = a.alpha * s;
+      s *= g_row;
+    }
+    const float mean = s * a.inv_d;
+    const T* gr = (const T*)a.gr + t * a.ldgr;
+    const T* u = (const T*)a.u + t * a.ldu;
+    float b = 0.f;
+#pragma unroll
+    for (int q = 0; q < KC; ++q) {
+      const int c = (li + q * NT) * VE;
+      if (c >= a.d) continue;
+      float dx[VE];
+#pragma unroll
+      for (int i = 0; i < VE; ++i) dx[i] = rstd * (p[q][i] - xh[q][i] * mean);
+      if constexpr (!OUT) {
+        if (a.gr) {
+          float more[VE];
+          load_f<T, VE>(gr + c, more);
+#pragma unroll
+          for (int i = 0; i < VE; ++i) dx[i] += more[i];
+        }
+        if (a.u) {
+          float uu[VE], g[VE], du[VE];
+          load_f<T, VE>(u + c, uu);
+          load_g<VE>(a, c, g_row, g);
+#pragma unroll
+          for (int i = 0; i < VE; ++i) {
+            du[i] = g[i] * dx[i];
+            if constexpr (FEAT) dg[q][i] += uu[i] * dx[i];
+            else b += uu[i] * dx[i];
+          }
+          store_f<T, VE>((T*)a.r + t * a.ldr + c, du);
+        }
+      }
+      store_f<T, VE>((T*)a.n + t * a.ldn + c, dx);
+    }
+    if constexpr (!OUT && !FEAT)
+      if (a.kind == MOE_GATE_TOKEN) {
+        b = row_sum<NT>(b, red, turn++);
+        if (li == 0) a.dgate[t] = a.alpha * b;
+      }
+  }
+  const bool alone = gridDim.x == 1;
+#pragma unroll
+  for (int q = 0; q < KC; ++q) {
+    const int c = (li + q * NT) * VE;
+#pragma unroll
+    for (int h = 0; h < (FEAT ? 2 : 1); ++h) {
+      float sum[VE];
+#pragma unroll
+      for (int i = 0; i < VE; ++i) sum[i] = h ? (FEAT ? dg[FEAT ? q : 0][i] : 0.f) : dw[q][i];
+      if constexpr (RPW > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VE; ++i) join[rg][li * VE + i] = sum[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          sum[i] = 0.f;
+#pragma unroll
+          for (int o = 0; o < RPW; ++o) sum[i] += join[o][li * VE + i];
+        }
+        if (rg) continue;
+      }
+      if (c >= a.d) continue;
+      float* to = (h ? a.part_g : a.part_w) + (size_t)blockIdx.x * a.d + c;
+#pragma unroll
+      for (int i = 0; i < VE; ++i) to[i] = h && alone ? a.alpha * sum[i] : sum[i];
+    }
+  }
+}
+
+// dw (and dgate) from the workgroups' sums: 64 columns a workgroup, 16 strands
+// of partial rows joined through LDS.
+__global__ __launch_bounds__(1024) void k_norm_cols(const float* __restrict__ part_w,
+                                                    const float* __restrict__ part_g, int parts,
+                                                    int d, float alpha, float* __restrict__ dw,
+                                                    float* __restrict__ dgate) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, strand = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  const float* part = blockIdx.y ? part_g : part_w;
+  float s = 0.f;
+  if (c < d)
+    for (int b = strand; b < parts; b += 16) s += part[(size_t)b * d + c];
+  red[strand][lane] = s;
+  __syncthreads();
+  if (strand == 0 && c < d) {
+    for (int i = 1; i < 16; ++i) s += red[i][lane];
+    if (blockIdx.y) dgate[c] = alpha * s;
+    else dw[c] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// The backward's workgroups: what every d can use; the partial sums are 2 * d
+// floats for each.
+constexpr int kNormMaxWG = 256;
+static int norm_grid(int T, int rpw) {
+  return std::max(1, std::min((int)(((long long)T + rpw - 1) / rpw), kNormMaxWG));
+}
+
+size_t norm_ws_bytes(int T, int d) {
+  return 2 * align_up((size_t)norm_grid(T, 1) * d * sizeof(float));
+}
+
+static bool aligned16(const void* p, size_t ld_bytes) {
+  return !p || (((uintptr_t)p & 15u) == 0 && ld_bytes % 16 == 0);
+}
+
+// F::go<T, VE, NT, KC>(args...): by how many pieces of VE elements a row has
+template <class F, typename T, int VE, typename... A> static void norm_shape(int d, A&&... args) {
+  const int pieces = (d + VE - 1) / VE;
+  if (pieces <= 64) F::template go<T, VE, 64, 1>(args...);
+  else if (pieces <= 128) F::template go<T, VE, 64, 2>(args...);
+  else if (pieces <= 256) F::template go<T, VE, 64, 4>(args...);
+  else if (pieces <= 512) F::template go<T, VE, 256, 2>(args...);
+  else if (pieces <= 1024) F::template go<T, VE, 256, 4>(args...);
+  else if (pieces <= 2048) F::template go<T, VE, 1024, 2>(args...);
+  else if constexpr (VE < 8) {                           // 8 elements: d ends at 2048 pieces
+    if (pieces <= 4096) F::template go<T, VE, 1024, 4>(args...);
+    else if constexpr (VE == 1) F::template go<T, VE, 1024, 16>(args...);
+  }
+}
+template <class F, typename... A> static void norm_kind(int dtype, bool vec, int d, A&&... args) {
+  if (dtype == MOE_F32) {
+    if (vec) norm_shape<F, float, 4>(d, args...);
+    else norm_shape<F, float, 1>(d, args...);
+  } else {
+    if (vec) norm_shape<F, uint16_t, 8>(d, args...);
+    else norm_shape<F, uint16_t, 1>(d, args...);
+  }
+}
+
+struct NormFwd {
+  template <typename T, int VE, int NT, int KC>
+  static void go(const NormArgs& a, bool out, hipStream_t st) {
+    constexpr int RPW = NT < 256 ? 256 / NT : 1, WG = NT < 256 ? 256 : NT;
+    const dim3 grid((unsigned)(((size_t)a.T + RPW - 1) / RPW));
+    if (out) hipLaunchKernelGGL((k_norm<T, VE, NT, KC, true>), grid, dim3(WG), 0, st, a);
+    else hipLaunchKernelGGL((k_norm<T, VE, NT, KC, false>), grid, dim3(WG), 0, st, a);
+  }
+};
+
+struct NormBwd {
+  template <typename T, int VE, int NT, int KC>
+  static void go(NormArgs& a, bool out, float* dw, float* dgate, hipStream_t st) {
+    constexpr int RPW = NT < 256 ? 256 / NT : 1, WG = NT < 256 ? 256 : NT;
+    const int parts = norm_grid(a.T, RPW);
+    const bool feat = a.kind == MOE_GATE_FEATURE;
+    float* pw = a.part_w;
+    float* pg = a.part_g;
+    if (parts == 1) {
+      a.part_w = dw;
+      a.part_g = dgate;
+    }
+    const dim3 grid(parts), wg(WG);
+    if (out && feat) hipLaunchKernelGGL((k_norm_bwd<T, VE, NT, KC, true, true>), grid, wg, 0, st, a);
+    else if (out) hipLaunchKernelGGL((k_norm_bwd<T, VE, NT, KC, true, false>), grid, wg, 0, st, a);
+    else if (feat) hipLaunchKernelGGL((k_norm_bwd<T, VE, NT, KC, false, true>), grid, wg, 0, st, a);
+    else hipLaunchKernelGGL((k_norm_bwd<T, VE, NT, KC, false, false>), grid, wg, 0, st, a);
+    if (parts > 1)
+      hipLaunchKernelGGL(k_norm_cols, dim3((a.d + 63) / 64, feat ? 2 : 1), dim3(1024), 0, st, pw,
+                         pg, parts, a.d, a.alpha, dw, dgate);
+  }
+};
+
+static NormArgs norm_args(const moe_norm& N) {
+  NormArgs a{};
+  a.w = N.w; a.gate = N.gate; a.T = N.T; a.d = N.d; a.kind = N.gate_kind;
+  a.w32 = N.w_dtype == MOE_F32 ? 1 : 0;
+  a.alpha = N.alpha; a.eps = N.eps; a.inv_d = 1.f / (float)N.d;
+  return a;
+}
+
+// 16-byte pieces: every row and vector starts on one, and d is whole pieces
+static bool norm_vec(const moe_norm& N, std::initializer_list<NormRows> rows) {
+  const size_t eb = N.dtype == MOE_F32 ? 4 : 2;
+  bool ok = (N.d * eb) % 16 == 0 && aligned16(N.w, 0) &&
+            (N.gate_kind != MOE_GATE_FEATURE || aligned16(N.gate, 0));
+  for (const NormRows& r : rows) ok = ok && aligned16(r.p, r.p ? (size_t)r.ld * eb : 0);
+  return ok;
+}
+
+int launch_norm(const moe_norm& N, bool out, NormRows x, NormRows u, NormRows r, NormRows n,
+                float* rstd, hipStream_t st) {
+  if (N.T == 0) return MOE_OK;
+  NormArgs a = norm_args(N);
+  a.x = x.p; a.ldx = (size_t)x.ld; a.u = u.p; a.ldu = (size_t)u.ld;
+  a.r = const_cast<void*>(r.p); a.ldr = (size_t)r.ld;
+  a.n = const_cast<void*>(n.p); a.ldn = (size_t)n.ld;
+  a.rstd = rstd;
+  norm_kind<NormFwd>(N.dtype, norm_vec(N, {x, u, r, n}), N.d, a, out, st);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int launch_norm_bwd(const moe_norm& N, bool out, NormRows dn, NormRows dr, NormRows r, NormRows u,
+                    const float* rstd, NormRows dx, NormRows du, float* dw, float* dgate, void* ws,
+                    hipStream_t st) {
+  NormArgs a = norm_args(N);
+  a.go = dn.p; a.ldgo = (size_t)dn.ld; a.gr = dr.p; a.ldgr = (size_t)dr.ld;
+  a.x = r.p; a.ldx = (size_t)r.ld; a.u = u.p; a.ldu = (size_t)u.ld;
+  a.n = const_cast<void*>(dx.p); a.ldn = (size_t)dx.ld;
+  a.r = const_cast<void*>(du.p); a.ldr = (size_t)du.ld;
+  a.rstd = const_cast<float*>(rstd);
+  a.dgate = dgate;
+  a.part_w = (float*)ws;
+  a.part_g = (float*)((char*)ws + norm_ws_bytes(N.T, N.d) / 2);
+  norm_kind<NormBwd>(N.dtype, norm_vec(N, {dn, dr, r, u, dx, du}), N.d, a, out, dw, dgate, st);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+}  // namespace moe

@@ -1,0 +1,75 @@
+"""Oracle: AdamW with fp32 states or e4m3 states -- TEST INFRASTRUCTURE ONLY.
+
+    m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+    p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+in fp64.  8-bit states hold m and sqrt(v) in blocks of 128 as e4m3 codes times
+a scale, the block's largest finite magnitude over 448, rounded up with the
+probability of the part cut off; the random words are a hash of the seed, the
+step, the tensor's place in its list and the element's index.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+BLOCK = 128
+GOLD, ROOT2, ROOT3 = 0x9E3779B9, 0x6A09E667, 0xBB67AE85
+_M = 0xFFFFFFFF
+
+
+def _mix(x):
+    x = x ^ (x >> 16)
+    x = (x * ROOT2) & _M
+    return x ^ (x >> 15)
+
+
+def words(seed, step, tensor, n):
+    key = _mix((seed + step * GOLD + tensor * ROOT3) & _M)
+    i = np.arange(n, dtype=np.uint64)
+    x = (i * np.uint64(GOLD) + np.uint64(key)) & np.uint64(_M)
+    x = x ^ (x >> np.uint64(16))
+    x = (x * np.uint64(ROOT2)) & np.uint64(_M)
+    return (x ^ (x >> np.uint64(15))).astype(np.int64)
+
+
+def step(p, g, m, v, t, lr, b1, b2, eps, wd):
+    m = b1 * m + (1 - b1) * g
+    v = b2 * v + (1 - b2) * g * g
+    with np.errstate(invalid="ignore"):
+        p = p * (1 - lr * wd) - lr * (m / (1 - b1 ** t)) / (np.sqrt(v / (1 - b2 ** t)) + eps)
+    return p, m, v
+
+
+def decode(codes, scales):
+    c = np.asarray(codes).astype(np.int64)
+    e, f = (c >> 3) & 15, c & 7
+    mag = np.where(e > 0, np.ldexp(1.0 + f / 8.0, e - 7), f / 512.0)
+    mag = np.where((c & 127) == 127, np.nan, mag)
+    return np.where(c & 128, -mag, mag) * np.repeat(np.asarray(scales, dtype=np.float64), BLOCK)[:c.size]
+
+
+def block_tops(x):
+    n = x.size
+    a = np.where(np.isfinite(x), np.abs(x), 0.0)
+    a = np.concatenate([a, np.zeros(-n % BLOCK)]).reshape(-1, BLOCK).max(1)
+    return np.where(a < 2.0 ** -100, 0.0, a)
+
+
+def encode(x, u16):
+    """(codes, scales, distance): distance of the sum that is cut to the next whole number, in code
+    steps -- where it is within the arithmetic's error, the neighbouring code is right as well."""
+    top = block_tops(x)
+    per = np.repeat(top, BLOCK)[:x.size]
+    fin = np.isfinite(x)
+    y = np.where(per > 0, np.abs(np.where(fin, x, 0.0)) * 448 / np.where(per > 0, per, 1.0), 0.0)
+    ex = np.clip(np.floor(np.log2(np.maximum(y, 2.0 ** -20))), -6, 8).astype(np.int64)
+    s = np.ldexp(y, 3 - ex) + (u16 + 0.5) / 65536
+    code = np.minimum((ex + 6) * 8 + np.floor(s).astype(np.int64), 126)
+    code = np.where(fin, code, 127) | np.where(x < 0, 128, 0)
+    return code.astype(np.uint8), top / 448, np.abs(s - np.round(s))
+
+
+def random_bf16(p, word):
+    """fp32 values rounded to bf16 at random by the high half of word * ROOT3."""
+    b = np.asarray(p, dtype=np.float32).view(np.uint32).astype(np.int64)
+    up = ((b + (((word * ROOT3) & _M) >> 16)) & 0xFFFF0000).astype(np.uint32).view(np.float32)
+    return np.where(np.isfinite(p), up, p)
