@@ -524,12 +524,30 @@ def backward(layer: Layer, x, gates, dy, z_save, topk_ids, beta, P, s, rs, owner
 
 # ---- around the layer: router, gate gradients, norms, optimizer ---------------
 
-def _here(*ts):
-    """Every tensor given is on the current device, whose stream the call uses."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
-    for t in ts:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise MoeError("all buffers must be tensors on the current device")
+# These calls take a few microseconds on the GPU, so their checks are kept cheap: device and
+# stream come from torch's own raw queries, and pointers travel as plain numbers.
+
+def _here(first, *rest):
+    """Every tensor given is on the current device; that device's current stream."""
+    dev = first.get_device()                    # -1: not on a GPU
+    for t in rest:
+        if t is not None and t.get_device() != dev:
+            dev = -1
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise MoeError("all buffers must be tensors on the current device")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _ws_at(ws):
+    if ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise MoeError("ws: expected contiguous uint8")
+    p = ws.data_ptr()
+    off = -p % 256
+    return p + off, max(ws.numel() - off, 0)
 
 
 def _rows(t, T, cols, dtype, name):
@@ -599,7 +617,7 @@ def _router_args(router, logits, mask):
 
 def router_forward(router: Router, logits, out: dict, ws, status, mask=None):
     """Routes logits [T][E] into out (alloc_router): ids, gates, counts, prob_sum, live, losses."""
-    _here(logits, mask, ws, status, *out.values())
+    st = _here(logits, mask, ws, status, *out.values())
     T, ld, _ = _router_args(router, logits, mask)
     _vector(out["topk_ids"], T * router.k, torch.int32, "topk_ids")
     _vector(out["gates"], T * router.k, torch.float32, "gates")
@@ -608,19 +626,18 @@ def router_forward(router: Router, logits, out: dict, ws, status, mask=None):
     _vector(out["live"], 1, torch.int32, "live")
     _vector(out["losses"], 2, torch.float32, "losses")
     _vector(status, 1, torch.int32, "status")
-    _vector(ws, 1, torch.uint8, "ws")
-    wsp, wsn = _aligned(ws)
+    wsp, wsn = _ws_at(ws)
     _check(load().moe_router_forward(
-        ctypes.byref(router), _ptr(logits), ld, _ptr(mask), T, _ptr(out["topk_ids"]),
-        _ptr(out["gates"]), _ptr(out["counts"]), _ptr(out["prob_sum"]), _ptr(out["live"]),
-        _ptr(out["losses"]), _ptr(status), wsp, wsn, _stream()))
+        ctypes.byref(router), _at(logits), ld, _at(mask), T, _at(out["topk_ids"]),
+        _at(out["gates"]), _at(out["counts"]), _at(out["prob_sum"]), _at(out["live"]),
+        _at(out["losses"]), _at(status), wsp, wsn, st))
     return out
 
 
 def router_backward(router: Router, logits, out: dict, dlogp, dlosses, dlogits, mask=None):
     """dlogits [T][E] from dlogp [T][k] (log-form gate gradients) and dlosses [2], each nullable;
     out: router_forward's on the same logits and mask."""
-    _here(logits, mask, dlogp, dlosses, dlogits, out["topk_ids"], out["counts"], out["live"])
+    st = _here(logits, mask, dlogp, dlosses, dlogits, out["topk_ids"], out["counts"], out["live"])
     T, ld, dt = _router_args(router, logits, mask)
     ld_out = _rows(dlogits, T, router.E, dt, "dlogits")
     _vector(out["topk_ids"], T * router.k, torch.int32, "topk_ids")
@@ -631,14 +648,14 @@ def router_backward(router: Router, logits, out: dict, dlogp, dlosses, dlogits, 
     if dlosses is not None:
         _vector(dlosses, 2, torch.float32, "dlosses")
     _check(load().moe_router_backward(
-        ctypes.byref(router), _ptr(logits), ld, _ptr(mask), T, _ptr(out["topk_ids"]), _ptr(dlogp),
-        _ptr(out["counts"]), _ptr(out["live"]), _ptr(dlosses), _ptr(dlogits), ld_out, _stream()))
+        ctypes.byref(router), _at(logits), ld, _at(mask), T, _at(out["topk_ids"]), _at(dlogp),
+        _at(out["counts"]), _at(out["live"]), _at(dlosses), _at(dlogits), ld_out, st))
     return dlogits
 
 
 def gate_grad(z, dz, row_to_slot, dlogp):
     """Log-form gate gradients <dU, U> of routed rows from rows [G, U] and [dG, dU] [slots][2 d_ff]."""
-    _here(z, dz, row_to_slot, dlogp)
+    st = _here(z, dz, row_to_slot, dlogp)
     if z.dim() != 2 or z.shape[1] % 2:
         raise MoeError(f"z: expected [slots][2 d_ff], got {tuple(z.shape)}")
     slots, two = z.shape
@@ -648,8 +665,8 @@ def gate_grad(z, dz, row_to_slot, dlogp):
     rows = row_to_slot.numel()
     _vector(row_to_slot, rows, torch.int32, "row_to_slot")
     _vector(dlogp, rows, torch.float32, "dlogp")
-    _check(load().moe_gate_grad(_ptr(z), _ptr(dz), code, _ptr(row_to_slot), rows, slots, two // 2,
-                                _ptr(dlogp), _stream()))
+    _check(load().moe_gate_grad(_at(z), _at(dz), code, _at(row_to_slot), rows, slots, two // 2,
+                                _at(dlogp), st))
     return dlogp
 
 
@@ -685,17 +702,17 @@ def _norm_desc(rows, w, gate, alpha, eps, name):
 
 
 def _opt_rows(t, T, d, dtype, name):
-    return (None, 0) if t is None else (_ptr(t), _rows(t, T, d, dtype, name))
+    return (None, 0) if t is None else (t.data_ptr(), _rows(t, T, d, dtype, name))
 
 
 def norm_in(x, w, eps, n, rstd, u=None, gate=None, alpha=1.0, r=None):
     """Before the block: r = x + alpha gate u, n = w r / rms(r); rstd [T] for the backward pass."""
-    _here(x, w, n, rstd, u, gate, r)
+    st = _here(x, w, n, rstd, u, gate, r)
     N, T, d, ldx = _norm_desc(x, w, gate, alpha, eps, "x")
     _vector(rstd, T, torch.float32, "rstd")
-    _check(load().moe_norm_in(ctypes.byref(N), _ptr(x), ldx, *_opt_rows(u, T, d, x.dtype, "u"),
-                              *_opt_rows(r, T, d, x.dtype, "r"), _ptr(n),
-                              _rows(n, T, d, x.dtype, "n"), _ptr(rstd), _stream()))
+    _check(load().moe_norm_in(ctypes.byref(N), _at(x), ldx, *_opt_rows(u, T, d, x.dtype, "u"),
+                              *_opt_rows(r, T, d, x.dtype, "r"), _at(n),
+                              _rows(n, T, d, x.dtype, "n"), _at(rstd), st))
     return n
 
 
@@ -703,54 +720,54 @@ def _norm_grads(T, d, gate, dw, dgate, ws):
     _vector(dw, d, torch.float32, "dw")
     if gate is not None and dgate is not None:
         _vector(dgate, gate.numel(), torch.float32, "dgate")
-    _vector(ws, 1, torch.uint8, "ws")
-    return _aligned(ws)
+    return _ws_at(ws)
 
 
 def norm_in_backward(dn, r, w, rstd, dx, dw, ws, dr=None, u=None, gate=None, alpha=1.0, du=None,
                      dgate=None):
     """Gradients of norm_in: dx (r's and x's), dw, and with u also du and dgate (shaped like gate)."""
-    _here(dn, r, w, rstd, dx, dw, ws, dr, u, gate, du, dgate)
+    st = _here(dn, r, w, rstd, dx, dw, ws, dr, u, gate, du, dgate)
     N, T, d, ldr = _norm_desc(r, w, gate, alpha, 1.0, "r")
     dt = r.dtype
     _vector(rstd, T, torch.float32, "rstd")
     wsp, wsn = _norm_grads(T, d, gate, dw, dgate, ws)
     _check(load().moe_norm_in_backward(
-        ctypes.byref(N), _ptr(dn), _rows(dn, T, d, dt, "dn"), *_opt_rows(dr, T, d, dt, "dr"),
-        _ptr(r), ldr, *_opt_rows(u, T, d, dt, "u"), _ptr(rstd), _ptr(dx),
-        _rows(dx, T, d, dt, "dx"), *_opt_rows(du, T, d, dt, "du"), _ptr(dw), _ptr(dgate), wsp, wsn,
-        _stream()))
+        ctypes.byref(N), _at(dn), _rows(dn, T, d, dt, "dn"), *_opt_rows(dr, T, d, dt, "dr"),
+        _at(r), ldr, *_opt_rows(u, T, d, dt, "u"), _at(rstd), _at(dx),
+        _rows(dx, T, d, dt, "dx"), *_opt_rows(du, T, d, dt, "du"), _at(dw), _at(dgate), wsp, wsn,
+        st))
     return dx
 
 
 def norm_out(y, x, w, eps, out, rstd, gate=None, alpha=1.0):
     """After the block: out = x + alpha gate w y / rms(y); rstd [T] for the backward pass."""
-    _here(y, x, w, out, rstd, gate)
+    st = _here(y, x, w, out, rstd, gate)
     N, T, d, ldy = _norm_desc(y, w, gate, alpha, eps, "y")
     _vector(rstd, T, torch.float32, "rstd")
-    _check(load().moe_norm_out(ctypes.byref(N), _ptr(y), ldy, _ptr(x),
-                               _rows(x, T, d, y.dtype, "x"), _ptr(out),
-                               _rows(out, T, d, y.dtype, "out"), _ptr(rstd), _stream()))
+    _check(load().moe_norm_out(ctypes.byref(N), _at(y), ldy, _at(x),
+                               _rows(x, T, d, y.dtype, "x"), _at(out),
+                               _rows(out, T, d, y.dtype, "out"), _at(rstd), st))
     return out
 
 
 def norm_out_backward(dout, y, w, rstd, dy, dw, ws, gate=None, alpha=1.0, dgate=None):
     """Gradients of norm_out: dy, dw and dgate (shaped like gate); x's is dout."""
-    _here(dout, y, w, rstd, dy, dw, ws, gate, dgate)
+    st = _here(dout, y, w, rstd, dy, dw, ws, gate, dgate)
     N, T, d, ldy = _norm_desc(y, w, gate, alpha, 1.0, "y")
     _vector(rstd, T, torch.float32, "rstd")
     wsp, wsn = _norm_grads(T, d, gate, dw, dgate, ws)
     _check(load().moe_norm_out_backward(
-        ctypes.byref(N), _ptr(dout), _rows(dout, T, d, y.dtype, "dout"), _ptr(y), ldy, _ptr(rstd),
-        _ptr(dy), _rows(dy, T, d, y.dtype, "dy"), _ptr(dw), _ptr(dgate), wsp, wsn, _stream()))
+        ctypes.byref(N), _at(dout), _rows(dout, T, d, y.dtype, "dout"), _at(y), ldy, _at(rstd),
+        _at(dy), _rows(dy, T, d, y.dtype, "dy"), _at(dw), _at(dgate), wsp, wsn, st))
     return dy
 
 
 class PreparedAdamw:
-    """A prepared list of tensors (moe_adamw_prepare) and the tensors, which it keeps alive."""
+    """A prepared list of tensors (moe_adamw_prepare), its workspace, and the tensors, which it keeps
+    alive."""
 
-    def __init__(self, c_list, device, keep):
-        self.list, self.device, self.keep = c_list, device, keep
+    def __init__(self, c_list, ws, keep):
+        self.list, self.ws, self.keep = c_list, ws, keep
 
 
 def make_adamw(p, g, m, v, m_scale=None, v_scale=None, master=None) -> PreparedAdamw:
@@ -791,7 +808,6 @@ def make_adamw(p, g, m, v, m_scale=None, v_scale=None, master=None) -> PreparedA
         a.p, a.g, a.m, a.v, a.n = (p[i].data_ptr(), g[i].data_ptr(), m[i].data_ptr(),
                                    v[i].data_ptr(), n)
         a.p_dtype, a.g_dtype = _dtype_code(p[i].dtype, f"p[{i}]"), _dtype_code(g[i].dtype, f"g[{i}]")
-    device = torch.cuda.current_device()
     size = int(load().moe_adamw_workspace_size(count))
     if size == 0 and count:
         raise MoeError("moe_adamw_workspace_size rejected the list")
@@ -799,7 +815,7 @@ def make_adamw(p, g, m, v, m_scale=None, v_scale=None, master=None) -> PreparedA
     wsp, wsn = _aligned(ws)
     out = AdamwList()
     _check(load().moe_adamw_prepare(arr, count, bits, ctypes.byref(out), wsp, wsn, _stream()))
-    return PreparedAdamw(out, device, keep + [ws])
+    return PreparedAdamw(out, ws, keep)
 
 
 def adamw(prepared: PreparedAdamw, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1,
@@ -824,9 +840,7 @@ def adamw(prepared: PreparedAdamw, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_
         _here(grad_scale)
         _vector(grad_scale, 1, torch.float32, "grad_scale")
         h.grad_scale = grad_scale.data_ptr()
-    if prepared.device != torch.cuda.current_device():
-        raise MoeError("the list was prepared on another device")
-    _check(load().moe_adamw(ctypes.byref(prepared.list), ctypes.byref(h), _stream()))
+    _check(load().moe_adamw(ctypes.byref(prepared.list), ctypes.byref(h), _here(prepared.ws)))
 
 
 class Events:

@@ -80,11 +80,13 @@ class LayerRunner:
                   self.fp8_act)
         return self.y
 
-    def backward(self, x, gates, dy, topk_ids, block_worker=None, events=None, timeline=None):
+    def backward(self, x, gates, dy, topk_ids, block_worker=None, events=None, timeline=None,
+                 dlogp=None):
+        """dx, dw1, dw2; into dlogp [T][k] (optional) the gates' gradients in log form, p dL/dp."""
         bw = self.plan_b["block_worker"] if block_worker is None else block_worker
         B.backward(self.layer, x, gates, dy, self.z, topk_ids, self.beta, self.P, self.s, self.rs,
                    self.owner, bw, self.dx, self.dw1, self.dw2, self.ws, self.status, events,
-                   timeline, self.two_phase, self.split_bwd, self.fp8_act)
+                   timeline, self.two_phase, self.split_bwd, self.fp8_act, dlogp)
         return self.dx, self.dw1, self.dw2
 
     def step(self, x, gates, topk_ids, dy=None, s=None, timeline=None):
@@ -120,3 +122,100 @@ class LayerRunner:
     def join_bwd_plan(self):
         """The current stream waits for the backward plan."""
         torch.cuda.current_stream(self.dev).wait_stream(self.side)
+
+
+class BlockRunner(LayerRunner):
+    """The expert layer as a block of a model, trained: norm -> router -> layer -> norm, gate and
+    residual, its gradients, and AdamW on its weights.
+
+        n = w_in x / rms(x);  logits = n w_router^T;  ids, gates, losses = router(logits)
+        out = x + alpha gate (w_out y / rms(y)),  y = layer(n, gates, ids)
+
+    w_router [E][d] and the norms' weights w_in, w_out [d] are of the activation dtype, gate [d] is
+    fp32 (None: 1).  The two products with w_router are plain library products; every other step
+    is a library call of its own over buffers made here, on the current stream."""
+
+    def __init__(self, w1, w2, w_router, w_in, w_out, gate=None, w1_scale=None, w2_scale=None, *,
+                 score="softmax", renorm=True, scale=1.0, alpha=1.0, eps=1e-6, **layer):
+        super().__init__(w1, w2, w1_scale, w2_scale, **layer)
+        T, d, dev, dt = self.T, self.d, self.dev, self.act_dtype
+        if tuple(w_router.shape) != (self.E, d) or w_router.dtype != dt:
+            raise B.MoeError(f"w_router: expected {(self.E, d)} of {dt}, got "
+                             f"{tuple(w_router.shape)} of {w_router.dtype}")
+        self.w_router, self.w_in, self.w_out, self.gate = w_router, w_in, w_out, gate
+        self.alpha, self.eps = alpha, eps
+        self.router = B.make_router(self.E, self.k, dt, score, renorm, scale)
+        self.routed = B.alloc_router(self.router, T, dev)
+        self.router_ws = B.router_workspace(self.router, T, dev)
+        rows = dict(dtype=dt, device=dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.n, self.out = torch.empty((T, d), **rows), torch.empty((T, d), **rows)
+        self.logits = torch.empty((T, self.E), **rows)
+        self.rstd_in, self.rstd_out = torch.empty(T, **f32), torch.empty(T, **f32)
+        self.optimizer = None
+        if self.with_backward:
+            self.norm_ws = B.norm_workspace(T, d, dev)
+            self.dy, self.dn = torch.empty((T, d), **rows), torch.empty((T, d), **rows)
+            self.dx_block = torch.empty((T, d), **rows)
+            self.dlogits = torch.empty((T, self.E), **rows)
+            self.dw_router = torch.empty((self.E, d), **rows)
+            self.dlogp = torch.empty((T, self.k), **f32)
+            self.dw_in, self.dw_out = torch.empty(d, **f32), torch.empty(d, **f32)
+            self.dgate = None if gate is None else torch.empty(d, **f32)
+
+    def block_forward(self, x, mask=None):
+        """out [T][d] of x [T][d]; mask [T] (optional): 0 where a row is padding, which passes the
+        residual alone.  The routing's losses are in self.routed["losses"]."""
+        self.x, self.mask = x, mask
+        B.norm_in(x, self.w_in, self.eps, self.n, self.rstd_in)
+        torch.mm(self.n, self.w_router.t(), out=self.logits)
+        r = B.router_forward(self.router, self.logits, self.routed, self.router_ws, self.status, mask)
+        self.route(r["topk_ids"])
+        if self.with_backward:
+            self.plan_bwd_async()
+        self.make_plan()
+        self.forward(self.n, r["gates"], r["topk_ids"])
+        if self.with_backward:                 # the next call rewrites what the plan reads
+            self.join_bwd_plan()
+        return B.norm_out(self.y, x, self.w_out, self.eps, self.out, self.rstd_out, self.gate,
+                          self.alpha)
+
+    def block_backward(self, dout, dlosses=None):
+        """Gradients of block_forward's last call from dout [T][d] and (optional) dlosses [2], those
+        of the balance and z losses: dx, and dw1, dw2, dw_router, dw_in, dw_out, dgate in self."""
+        r = self.routed
+        B.norm_out_backward(dout, self.y, self.w_out, self.rstd_out, self.dy, self.dw_out,
+                            self.norm_ws, self.gate, self.alpha, self.dgate)
+        self.backward(self.n, r["gates"], self.dy, r["topk_ids"], dlogp=self.dlogp)
+        B.router_backward(self.router, self.logits, r, self.dlogp, dlosses, self.dlogits, self.mask)
+        torch.mm(self.dlogits.t(), self.n, out=self.dw_router)
+        torch.addmm(self.dx, self.dlogits, self.w_router, out=self.dn)
+        return B.norm_in_backward(self.dn, self.x, self.w_in, self.rstd_in, self.dx_block, self.dw_in,
+                                  self.norm_ws, dr=dout)
+
+    def make_optimizer(self, state_bits=32):
+        """AdamW states (zeros) for the block's weights; state_bits 32 (fp32) or 8 (e4m3 codes and
+        a scale for 128 of them)."""
+        if not self.with_backward or self.layer.w_dtype == B.MOE_FP8_E4M3:
+            raise B.MoeError("the optimizer needs a runner with a backward pass and fp32 or bf16 weights")
+        w1, w2 = self.keep[:2]
+        p = [w1, w2, self.w_router, self.w_in, self.w_out]
+        g = [self.dw1, self.dw2, self.dw_router, self.dw_in, self.dw_out]
+        if self.gate is not None:
+            p.append(self.gate)
+            g.append(self.dgate)
+        if state_bits not in (8, 32):
+            raise B.MoeError(f"state_bits={state_bits}: 8 or 32")
+        dt = torch.uint8 if state_bits == 8 else torch.float32
+        states = lambda: [torch.zeros(t.shape, dtype=dt, device=self.dev) for t in p]
+        scales = lambda: [torch.zeros(-(-t.numel() // B.ADAMW_BLOCK), device=self.dev) for t in p] \
+            if state_bits == 8 else None
+        self.state = {"m": states(), "v": states(), "m_scale": scales(), "v_scale": scales()}
+        self.optimizer = B.make_adamw(p, g, **self.state)
+        return self.optimizer
+
+    def optimizer_step(self, lr, step, **hyper):
+        """One AdamW step (binding.adamw's arguments) on the block's weights, in place."""
+        if self.optimizer is None:
+            raise B.MoeError("make_optimizer first")
+        B.adamw(self.optimizer, lr, step=step, **hyper)
