@@ -608,7 +608,8 @@ typedef struct {
 typedef struct {
   const void* table;     /* device */
   int tensors, state_bits;
-  uint32_t items;
+  uint32_t items;        /* of `item` consecutive elements of one tensor each */
+  int item;
 } moe_adamw_list;
 
 typedef struct {

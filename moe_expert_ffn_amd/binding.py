@@ -87,7 +87,7 @@ class AdamwTensor(ctypes.Structure):
 
 class AdamwList(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("tensors", ctypes.c_int),
-                ("state_bits", ctypes.c_int), ("items", ctypes.c_uint32)]
+                ("state_bits", ctypes.c_int), ("items", ctypes.c_uint32), ("item", ctypes.c_int)]
 
 
 class AdamwHyper(ctypes.Structure):

@@ -11,8 +11,8 @@
 namespace moe {
 
 // The table of a prepared list: the tensors, and the first item of each.  An
-// item is kAdamItem consecutive elements of one tensor, a workgroup's unit.
-constexpr int kAdamItem = 4096, kAdamThreads = 256, kAdamVE = 8;
+// item is a number of consecutive elements of one tensor, a workgroup's unit.
+constexpr int kAdamThreads = 256, kAdamVE = 8, kAdamPass = kAdamThreads * kAdamVE;
 static_assert(MOE_ADAMW_BLOCK == 16 * kAdamVE, "a block of states is a row of 16 lanes");
 
 struct AdamTensor {
@@ -53,10 +53,11 @@ __global__ void k_adamw_table(AdamPart part, int base, int count, AdamTensor* t,
 struct AdamArgs {
   const AdamTensor* t;
   const uint32_t* first;
-  int tensors;
+  int tensors, item;
   uint32_t items;
   float lr, beta1, beta2, c1, c2, eps, wd;   // c = 1 - beta
-  double log_beta1, log_beta2;   // -infinity for 0
+  double log_beta1, log_beta2;   // -infinity for 0; only with step_dev
+  float bias1, bias2;            // 1 - beta^step without
   int step;
   uint32_t seed;
   const int32_t* step_dev;
@@ -123,52 +124,68 @@ MOE_DEV void from_e4m3(const uint8_t* codes, float scale, float* v) {
   }
 }
 
+// sqrt rounded to nearest: the hardware's is within an ulp, and of s and its two neighbours the
+// nearest to the root has s (s - ulp) < x <= s (s + ulp).  (0, infinity and NaN pass: their
+// neighbours compare false.)
+MOE_DEV float sqrt_nearest(float x) {
+  const float s = __builtin_amdgcn_sqrtf(x);
+  const float dn = __uint_as_float(__float_as_uint(s) - 1u), up = __uint_as_float(__float_as_uint(s) + 1u);
+  const float low = __builtin_fmaf(-dn, s, x), high = __builtin_fmaf(-up, s, x);
+  return high > 0.f ? up : low <= 0.f ? dn : s;
+}
+
+constexpr uint32_t kInfBits = 0x7F800000u;
+MOE_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
 // Eight states of a lane into codes; the 16 lanes of a block share its scale.
-// y = |x| * 448 / top is rounded up with the probability of the part cut off:
-// the low 20 bits of its fp32 word are that part, so adding u16 + 1/2 in units
-// of 2^4 to the word and dropping them is floor(y / step + u) steps, in whole
-// numbers.  Below e4m3's normal range the step stays 2^-9: there 2^-6 is added
-// first, which puts y into an octave with that step.  y is at most two ulps
-// above 448, which no u16 carries to the next code, so no clamp is needed.
-// SIGNED: x may be negative.  random: bits SHIFT..SHIFT + 15 of word.
+// y = |x| * (1 / top * 448) is rounded up with the probability of the part cut off:
+// with the code step at y, 2^(exponent - 3) and at least 2^-9, and u the random
+// 16 bits plus a half over 2^16, t = y + u * step loses what is below a step.
+// In e4m3's normal range those are the low 20 bits of t's word, below it the
+// fraction of t * 512; of the two readings b and c the right one is the middle
+// one of b, c and 8 (b <= c everywhere, both 8 at 2^-6).  y is at most two ulps
+// above 448, which no u carries to the next code, so no clamp is needed.
+// Every operation is one fp32 rounding in this order, so that equal states give
+// equal codes wherever they are computed so.
+// SIGNED: x may be negative.  u: bits SHIFT..SHIFT + 15 of word.
 template <bool SIGNED, int SHIFT>
 MOE_DEV void to_e4m3(const float* x, const uint32_t* word, uint8_t* codes, float* scale) {
-  float top = 0.f;
+#pragma clang fp contract(off)
+  uint32_t most = 0;                                     // magnitudes order as their words do
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));       // NaN is passed over
-  top = group_all<16>(top, OpMaxF());
+  for (int i = 0; i < 8; ++i) most = max(most, SIGNED ? abs_bits(x[i]) : __float_as_uint(x[i]));
+  most = group_all<16>(most, OpMax());
   // a value that is not finite stays out of the scale (rare: a branch of whole waves)
-  bool odd = false;
+  const bool odd = __any(most >= kInfBits);
+  if (odd) {
+    most = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) odd |= !(fabsf(x[i]) < INFINITY);
-  if (__any(odd)) {
-    top = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
-    top = group_all<16>(top, OpMaxF());
+    for (int i = 0; i < 8; ++i) most = max(most, abs_bits(x[i]) < kInfBits ? abs_bits(x[i]) : 0u);
+    most = group_all<16>(most, OpMax());
   }
-  if (top < 0x1p-100f) top = 0.f;
-  const float inv = top > 0.f ? 448.f / top : 0.f;
-  const float small = top * (0x1p-6f / 448.f);
+  const float top = __uint_as_float(most) < 0x1p-100f ? 0.f : __uint_as_float(most);
+  const float inv = top > 0.f ? 1.f / top * 448.f : 0.f;
   *scale = top * (1.f / 448.f);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const bool low = fabsf(x[i]) < small || inv == 0.f;
-    const float y = fabsf(x[i]) * inv + (low ? 0x1p-6f : 0.f);
-    const uint32_t r = (SHIFT ? word[i] >> (SHIFT - 4) : word[i] << 4) & 0xFFFF0u;
-    uint32_t c = ((__float_as_uint(y) + r + 8u) >> 20) - (low ? 121u << 3 : 120u << 3);
-    if (SIGNED) c |= __float_as_uint(x[i]) >> 24 & 0x80u;
-    codes[i] = (uint8_t)c;
+    const float y = fabsf(x[i]) * inv;
+    const uint32_t step = max((__float_as_uint(y) & 0x7F800000u) - (20u << 23), 101u << 23);   // / 2^17
+    const uint32_t u = ((SHIFT ? word[i] >> (SHIFT - 1) : word[i] << 1) & 0x1FFFEu) | 1u;
+    const float t = __builtin_fmaf((float)u, __uint_as_float(step), y);
+    const int b = (int)(__float_as_uint(t) >> 20) - (120 << 3), c = (int)(t * 512.f);
+    int code = max(min(b, c), min(max(b, c), 8));
+    if (SIGNED) code |= (int)(__float_as_uint(x[i]) >> 24 & 0x80u);
+    codes[i] = (uint8_t)code;
   }
-  if (__any(odd)) {
+  if (odd) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (!(fabsf(x[i]) < INFINITY)) codes[i] = 0x7F;
+      if (abs_bits(x[i]) >= kInfBits) codes[i] = 0x7F;
   }
 }
 
 // 1 - beta^t, from log(beta) in double: no cancellation at beta near 1
-MOE_DEV float bias(double log_beta, int t) { return (float)-expm1(log_beta * t); }
+static __host__ __device__ float bias(double log_beta, int t) { return (float)-expm1(log_beta * t); }
 
 // The tensor that holds an item: how many of first[1..tensors] are at or below
 // it.  64 lanes look at a sorted table of up to 64 * 64 entries in two steps.
@@ -186,6 +203,7 @@ struct AdamRates { float rate, root, keep, gs; };
 template <int BITS, bool FULL>
 MOE_DEV void adam8(const AdamArgs& a, const AdamTensor& t, const AdamRates& h, uint32_t key,
                    int64_t at, int n) {
+#pragma clang fp contract(off)
   float p[8], g[8], m[8], v[8];
   load8f<FULL>(t.master ? t.master : t.p, t.master || t.p32, at, n, p);
   load8f<FULL>(t.g, t.g32, at, n, g);
@@ -201,18 +219,23 @@ MOE_DEV void adam8(const AdamArgs& a, const AdamTensor& t, const AdamRates& h, u
     from_e4m3(mc, ms, m);
     from_e4m3(vc, vs, v);
   }
+  if (a.grad_scale) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] *= h.gs;
+  }
   uint32_t word[8];
   const uint32_t w0 = (uint32_t)at * kGold + key;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     word[i] = mix(w0 + (uint32_t)i * kGold);
     if constexpr (BITS == 8) v[i] *= v[i];
-    g[i] *= h.gs;
     m[i] = a.beta1 * m[i] + a.c1 * g[i];
-    v[i] = a.beta2 * v[i] + a.c2 * g[i] * g[i];
-    // sqrt and reciprocal of 1 ulp: the update is lr times a number near 1
-    const float s = __builtin_amdgcn_sqrtf(v[i]);
-    p[i] = p[i] * h.keep - h.rate * m[i] * __builtin_amdgcn_rcpf(s * h.root + a.eps);
+    v[i] = a.beta2 * v[i] + a.c2 * (g[i] * g[i]);
+    // the update is lr times a number near 1: a reciprocal of 1 ulp, and where its root is not stored
+    // a root of 1 ulp
+    const float s = BITS == 8 ? sqrt_nearest(v[i]) : __builtin_amdgcn_sqrtf(v[i]);
+    const float d = __builtin_amdgcn_rcpf(__builtin_fmaf(s, h.root, a.eps));
+    p[i] = __builtin_fmaf(-h.rate * m[i], d, p[i] * h.keep);
     if constexpr (BITS == 8) v[i] = s;
   }
   if constexpr (BITS == 32) {
@@ -248,59 +271,67 @@ MOE_DEV void adam8(const AdamArgs& a, const AdamTensor& t, const AdamRates& h, u
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       o[i] = (uint16_t)((__float_as_uint(p[i]) + (word[i] * kRoot3 >> 16)) >> 16);
-    bool odd = false;
+    uint32_t most = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) odd |= !(fabsf(p[i]) < INFINITY);
-    if (__any(odd)) {                                     // adding to NaN's or infinity's word
+    for (int i = 0; i < 8; ++i) most = max(most, abs_bits(p[i]));
+    if (__any(most >= kInfBits)) {                        // adding to a NaN's word may leave NaN
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (!(fabsf(p[i]) < INFINITY)) o[i] = f2bf(p[i]);
+        if (abs_bits(p[i]) >= kInfBits) o[i] = f2bf(p[i]);
     }
   }
   store8<uint16_t, FULL>((uint16_t*)t.p + at, n, o);
 }
 
+// One pass over everything a step touches; a workgroup an item.  Bound by HBM: with 8-bit states,
+// bf16 parameters and fp32 gradients 12.1 bytes an element, 604M elements in 1.35 ms (5.4 TB/s; a
+// 1 GiB copy reaches 4.96), with 32-bit states 24 bytes, 2.63 ms (5.5 TB/s).  The 8-bit path issues
+// some 60 VALU cycles-of-four an element, about 1 ms of the chip, which is why codes are converted by
+// hardware, rounded as whole numbers and never divided.  A persistent grid was slower (1.46 ms),
+// non-temporal accesses 3% faster here but 20% slower where the tensors fit the caches.
 template <int BITS>
 __global__ __launch_bounds__(kAdamThreads, 4) void k_adamw(AdamArgs a) {
-  __shared__ float hyper[2];
   const int tid = threadIdx.x;
-  const int step = a.step_dev ? *a.step_dev : a.step;
-  if (tid < 2) hyper[tid] = bias(tid ? a.log_beta2 : a.log_beta1, step);
-  __syncthreads();
+  int step = a.step;
+  float b1 = a.bias1, b2 = a.bias2;
+  if (a.step_dev) {                                       // a few microseconds of fp64
+    __shared__ float hyper[2];
+    step = *a.step_dev;
+    if (tid < 2) hyper[tid] = bias(tid ? a.log_beta2 : a.log_beta1, step);
+    __syncthreads();
+    b1 = hyper[0];
+    b2 = hyper[1];
+  }
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
-  const AdamRates h{lr / hyper[0], 1.f / sqrtf(hyper[1]), 1.f - lr * a.wd,
-                    a.grad_scale ? *a.grad_scale : 1.f};
-  AdamTensor t{};
-  uint32_t begin = 0, end = 0, key = 0;                   // the tensor's items
-  for (uint32_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-    if (item >= end) {
-      const int j = __builtin_amdgcn_readfirstlane(tensor_of(a.first, a.tensors, item));
-      t = a.t[j];
-      begin = a.first[j];
-      end = a.first[j + 1];
-      key = mix(a.seed + (uint32_t)step * kGold + (uint32_t)j * kRoot3);
-    }
-    const int64_t base = (int64_t)(item - begin) * kAdamItem;
-    if (t.vec && t.n - base >= kAdamItem) {
+  const AdamRates h{lr / b1, 1.f / sqrtf(b2), 1.f - lr * a.wd, a.grad_scale ? *a.grad_scale : 1.f};
+  const uint32_t item = blockIdx.x;
+  const int j = __builtin_amdgcn_readfirstlane(tensor_of(a.first, a.tensors, item));
+  const AdamTensor t = a.t[j];
+  const uint32_t key = mix(a.seed + (uint32_t)step * kGold + (uint32_t)j * kRoot3);
+  // whole blocks of 128 (a row of 16 lanes) take the wide accesses
 #pragma unroll 1
-      for (int o = tid * 8; o < kAdamItem; o += kAdamThreads * 8)
-        adam8<BITS, true>(a, t, h, key, base + o, 8);
-    } else {
-#pragma unroll 1
-      for (int o = tid * 8; o < kAdamItem; o += kAdamThreads * 8) {
-        const int64_t left = t.n - base - o;
-        adam8<BITS, false>(a, t, h, key, base + o, left >= 8 ? 8 : left > 0 ? (int)left : 0);
-      }
-    }
+  for (int pass = 0; pass < a.item; pass += kAdamPass) {
+    const int64_t at = (int64_t)(item - a.first[j]) * a.item + pass + tid * 8;
+    const int64_t left = t.n - at, block = t.n - (at & ~(int64_t)(MOE_ADAMW_BLOCK - 1));
+    if (t.vec && block >= MOE_ADAMW_BLOCK)
+      adam8<BITS, true>(a, t, h, key, at, 8);
+    else if (block > 0)
+      adam8<BITS, false>(a, t, h, key, at, left >= 8 ? 8 : left > 0 ? (int)left : 0);
   }
 }
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-int launch_adamw_table(const moe_adamw_tensor* t, int count, int bits, uint32_t* items, void* ws,
-                       hipStream_t st) {
-  const AdamTable tab = adamw_table(ws, count);
+int launch_adamw_table(const moe_adamw_tensor* t, int count, moe_adamw_list* out, hipStream_t st) {
+  const AdamTable tab = adamw_table(out->table, count);
+  const int bits = out->state_bits;
+  // 32-bit states are bound by HBM at any item; 8-bit ones spend their time in the VALU too, where the
+  // search at a workgroup's start shows: 604M elements 1495 us at 2048, 1354 at 8192 (1376 at 16384),
+  // 20M 47.8 and 45.5; 5M 17.7 at 2048 and 20.7 at 8192, which leaves too few workgroups.
+  long long elements = 0;
+  for (int i = 0; i < count; ++i) elements += t[i].n;
+  out->item = bits == 8 && elements >= 2048ll * 4 * kAdamPass ? 4 * kAdamPass : kAdamPass;
   uint32_t total = 0;
   for (int base = 0; base < count; base += kAdamPart) {
     AdamPart part{};
@@ -317,12 +348,12 @@ int launch_adamw_table(const moe_adamw_tensor* t, int count, int bits, uint32_t*
                                        : (uintptr_t)s.m | (uintptr_t)s.v);
       d.vec = (all & 15u) == 0;
       part.first[i] = total;
-      total += (uint32_t)((s.n + kAdamItem - 1) / kAdamItem);
+      total += (uint32_t)((s.n + out->item - 1) / out->item);
     }
     part.first[n] = total;
     hipLaunchKernelGGL(k_adamw_table, dim3(1), dim3(64), 0, st, part, base, n, tab.t, tab.first);
   }
-  *items = total;
+  out->items = total;
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
@@ -330,13 +361,15 @@ int launch_adamw(const moe_adamw_list& l, const moe_adamw_hyper& h, hipStream_t 
   if (l.items == 0) return MOE_OK;
   const AdamTable tab = adamw_table(l.table, l.tensors);
   AdamArgs a{};
-  a.t = tab.t; a.first = tab.first; a.tensors = l.tensors; a.items = l.items;
+  a.t = tab.t; a.first = tab.first; a.tensors = l.tensors; a.items = l.items; a.item = l.item;
   a.lr = (float)h.lr; a.eps = (float)h.eps; a.wd = (float)h.weight_decay;
   a.beta1 = (float)h.beta1; a.c1 = (float)(1.0 - h.beta1); a.log_beta1 = std::log(h.beta1);
   a.beta2 = (float)h.beta2; a.c2 = (float)(1.0 - h.beta2); a.log_beta2 = std::log(h.beta2);
+  a.bias1 = h.step_dev ? 1.f : bias(a.log_beta1, h.step);
+  a.bias2 = h.step_dev ? 1.f : bias(a.log_beta2, h.step);
   a.step = h.step; a.seed = h.seed;
   a.step_dev = h.step_dev; a.lr_dev = h.lr_dev; a.grad_scale = h.grad_scale;
-  const dim3 grid(std::min<uint32_t>(l.items, 256 * 8));
+  const dim3 grid(l.items);
   if (l.state_bits == 8) hipLaunchKernelGGL(k_adamw<8>, grid, dim3(kAdamThreads), 0, st, a);
   else hipLaunchKernelGGL(k_adamw<32>, grid, dim3(kAdamThreads), 0, st, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;

@@ -533,14 +533,13 @@ int moe_adamw_prepare(const moe_adamw_tensor* tensors, int count, int state_bits
     free(ext);
     if (!apart) return MOE_ERR_ARG;
   }
-  uint32_t items = 0;
-  const int rc = launch_adamw_table(tensors, count, state_bits, &items, ws, (hipStream_t)stream);
-  if (rc != MOE_OK) return rc;
-  out->table = ws;
-  out->tensors = count;
-  out->state_bits = state_bits;
-  out->items = items;
-  return MOE_OK;
+  moe_adamw_list list{};
+  list.table = ws;
+  list.tensors = count;
+  list.state_bits = state_bits;
+  const int rc = launch_adamw_table(tensors, count, &list, (hipStream_t)stream);
+  if (rc == MOE_OK) *out = list;
+  return rc;
 }
 
 int moe_adamw(const moe_adamw_list* list, const moe_adamw_hyper* h, void* stream) {

@@ -99,8 +99,7 @@ int launch_norm_bwd(const moe_norm& N, bool out, NormRows dn, NormRows dr, NormR
                     hipStream_t st);
 
 size_t adamw_ws_bytes(int tensors);
-int launch_adamw_table(const moe_adamw_tensor* t, int count, int bits, uint32_t* items, void* ws,
-                       hipStream_t st);
+int launch_adamw_table(const moe_adamw_tensor* t, int count, moe_adamw_list* out, hipStream_t st);
 int launch_adamw(const moe_adamw_list& l, const moe_adamw_hyper& h, hipStream_t st);
 
 int launch_forward(const Sizes& z, const LayerPtrs& L, const void* x, const float* gates,
