@@ -149,39 +149,54 @@ MOE_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 // equal codes wherever they are computed so.
 // SIGNED: x may be negative.  u: bits SHIFT..SHIFT + 15 of word.
 template <bool SIGNED, int SHIFT>
-MOE_DEV void to_e4m3(const float* x, const uint32_t* word, uint8_t* codes, float* scale) {
+MOE_DEV void to_e4m3(float* x, const uint32_t* word, uint8_t* codes, float* scale) {
 #pragma clang fp contract(off)
   uint32_t most = 0;                                     // magnitudes order as their words do
 #pragma unroll
   for (int i = 0; i < 8; ++i) most = max(most, SIGNED ? abs_bits(x[i]) : __float_as_uint(x[i]));
   most = group_all<16>(most, OpMax());
   // a value that is not finite stays out of the scale (rare: a branch of whole waves)
+  uint32_t nan[2] = {0u, 0u};                            // their codes
   const bool odd = __any(most >= kInfBits);
   if (odd) {
+    asm volatile("");                                    // keeps the branch: not worth 40 selects
     most = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) most = max(most, abs_bits(x[i]) < kInfBits ? abs_bits(x[i]) : 0u);
+    for (int i = 0; i < 8; ++i) {
+      if (abs_bits(x[i]) >= kInfBits) {
+        x[i] = 0.f;
+        nan[i / 4] |= 0x7Fu << 8 * (i % 4);
+      }
+      most = max(most, abs_bits(x[i]));
+    }
     most = group_all<16>(most, OpMax());
   }
   const float top = __uint_as_float(most) < 0x1p-100f ? 0.f : __uint_as_float(most);
   const float inv = top > 0.f ? 1.f / top * 448.f : 0.f;
   *scale = top * (1.f / 448.f);
+  uint32_t code[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float y = fabsf(x[i]) * inv;
-    const uint32_t step = max((__float_as_uint(y) & 0x7F800000u) - (20u << 23), 101u << 23);   // / 2^17
-    const uint32_t u = ((SHIFT ? word[i] >> (SHIFT - 1) : word[i] << 1) & 0x1FFFEu) | 1u;
-    const float t = __builtin_fmaf((float)u, __uint_as_float(step), y);
+    const float octave = __uint_as_float(__float_as_uint(fmaxf(y, 0x1p-6f)) & kInfBits);   // 8 steps
+    const float u = __builtin_fmaf((float)(uint16_t)(word[i] >> SHIFT), 0x1p-19f, 0x1p-20f);
+    const float t = __builtin_fmaf(u, octave, y);
     const int b = (int)(__float_as_uint(t) >> 20) - (120 << 3), c = (int)(t * 512.f);
-    int code = max(min(b, c), min(max(b, c), 8));
-    if (SIGNED) code |= (int)(__float_as_uint(x[i]) >> 24 & 0x80u);
-    codes[i] = (uint8_t)code;
+    code[i] = (uint32_t)max(min(b, c), min(max(b, c), 8));
   }
-  if (odd) {
+  uint32_t packed[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (abs_bits(x[i]) >= kInfBits) codes[i] = 0x7F;
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t* q = code + 4 * h;
+    packed[h] = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
+    if constexpr (SIGNED) {                              // the words' top bytes, by pairs
+      const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(x[4 * h + 1]), __float_as_uint(x[4 * h]), 0x0c0c0703u);
+      const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(x[4 * h + 3]), __float_as_uint(x[4 * h + 2]), 0x07030c0cu);
+      packed[h] |= (lo | hi) & 0x80808080u;
+    }
+    packed[h] |= nan[h];
   }
+  __builtin_memcpy(codes, packed, 8);
 }
 
 // 1 - beta^t, from log(beta) in double: no cancellation at beta near 1
@@ -275,6 +290,7 @@ MOE_DEV void adam8(const AdamArgs& a, const AdamTensor& t, const AdamRates& h, u
 #pragma unroll
     for (int i = 0; i < 8; ++i) most = max(most, abs_bits(p[i]));
     if (__any(most >= kInfBits)) {                        // adding to a NaN's word may leave NaN
+      asm volatile("");
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (abs_bits(p[i]) >= kInfBits) o[i] = f2bf(p[i]);
