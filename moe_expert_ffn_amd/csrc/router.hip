@@ -13,7 +13,8 @@ namespace moe {
 // (L * V >= E, V a multiple of 8 so that a lane's logits are whole 16-byte
 // pieces); a workgroup of four waves holds 256 / L rows at a time.
 constexpr int kRouterThreads = 256;
-constexpr int kRouterMaxWG = 256;       // workgroups, and so partial sums, of the forward
+constexpr int kRouterMaxWG = 512;       // workgroups, and so partial sums, of the forward
+constexpr int kTotalThreads = 1024, kTotalCols = 16;
 
 struct RouterArgs {
   const void* logits;
@@ -35,6 +36,8 @@ struct RouterArgs {
   int32_t* part_c;     // [workgroups][E] counts
   float* part_z;       // [workgroups] sums of lse^2
   int32_t* part_n;     // [workgroups] rows routed
+  float* dots;         // [workgroups of the totals] sums of c_e prob_sum_e
+  int32_t* done;       // workgroups of the totals that have written theirs
   size_t ld, ld_out;
   int T, E, k, renorm, vec, parts;
   float scale;
@@ -51,13 +54,12 @@ MOE_DEV float key_value(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// log of the score: l, or log sigmoid(l) = min(l, 0) - log(1 + exp(-|l|))
-template <int SCORE> MOE_DEV float log_score(float l) {
-  if constexpr (SCORE == MOE_SCORE_SOFTMAX) return l;
-  else return fminf(l, 0.f) - log1pf(expf(-fabsf(l)));
-}
+// e^x by the hardware's 2^x: the product's rounding costs |x| 2^-24 relative,
+// next to nothing for the experts that carry a row's weight (x near 0).
+MOE_DEV float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+MOE_DEV float inverse(float x) { return __builtin_amdgcn_rcpf(x); }   // 1 ulp
 
-// The lane's V logits in fp32 (-infinity past E).
+// The lane's V logits in fp32 (-infinity past E and in a row that is off).
 template <typename T, int V>
 MOE_DEV void load_logits(const T* row, int c0, int E, bool vec, bool on, float* v) {
   T raw[V];
@@ -71,42 +73,66 @@ MOE_DEV void load_logits(const T* row, int c0, int E, bool vec, bool on, float* 
   }
 }
 
-// Whether a row with these logits is routed: no NaN, no +infinity, and one
-// logit above -infinity.  *bad: NaN or +infinity.
-template <int L, int V> MOE_DEV bool row_live(const float* v, bool* bad) {
-  int f = 0;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    f |= !(v[i] < INFINITY) ? 2 : 0;                     // NaN compares false
-    f |= v[i] > -INFINITY ? 1 : 0;
+// The row's scores.  w: the scores' exponentials up to a factor of the row,
+// sum their sum, so P = w / sum; top the largest logit.  Softmax: w = e^(l - top).
+// Sigmoid: with a = e^-|l|, sigmoid(l) is 1 / (1 + a) or a / (1 + a); where even the
+// largest logit is negative, a carries the factor e^-top, so that a row whose
+// sigmoids all underflow still has its shares: t = e^(-|l| - low), low = min(top, 0),
+// w = (l < 0 ? t : 1) / (1 + t e^low), and sigmoid(l) = w e^low.
+// A row that is not routed shows in sum and top alone (see row_live).
+template <int SCORE> struct Score {
+  float top, low, elow;
+  MOE_DEV void at_top(float m) {
+    top = m;
+    low = SCORE == MOE_SCORE_SOFTMAX ? m : fminf(m, 0.f);
+    elow = SCORE == MOE_SCORE_SOFTMAX ? 1.f : exp_of(low);
   }
-  f = group_all<L>(f, [](int a, int b) { return a | b; });
-  *bad = (f & 2) != 0;
-  return f == 1;
-}
+  // *away: sigmoid(-l), the slope of log sigmoid
+  MOE_DEV float weight(float l, float* away = nullptr) const {
+    if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+      return exp_of(l - low);
+    } else {
+      const float t = exp_of(-fabsf(l) - low), a = t * elow, r = inverse(1.f + a);
+      if (away) *away = (l < 0.f ? 1.f : a) * r;
+      return (l < 0.f ? t : 1.f) * r;
+    }
+  }
+};
 
-// softmax of v (-infinity: 0) into e; *top its maximum, *sum the sum of exp(v - top)
-template <int L, int V> MOE_DEV void row_softmax(const float* v, float* e, float* top, float* sum) {
+template <int L, int V> MOE_DEV float row_top(const float* v) {
   float m = v[0];
 #pragma unroll
-  for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
-  m = group_all<L>(m, OpMaxF());
+  for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);        // NaN is passed over
+  return group_all<L>(m, OpMaxF());
+}
+
+// Whether a row is routed: NaN makes its sum NaN, so does +infinity in a softmax and a row of
+// -infinities anywhere (inf - inf).
+MOE_DEV bool row_live(float top, float sum) { return top < INFINITY && sum < INFINITY; }
+
+// e^(l - top) summed over the row
+template <int L, int V> MOE_DEV float row_exp_sum(const float* v, float top, float* e) {
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    e[i] = expf(v[i] - m);
+    e[i] = exp_of(v[i] - top);
     s += e[i];
   }
-  s = group_all<L>(s, OpAdd());
-  *top = m;
-  *sum = s;
-  const float inv = 1.f / s;
-#pragma unroll
-  for (int i = 0; i < V; ++i) e[i] *= inv;
+  return group_all<L>(s, OpAdd());
 }
 
-MOE_DEV double balance_of(double sum, int E, int k, int n) {
-  return n > 0 ? (double)E / k * sum / n / n : 0.0;
+MOE_DEV float balance_of(float sum, int E, int k, int n) {
+  return n > 0 ? (float)E / (float)k * (sum / (float)n) / (float)n : 0.f;
+}
+
+// Sum over a workgroup of `waves` waves, for every thread of the first wave.
+MOE_DEV float block_sum(float s, float* red, int waves) {
+  s = group_all<64>(s, OpAdd());
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0.f;
+  for (int i = 0; i < waves; ++i) s += red[i];
+  return s;
 }
 
 // Forward.  Each group takes rows in turn; its lanes keep the sums of P of
@@ -117,13 +143,14 @@ template <typename T, int L, int V, int SCORE>
 __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
   constexpr int G = kRouterThreads / L;                  // rows at a time
   constexpr int C = L * V;
+  constexpr int KQ = (kRouterMaxK + L - 1) / L;          // choices a lane keeps
   __shared__ float sp[4][C];
   __shared__ int sc[C];
-  __shared__ float sz[G];
-  __shared__ int sn[G];
-  __shared__ double sred[4];
+  __shared__ float red[2][4];
+  __shared__ int redn[4];
   const int tid = threadIdx.x, li = tid % L, g = tid / L, c0 = li * V;
   for (int i = tid; i < C; i += kRouterThreads) sc[i] = 0;
+  if (blockIdx.x == 0 && tid == 0 && gridDim.x > 1) *a.done = 0;
   __syncthreads();
   float psum[V];
 #pragma unroll
@@ -132,77 +159,97 @@ __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
   int n = 0;
   const size_t step = (size_t)gridDim.x * G;
   for (size_t t = (size_t)blockIdx.x * G + g; t < (size_t)a.T; t += step) {
-    float v[V], p[V];
+    float v[V], w[V];
     const bool on = !a.mask || a.mask[t];
     load_logits<T, V>((const T*)a.logits + t * a.ld, c0, a.E, a.vec, on, v);
-    bool bad;
-    const bool live = row_live<L, V>(v, &bad);
     int32_t* ids = a.ids + t * a.k;
     float* gates = a.gates + t * a.k;
-    if (!live) {                                         // the whole group
+    Score<SCORE> sc_;
+    sc_.at_top(row_top<L, V>(v));
+    float lsum = row_exp_sum<L, V>(v, sc_.top, w), sum = lsum;
+    if constexpr (SCORE == MOE_SCORE_SIGMOID) {
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        w[i] = sc_.weight(v[i]);
+        sum += w[i];
+      }
+      sum = group_all<L>(sum, OpAdd());
+    }
+    if (!row_live(sc_.top, sum)) {                       // the whole group
       for (int j = li; j < a.k; j += L) {
         ids[j] = -1;
         gates[j] = 0.f;
       }
-      if (bad && li == 0) atomicOr(a.status, MOE_DEV_BAD_LOGIT);
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < V; ++i) bad |= !(v[i] < INFINITY);       // NaN or +infinity
+      if (bad) atomicOr(a.status, MOE_DEV_BAD_LOGIT);
       continue;
     }
-    float top, sum, ltop, lsum;
-    if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-      row_softmax<L, V>(v, p, &top, &sum);
-      ltop = top;
-      lsum = sum;
-    } else {
-      row_softmax<L, V>(v, p, &ltop, &lsum);
-      float s[V];
+    const float inv = inverse(sum);
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = log_score<SCORE>(v[i]);
-      row_softmax<L, V>(s, p, &top, &sum);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) psum[i] += p[i];
-    const float lse = ltop + logf(lsum);
+    for (int i = 0; i < V; ++i) psum[i] += w[i] * inv;
+    const float lse = sc_.top + logf(lsum);
     z += lse * lse;
     ++n;
-    // the k largest: in turn the largest key, then the lowest index that has it
+    // The k largest: in turn the largest key, then the lowest index that has it.  bf16 logits
+    // leave the key's low half free for the index (the lowest the largest), one search for both.
+    constexpr bool kOne = sizeof(T) == 2;
     uint32_t key[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = sort_key(v[i]);
-    constexpr int KQ = (kRouterMaxK + L - 1) / L;          // choices a lane keeps
-    float chosen = 0.f, mine[KQ];
+    for (int i = 0; i < V; ++i) {
+      key[i] = sort_key(v[i]);
+      if (kOne && key[i]) key[i] = (key[i] & 0xFFFF0000u) | (uint32_t)(0xFFFF - (c0 + i));
+    }
+    uint32_t won[KQ];
     int where[KQ];
+#pragma unroll
+    for (int q = 0; q < KQ; ++q) won[q] = 0;
     for (int j = 0; j < a.k; ++j) {
       uint32_t best = key[0];
 #pragma unroll
       for (int i = 1; i < V; ++i) best = max(best, key[i]);
       best = group_all<L>(best, OpMax());
-      int at = C;
+      int at;
+      if constexpr (kOne) {
+        at = 0xFFFF - (int)(best & 0xFFFFu);
 #pragma unroll
-      for (int i = V - 1; i >= 0; --i) at = key[i] == best ? c0 + i : at;
-      at = group_all<L>(at, OpMin());
-      const bool some = best != 0;
+        for (int i = 0; i < V; ++i) key[i] = key[i] == best ? 0u : key[i];
+      } else {
+        at = C;
 #pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = c0 + i == at ? 0u : key[i];
-      const float w = some ? expf(log_score<SCORE>(key_value(best)) - top) : 0.f;
-      chosen += w;
+        for (int i = V - 1; i >= 0; --i) at = key[i] == best ? c0 + i : at;
+        at = group_all<L>(at, OpMin());
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = c0 + i == at ? 0u : key[i];
+      }
 #pragma unroll
       for (int q = 0; q < KQ; ++q)
         if (j == q * L + li) {
-          mine[q] = w;
-          where[q] = some ? at : -1;
+          won[q] = best;
+          where[q] = at;
         }
     }
-    float mul = a.scale;
-    if (a.renorm) mul /= chosen;
-    else if constexpr (SCORE == MOE_SCORE_SOFTMAX) mul /= sum;
-    else mul *= expf(top);
+    // lane j's choice: its weight again from its logit, which the key holds
+    float mine[KQ], chosen = 0.f;
+#pragma unroll
+    for (int q = 0; q < KQ; ++q) {
+      uint32_t b = won[q];
+      if (kOne) b = b & 0x80000000u ? b & 0xFFFF0000u : b | 0xFFFFu;
+      mine[q] = won[q] ? sc_.weight(key_value(b)) : 0.f;
+      chosen += mine[q];
+    }
+    chosen = group_all<L>(chosen, OpAdd());
+    const float mul = a.renorm ? a.scale / chosen
+                      : SCORE == MOE_SCORE_SOFTMAX ? a.scale / sum : a.scale * sc_.elow;
 #pragma unroll
     for (int q = 0; q < KQ; ++q) {
       const int j = q * L + li;
       if (j >= a.k) continue;
-      ids[j] = where[q];
-      gates[j] = where[q] >= 0 ? mine[q] * mul : 0.f;
-      if (where[q] >= 0) atomicAdd(&sc[where[q]], 1);
+      ids[j] = won[q] ? where[q] : -1;
+      gates[j] = mine[q] * mul;
+      if (won[q]) atomicAdd(&sc[where[q]], 1);
     }
   }
   // the wave's groups, then the four waves, each in a fixed order
@@ -213,115 +260,124 @@ __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
     for (int o = L; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
     if ((tid & 63) < L) sp[tid >> 6][c0 + i] = s;
   }
-  if (li == 0) {
-    sz[g] = z;
-    sn[g] = n;
+  z = li == 0 ? z : 0.f;
+  n = li == 0 ? n : 0;
+  z = group_all<64>(z, OpAdd());
+  n = group_all<64>(n, OpAdd());
+  if ((tid & 63) == 0) {
+    red[0][tid >> 6] = z;
+    redn[tid >> 6] = n;
   }
   __syncthreads();
   const bool alone = gridDim.x == 1;
-  double dot = 0.0;
+  float dot = 0.f;
   for (int e = tid; e < a.E; e += kRouterThreads) {
     const float s = sp[0][e] + sp[1][e] + sp[2][e] + sp[3][e];
     const int c = sc[e];
     if (alone) {
       a.psum[e] = s;
       a.counts[e] = c;
-      dot += (double)c * s;
+      dot += (float)c * s;
     } else {
       a.part_p[(size_t)blockIdx.x * a.E + e] = s;
       a.part_c[(size_t)blockIdx.x * a.E + e] = c;
     }
   }
-  if (alone) {
-    for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, 64);
-    if ((tid & 63) == 0) sred[tid >> 6] = dot;
-    __syncthreads();
-  }
+  if (alone) dot = block_sum(dot, red[1], 4);
   if (tid == 0) {
-    double zs = 0.0;
-    int ns = 0;
-    for (int i = 0; i < G; ++i) {
-      zs += sz[i];
-      ns += sn[i];
-    }
+    const float zs = red[0][0] + red[0][1] + red[0][2] + red[0][3];
+    const int ns = redn[0] + redn[1] + redn[2] + redn[3];
     if (alone) {
       a.live[0] = ns;
-      a.losses[0] = (float)balance_of(sred[0] + sred[1] + sred[2] + sred[3], a.E, a.k, ns);
-      a.losses[1] = ns > 0 ? (float)(zs / ns) : 0.f;
+      a.losses[0] = balance_of(dot, a.E, a.k, ns);
+      a.losses[1] = ns > 0 ? zs / (float)ns : 0.f;
     } else {
-      a.part_z[blockIdx.x] = (float)zs;
+      a.part_z[blockIdx.x] = zs;
       a.part_n[blockIdx.x] = ns;
     }
   }
 }
 
-// Totals of the workgroups' partial sums, one workgroup: thread (q, e) adds
-// every Q-th partial of expert e, LDS joins the Q strands.
-constexpr int kTotalThreads = 1024;
+// Totals of the workgroups' partial sums.  A workgroup takes 16 experts, 64
+// strands of partials joined through LDS; the last one to finish joins their
+// products c_e prob_sum_e, in order, into the losses.
 __global__ __launch_bounds__(kTotalThreads) void k_router_totals(RouterArgs a) {
-  __shared__ float sp[kTotalThreads];
-  __shared__ int sc[kTotalThreads];
-  __shared__ double sd[kTotalThreads / 64];
-  __shared__ double sz[kTotalThreads / 64];
-  __shared__ int sn[kTotalThreads / 64];
-  const int tid = threadIdx.x, wide = min(a.E, kTotalThreads);
-  const int Q = kTotalThreads / wide, q = tid / wide, e = tid % wide;
+  constexpr int S = kTotalThreads / kTotalCols;
+  __shared__ float sp[S][kTotalCols];
+  __shared__ int sc[S][kTotalCols];
+  __shared__ float red[kTotalThreads / 64];
+  __shared__ int redn[kTotalThreads / 64];
+  __shared__ int last;
+  const int tid = threadIdx.x, col = tid % kTotalCols, q = tid / kTotalCols;
+  const int e = blockIdx.x * kTotalCols + col;
   float s = 0.f;
   int c = 0;
-  if (q < Q)
-    for (int b = q; b < a.parts; b += Q) {
+  if (e < a.E)
+    for (int b = q; b < a.parts; b += S) {
       s += a.part_p[(size_t)b * a.E + e];
       c += a.part_c[(size_t)b * a.E + e];
     }
-  sp[tid] = s;
-  sc[tid] = c;
-  double zs = 0.0;
-  int ns = 0;
+  sp[q][col] = s;
+  sc[q][col] = c;
+  __syncthreads();
+  if (tid < 64) {                                        // four lanes a column, 16 strands each
+    const int cc = tid >> 2, e4 = blockIdx.x * kTotalCols + cc;
+    s = 0.f;
+    c = 0;
+    for (int i = tid & 3; i < S; i += 4) {
+      s += sp[i][cc];
+      c += sc[i][cc];
+    }
+    s += dpp_of<0xB1>(s);
+    s += dpp_of<0x4E>(s);
+    c += dpp_of<0xB1>(c);
+    c += dpp_of<0x4E>(c);
+    const bool mine = e4 < a.E && (tid & 3) == 0;
+    if (mine) {
+      a.psum[e4] = s;
+      a.counts[e4] = c;
+    }
+    const float dot = group_all<64>(mine ? (float)c * s : 0.f, OpAdd());
+    if (tid == 0) {
+      __hip_atomic_store(a.dots + blockIdx.x, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+             (int)gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  float z = 0.f;
+  int n = 0;
   for (int b = tid; b < a.parts; b += kTotalThreads) {
-    zs += a.part_z[b];
-    ns += a.part_n[b];
+    z += a.part_z[b];
+    n += a.part_n[b];
   }
-  __syncthreads();
-  double dot = 0.0;
-  if (tid < wide) {
-    for (int i = 1; i < Q; ++i) {
-      s += sp[i * wide + e];
-      c += sc[i * wide + e];
+  n = group_all<64>(n, OpAdd());
+  if ((tid & 63) == 0) redn[tid >> 6] = n;
+  z = block_sum(z, red, kTotalThreads / 64);
+  if (tid < 64) {                                        // at most 1024 / 16 workgroups
+    const float mine = tid < (int)gridDim.x ? __hip_atomic_load(a.dots + tid, __ATOMIC_RELAXED,
+                                                                __HIP_MEMORY_SCOPE_AGENT) : 0.f;
+    const float dot = group_all<64>(mine, OpAdd());
+    if (tid == 0) {
+      n = 0;
+      for (int i = 0; i < kTotalThreads / 64; ++i) n += redn[i];
+      a.live[0] = n;
+      a.losses[0] = balance_of(dot, a.E, a.k, n);
+      a.losses[1] = n > 0 ? z / (float)n : 0.f;
     }
-    a.psum[e] = s;
-    a.counts[e] = c;
-    dot = (double)c * s;
-  }
-  for (int o = 32; o > 0; o >>= 1) {
-    dot += __shfl_xor(dot, o, 64);
-    zs += __shfl_xor(zs, o, 64);
-    ns += __shfl_xor(ns, o, 64);
-  }
-  if ((tid & 63) == 0) {
-    sd[tid >> 6] = dot;
-    sz[tid >> 6] = zs;
-    sn[tid >> 6] = ns;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    double d = 0.0, z = 0.0;
-    int n = 0;
-    for (int i = 0; i < kTotalThreads / 64; ++i) {
-      d += sd[i];
-      z += sz[i];
-      n += sn[i];
-    }
-    a.live[0] = n;
-    a.losses[0] = (float)balance_of(d, a.E, a.k, n);
-    a.losses[1] = n > 0 ? (float)(z / n) : 0.f;
   }
 }
 
-// Backward: the row's softmax again from its logits (they have to be read for
-// it in any case), every term in registers, one pass.
+// Backward: the row's scores again from its logits (they have to be read for
+// it in any case), every term in registers, one pass.  The k gate gradients
+// reach the lanes of their experts through LDS, a row's C places zeroed,
+// written and read by the row's own lanes (LDS keeps a wave's order).
 template <typename T, int L, int V, int SCORE>
 __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
-  constexpr int G = kRouterThreads / L;
+  constexpr int G = kRouterThreads / L, C = L * V;
+  __shared__ __attribute__((aligned(16))) float sh[G][C];
+  __shared__ __attribute__((aligned(16))) uint8_t sf[G][C];       // j + 1 of the choice
   const int tid = threadIdx.x, li = tid % L, g = tid / L, c0 = li * V;
   const int n = a.live_in[0];
   const float many = (float)max(n, 1);
@@ -333,72 +389,93 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
     ge[i] = c0 + i < a.E ? (float)a.counts_in[c0 + i] * (db * ((float)a.E / a.k) / many / many) : 0.f;
   const size_t step = (size_t)gridDim.x * G;
   for (size_t t = (size_t)blockIdx.x * G + g; t < (size_t)a.T; t += step) {
-    float v[V], p[V], d[V];
+    float v[V], w[V], away[V];
     const bool on = !a.mask || a.mask[t];
     load_logits<T, V>((const T*)a.logits + t * a.ld, c0, a.E, a.vec, on, v);
-    bool bad;
-    const bool live = row_live<L, V>(v, &bad);
+    // the choices: lane j's, and through LDS to the experts' lanes
+    float d[V], H = 0.f;
+    uint8_t flag[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      d[i] = 0.f;
+      flag[i] = 0;
+    }
+    __builtin_memcpy(&sh[g][c0], d, sizeof d);
+    __builtin_memcpy(&sf[g][c0], flag, sizeof flag);
+    __builtin_amdgcn_wave_barrier();
+    bool twice = false;
+    for (int j = li; j < a.k; j += L) {
+      const int id = a.ids_in[t * a.k + j];
+      if ((uint32_t)id < (uint32_t)a.E) {
+        const float h = a.dlogp ? a.dlogp[t * a.k + j] : 0.f;
+        H += h;
+        sh[g][id] = h;
+        sf[g][id] = (uint8_t)(j + 1);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    for (int j = li; j < a.k; j += L) {
+      const int id = a.ids_in[t * a.k + j];
+      if ((uint32_t)id < (uint32_t)a.E) twice |= sf[g][id] != (uint8_t)(j + 1);
+    }
+    if (__any(twice)) {                                  // an expert given twice: its gradients in order
+      if (li == 0) {
+        for (int j = 0; j < a.k; ++j) {
+          const int id = a.ids_in[t * a.k + j];
+          if ((uint32_t)id < (uint32_t)a.E) sh[g][id] = 0.f;
+        }
+        for (int j = 0; j < a.k; ++j) {
+          const int id = a.ids_in[t * a.k + j];
+          if ((uint32_t)id < (uint32_t)a.E && a.dlogp) sh[g][id] += a.dlogp[t * a.k + j];
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    __builtin_memcpy(d, &sh[g][c0], sizeof d);
+    __builtin_memcpy(flag, &sf[g][c0], sizeof flag);
+    __builtin_amdgcn_wave_barrier();
+    H = group_all<L>(H, OpAdd());
+
+    Score<SCORE> sc;
+    sc.at_top(row_top<L, V>(v));
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[i] = sc.weight(v[i], &away[i]);
+      sum += w[i];
+    }
+    sum = group_all<L>(sum, OpAdd());
     T* out = (T*)a.dlogits + t * a.ld_out;
     T o[V];
-    if (live) {                                          // the whole group
-      float top, sum, ltop, lsum, share[V];
-      if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-        row_softmax<L, V>(v, p, &top, &sum);
-        ltop = top;
-        lsum = sum;
-      } else {
-        row_softmax<L, V>(v, share, &ltop, &lsum);
-        float s[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = log_score<SCORE>(v[i]);
-        row_softmax<L, V>(s, p, &top, &sum);
-      }
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = 0.f;
-      float H = 0.f, Q = 0.f, pg = 0.f;
-      uint32_t chosen[(V + 31) / 32];
-#pragma unroll
-      for (int i = 0; i < (V + 31) / 32; ++i) chosen[i] = 0;
-      for (int j0 = 0; j0 < a.k; j0 += L) {
-        int id = -1;
-        float h = 0.f;
-        if (j0 + li < a.k) {
-          id = a.ids_in[t * a.k + j0 + li];
-          if ((uint32_t)id >= (uint32_t)a.E) id = -1;
-          if (id >= 0 && a.dlogp) h = a.dlogp[t * a.k + j0 + li];
-        }
-        H += h;
-        for (int j = 0; j < min(L, a.k - j0); ++j) {
-          const int src = (tid & 63 & ~(L - 1)) + j;
-          const int ij = __shfl(id, src, 64);
-          const float hj = __shfl(h, src, 64);
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (ij == c0 + i) {
-              d[i] += hj;
-              chosen[i / 32] |= 1u << (i % 32);
-            }
-        }
-      }
-      H = group_all<L>(H, OpAdd());
+    if (row_live(sc.top, sum)) {                         // the whole group
+      const float inv = inverse(sum);
+      float Q = 0.f, pg = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        Q += chosen[i / 32] >> (i % 32) & 1 ? p[i] : 0.f;
-        pg += p[i] * ge[i];
+        w[i] *= inv;                                     // P
+        Q += flag[i] ? w[i] : 0.f;
+        pg += w[i] * ge[i];
       }
       Q = group_all<L>(Q, OpAdd());
       pg = group_all<L>(pg, OpAdd());
       const float hq = a.renorm ? (Q > 0.f ? H / Q : 0.f)
                                 : (SCORE == MOE_SCORE_SOFTMAX ? H : 0.f);
-      const float zs = zmul * (ltop + logf(lsum));
+      const float rest = a.renorm ? 0.f : hq;            // of the experts not chosen
+      float zs = 0.f, lsum = sum, e[V];
+      if (zmul != 0.f) {
+        if constexpr (SCORE == MOE_SCORE_SIGMOID) lsum = row_exp_sum<L, V>(v, sc.top, e);
+        zs = zmul * (sc.top + logf(lsum));
+        if constexpr (SCORE == MOE_SCORE_SIGMOID) zs *= inverse(lsum);
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const bool take = !a.renorm || (chosen[i / 32] >> (i % 32) & 1);
-        float x = d[i] - (take ? p[i] * hq : 0.f) + p[i] * (ge[i] - pg);
-        if constexpr (SCORE == MOE_SCORE_SIGMOID)        // d log sigmoid(l) / dl = sigmoid(-l)
-          x = x * (expf(-fmaxf(v[i], 0.f)) / (1.f + expf(-fabsf(v[i])))) + zs * share[i];
-        else
-          x += zs * p[i];
+        float x = d[i] + w[i] * (ge[i] - pg - (flag[i] ? hq : rest));
+        if constexpr (SCORE == MOE_SCORE_SIGMOID) {
+          x *= away[i];
+          if (zmul != 0.f) x += zs * e[i];
+        } else {
+          x += zs * w[i];
+        }
         elem_set(o[i], x);
       }
     } else {
@@ -455,7 +532,7 @@ static int router_grid(int T, int E) {
 
 size_t router_ws_bytes(int T, int E) {
   const size_t wg = (size_t)router_grid(T, E);
-  return align_up(wg * E * 4) * 2 + align_up(wg * 4) * 2;
+  return align_up(wg * E * 4) * 2 + align_up(wg * 4) * 2 + 2 * align_up(64 * 4);
 }
 
 template <template <typename, int, int, int> class K, typename T, int SCORE>
@@ -504,10 +581,12 @@ int launch_router(const moe_router& R, const void* logits, int ld, const uint8_t
   a.part_c = (int32_t*)(w += align_up((size_t)grid * R.E * 4));
   a.part_z = (float*)(w += align_up((size_t)grid * R.E * 4));
   a.part_n = (int32_t*)(w += align_up((size_t)grid * 4));
+  a.dots = (float*)(w += align_up((size_t)grid * 4));
+  a.done = (int32_t*)(w += align_up(64 * 4));
   a.parts = grid;
   router_kind<FwdK>(R, a, grid, st);
   if (grid > 1)
-    hipLaunchKernelGGL(k_router_totals, dim3(1), dim3(kTotalThreads), 0, st, a);
+    hipLaunchKernelGGL(k_router_totals, dim3((R.E + kTotalCols - 1) / kTotalCols), dim3(kTotalThreads), 0, st, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
