@@ -129,14 +129,17 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(NormArgs a) {
   }
 }
 
-// Backward: threads keep their columns' sums over the rows of a workgroup in
-// registers (dw, and FEAT: the gate's); the workgroups' sums are joined by
-// k_norm_cols, so the order of every sum is fixed by the grid.
+// Backward.  A workgroup of 16 waves holds 1024 / NT rows at a time (one where NT is 1024);
+// threads keep their columns' sums over the rows in registers (dw, and FEAT: the gate's), joined over
+// the rows' groups at the end and over the workgroups by k_norm_cols, so the order of every sum is
+// fixed by the grid.  A row's loads are issued before the sum of the row before it is joined.
+constexpr int kNormWG = 1024;
 template <typename T, int VE, int NT, int KC, bool OUT, bool FEAT>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_bwd(NormArgs a) {
-  constexpr int RPW = NT < 256 ? 256 / NT : 1;
-  __shared__ float red[2][16];
-  __shared__ float join[RPW > 1 ? RPW : 1][RPW > 1 ? NT * VE : 1];
+__global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
+  constexpr int RPW = kNormWG / NT, NW = NT / 64;
+  constexpr int IN = OUT ? 2 : 4;                        // row operands: x, go and (before) gr, u
+  __shared__ float red[2][RPW][16];
+  __shared__ __attribute__((aligned(16))) float join[RPW > 1 ? kNormWG * VE : 1];
   const int li = threadIdx.x % NT, rg = threadIdx.x / NT;
   float dw[KC][VE], dg[FEAT ? KC : 1][VE];
 #pragma unroll
@@ -146,81 +149,121 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_bwd(NormArgs a) {
       dw[q][i] = 0.f;
       if constexpr (FEAT) dg[q][i] = 0.f;
     }
-  int turn = 0;
   const size_t step = (size_t)gridDim.x * RPW;
-  for (size_t t = (size_t)blockIdx.x * RPW + rg; t < (size_t)a.T; t += step) {
-    const float g_row = a.alpha * (a.kind == MOE_GATE_TOKEN ? a.gate[t] : 1.f);
-    const float rstd = a.rstd[t];
-    const T* x = (const T*)a.x + t * a.ldx;
-    const T* go = (const T*)a.go + t * a.ldgo;
+  T cur[KC][IN][VE];
+  float rstd = 0.f, g_row = a.alpha;
+  auto fetch = [&](size_t t, T (*to)[IN][VE], float* rs, float* gr_) {
+    if (t >= (size_t)a.T) return;
+    *rs = a.rstd[t];
+    if (a.kind == MOE_GATE_TOKEN) *gr_ = a.alpha * a.gate[t];
+#pragma unroll
+    for (int q = 0; q < KC; ++q) {
+      const int c = (li + q * NT) * VE;
+      if (c >= a.d) continue;
+      load_n<T, VE, (VE > 1)>((const T*)a.x + t * a.ldx + c, to[q][0]);
+      load_n<T, VE, (VE > 1)>((const T*)a.go + t * a.ldgo + c, to[q][1]);
+      if constexpr (!OUT) {
+        if (a.gr) load_n<T, VE, (VE > 1)>((const T*)a.gr + t * a.ldgr + c, to[q][2]);
+        if (a.u) load_n<T, VE, (VE > 1)>((const T*)a.u + t * a.ldu + c, to[q][3]);
+      }
+    }
+  };
+  int turn = 0;
+  // one barrier: the next sum goes to the other buffer
+  auto row_join = [&](float s) {
+    s = group_all<64>(s, OpAdd());
+    if constexpr (NW > 1) {
+      float* r = red[turn & 1][rg];
+      ++turn;
+      if ((threadIdx.x & 63) == 0) r[(threadIdx.x % NT) >> 6] = s;
+      __syncthreads();
+      s = 0.f;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) s += r[i];
+    }
+    return s;
+  };
+  fetch((size_t)blockIdx.x * RPW + rg, cur, &rstd, &g_row);
+  for (size_t t0 = (size_t)blockIdx.x * RPW; t0 < (size_t)a.T; t0 += step) {
+    const size_t t = t0 + rg;
+    const bool on = t < (size_t)a.T;
     float xh[KC][VE], p[KC][VE];       // x / rms, and the gradient of that
     float s = 0.f;
+    if (on) {
 #pragma unroll
-    for (int q = 0; q < KC; ++q) {
-      const int c = (li + q * NT) * VE;
-      if (c >= a.d) continue;
-      float o[VE], w[VE];
-      load_f<T, VE>(x + c, xh[q]);
-      load_f<T, VE>(go + c, o);
-      load_w<T, VE>(a, c, w);
-      float g[VE];
-      if constexpr (OUT) load_g<VE>(a, c, g_row, g);
+      for (int q = 0; q < KC; ++q) {
+        const int c = (li + q * NT) * VE;
+        if (c >= a.d) continue;
+        float w[VE], g[VE];
+        load_w<T, VE>(a, c, w);
+        if constexpr (OUT) load_g<VE>(a, c, g_row, g);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        xh[q][i] *= rstd;
-        float dv = o[i];
-        if constexpr (OUT) {
-          dv *= g[i];
-          if constexpr (FEAT) dg[q][i] += o[i] * (w[i] * xh[q][i]);
+        for (int i = 0; i < VE; ++i) {
+          const float o = elem_f(cur[q][1][i]);
+          xh[q][i] = elem_f(cur[q][0][i]) * rstd;
+          float dv = o;
+          if constexpr (OUT) {
+            dv *= g[i];
+            if constexpr (FEAT) dg[q][i] += o * (w[i] * xh[q][i]);
+          }
+          dw[q][i] += dv * xh[q][i];
+          p[q][i] = dv * w[i];
+          // after the block, a token's gate: the sum without it, which is also its gradient
+          s += (OUT && !FEAT ? o * w[i] : p[q][i]) * xh[q][i];
         }
-        dw[q][i] += dv * xh[q][i];
-        p[q][i] = dv * w[i];
-        // after the block, a token's gate: the sum without it, which is also its gradient
-        s += (OUT && !FEAT ? o[i] * w[i] : p[q][i]) * xh[q][i];
       }
     }
-    s = row_sum<NT>(s, red, turn++);
+    const float rs = rstd, gr_ = g_row;
+    T own[OUT ? 1 : KC][2][VE];                          // gr and u of this row
+    if constexpr (!OUT) {
+#pragma unroll
+      for (int q = 0; q < KC; ++q)
+#pragma unroll
+        for (int i = 0; i < VE; ++i) {
+          own[q][0][i] = cur[q][2][i];
+          own[q][1][i] = cur[q][3][i];
+        }
+    }
+    fetch(t + step, cur, &rstd, &g_row);
+    s = row_join(s);
     if constexpr (OUT && !FEAT) {
-      if (a.kind == MOE_GATE_TOKEN && li == 0) a.dgate[t] = a.alpha * s;
-      s *= g_row;
+      if (on && a.kind == MOE_GATE_TOKEN && li == 0) a.dgate[t] = a.alpha * s;
+      s *= gr_;
     }
     const float mean = s * a.inv_d;
-    const T* gr = (const T*)a.gr + t * a.ldgr;
-    const T* u = (const T*)a.u + t * a.ldu;
     float b = 0.f;
+    if (on) {
 #pragma unroll
-    for (int q = 0; q < KC; ++q) {
-      const int c = (li + q * NT) * VE;
-      if (c >= a.d) continue;
-      float dx[VE];
+      for (int q = 0; q < KC; ++q) {
+        const int c = (li + q * NT) * VE;
+        if (c >= a.d) continue;
+        float dx[VE];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) dx[i] = rstd * (p[q][i] - xh[q][i] * mean);
-      if constexpr (!OUT) {
-        if (a.gr) {
-          float more[VE];
-          load_f<T, VE>(gr + c, more);
+        for (int i = 0; i < VE; ++i) dx[i] = rs * (p[q][i] - xh[q][i] * mean);
+        if constexpr (!OUT) {
+          if (a.gr) {
 #pragma unroll
-          for (int i = 0; i < VE; ++i) dx[i] += more[i];
-        }
-        if (a.u) {
-          float uu[VE], g[VE], du[VE];
-          load_f<T, VE>(u + c, uu);
-          load_g<VE>(a, c, g_row, g);
-#pragma unroll
-          for (int i = 0; i < VE; ++i) {
-            du[i] = g[i] * dx[i];
-            if constexpr (FEAT) dg[q][i] += uu[i] * dx[i];
-            else b += uu[i] * dx[i];
+            for (int i = 0; i < VE; ++i) dx[i] += elem_f(own[q][0][i]);
           }
-          store_f<T, VE>((T*)a.r + t * a.ldr + c, du);
+          if (a.u) {
+            float g[VE], du[VE];
+            load_g<VE>(a, c, gr_, g);
+#pragma unroll
+            for (int i = 0; i < VE; ++i) {
+              du[i] = g[i] * dx[i];
+              if constexpr (FEAT) dg[q][i] += elem_f(own[q][1][i]) * dx[i];
+              else b += elem_f(own[q][1][i]) * dx[i];
+            }
+            store_f<T, VE>((T*)a.r + t * a.ldr + c, du);
+          }
         }
+        store_f<T, VE>((T*)a.n + t * a.ldn + c, dx);
       }
-      store_f<T, VE>((T*)a.n + t * a.ldn + c, dx);
     }
     if constexpr (!OUT && !FEAT)
       if (a.kind == MOE_GATE_TOKEN) {
-        b = row_sum<NT>(b, red, turn++);
-        if (li == 0) a.dgate[t] = a.alpha * b;
+        b = row_join(b);
+        if (on && li == 0) a.dgate[t] = a.alpha * b;
       }
   }
   const bool alone = gridDim.x == 1;
@@ -235,15 +278,14 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm_bwd(NormArgs a) {
       if constexpr (RPW > 1) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < VE; ++i) join[rg][li * VE + i] = sum[i];
+        for (int i = 0; i < VE; ++i) join[(rg * VE + i) * NT + li] = sum[i];
         __syncthreads();
+        if (rg) continue;
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
           sum[i] = 0.f;
-#pragma unroll
-          for (int o = 0; o < RPW; ++o) sum[i] += join[o][li * VE + i];
+          for (int o = 0; o < RPW; ++o) sum[i] += join[(o * VE + i) * NT + li];
         }
-        if (rg) continue;
       }
       if (c >= a.d) continue;
       float* to = (h ? a.part_g : a.part_w) + (size_t)blockIdx.x * a.d + c;
@@ -264,6 +306,7 @@ __global__ __launch_bounds__(1024) void k_norm_cols(const float* __restrict__ pa
   const float* part = blockIdx.y ? part_g : part_w;
   float s = 0.f;
   if (c < d)
+#pragma unroll 8
     for (int b = strand; b < parts; b += 16) s += part[(size_t)b * d + c];
   red[strand][lane] = s;
   __syncthreads();
@@ -295,12 +338,19 @@ static bool aligned16(const void* p, size_t ld_bytes) {
 // F::go<T, VE, NT, KC>(args...): by how many pieces of VE elements a row has
 template <class F, typename T, int VE, typename... A> static void norm_shape(int d, A&&... args) {
   const int pieces = (d + VE - 1) / VE;
-  if (pieces <= 64) F::template go<T, VE, 64, 1>(args...);
+  if constexpr (F::kOnePiece) {                          // threads for a row before pieces for a thread
+    if (pieces <= 64) return F::template go<T, VE, 64, 1>(args...);
+    if (pieces <= 128) return F::template go<T, VE, 128, 1>(args...);
+    if (pieces <= 256) return F::template go<T, VE, 256, 1>(args...);
+    if (pieces <= 512) return F::template go<T, VE, 512, 1>(args...);
+    if (pieces <= 1024) return F::template go<T, VE, 1024, 1>(args...);
+  } else if (pieces <= 64) F::template go<T, VE, 64, 1>(args...);
   else if (pieces <= 128) F::template go<T, VE, 64, 2>(args...);
   else if (pieces <= 256) F::template go<T, VE, 64, 4>(args...);
   else if (pieces <= 512) F::template go<T, VE, 256, 2>(args...);
   else if (pieces <= 1024) F::template go<T, VE, 256, 4>(args...);
-  else if (pieces <= 2048) F::template go<T, VE, 1024, 2>(args...);
+  if (pieces <= 1024) return;
+  if (pieces <= 2048) F::template go<T, VE, 1024, 2>(args...);
   else if constexpr (VE < 8) {                           // 8 elements: d ends at 2048 pieces
     if (pieces <= 4096) F::template go<T, VE, 1024, 4>(args...);
     else if constexpr (VE == 1) F::template go<T, VE, 1024, 16>(args...);
@@ -317,6 +367,7 @@ template <class F, typename... A> static void norm_kind(int dtype, bool vec, int
 }
 
 struct NormFwd {
+  static constexpr bool kOnePiece = false;
   template <typename T, int VE, int NT, int KC>
   static void go(const NormArgs& a, bool out, hipStream_t st) {
     constexpr int RPW = NT < 256 ? 256 / NT : 1, WG = NT < 256 ? 256 : NT;
@@ -327,9 +378,10 @@ struct NormFwd {
 };
 
 struct NormBwd {
+  static constexpr bool kOnePiece = true;
   template <typename T, int VE, int NT, int KC>
   static void go(NormArgs& a, bool out, float* dw, float* dgate, hipStream_t st) {
-    constexpr int RPW = NT < 256 ? 256 / NT : 1, WG = NT < 256 ? 256 : NT;
+    constexpr int RPW = kNormWG / NT, WG = kNormWG;
     const int parts = norm_grid(a.T, RPW);
     const bool feat = a.kind == MOE_GATE_FEATURE;
     float* pw = a.part_w;
