@@ -24,7 +24,7 @@ struct AdamTensor {
   float* ms;
   float* vs;
   int64_t n;
-  int p32, g32, vec, pad;
+  int p32, g32;
 };
 struct AdamTable { AdamTensor* t; uint32_t* first; };
 static AdamTable adamw_table(const void* ws, int tensors) {
@@ -72,31 +72,14 @@ MOE_DEV uint32_t mix(uint32_t x) {
   return x ^ (x >> 15);
 }
 
-// Eight elements at p; with FULL there are eight and p is aligned for them, else n (at most eight,
-// zeros past them) are read one by one.
+// Eight elements at p, with FULL all eight, else n (at most eight, zeros past them).
 template <typename T, bool FULL> MOE_DEV void load8(const T* p, int n, T* v) {
-  if constexpr (FULL && sizeof(T) == 1) {
-    const u32x2_t w = *(const MOE_GLB u32x2_t*)p;
-    __builtin_memcpy(v, &w, 8);
-  } else if constexpr (FULL) {
-    load_n<T, 8, true>(p, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? *(const MOE_GLB T*)(p + i) : (T)0;
-  }
+  if constexpr (FULL) load_n<T, 8>(p, v);
+  else load_upto<T, 8>(p, n, v);
 }
 template <typename T, bool FULL> MOE_DEV void store8(T* p, int n, const T* v) {
-  if constexpr (FULL && sizeof(T) == 1) {
-    u32x2_t w;
-    __builtin_memcpy(&w, v, 8);
-    *(MOE_GLB u32x2_t*)p = w;
-  } else if constexpr (FULL) {
-    store_n<T, 8, true>(p, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) *(MOE_GLB T*)(p + i) = v[i];
-  }
+  if constexpr (FULL) store_n<T, 8>(p, v);
+  else store_upto<T, 8>(p, n, v);
 }
 template <bool FULL> MOE_DEV void load8f(const void* p, bool f32, int64_t at, int n, float* v) {
   if (f32) {
@@ -329,7 +312,7 @@ __global__ __launch_bounds__(kAdamThreads, 4) void k_adamw(AdamArgs a) {
   for (int pass = 0; pass < a.item; pass += kAdamPass) {
     const int64_t at = (int64_t)(item - a.first[j]) * a.item + pass + tid * 8;
     const int64_t left = t.n - at, block = t.n - (at & ~(int64_t)(MOE_ADAMW_BLOCK - 1));
-    if (t.vec && block >= MOE_ADAMW_BLOCK)
+    if (block >= MOE_ADAMW_BLOCK)
       adam8<BITS, true>(a, t, h, key, at, 8);
     else if (block > 0)
       adam8<BITS, false>(a, t, h, key, at, left >= 8 ? 8 : left > 0 ? (int)left : 0);
@@ -358,11 +341,6 @@ int launch_adamw_table(const moe_adamw_tensor* t, int count, moe_adamw_list* out
       d.p = s.p; d.master = s.master; d.g = s.g; d.m = s.m; d.v = s.v;
       d.ms = s.m_scale; d.vs = s.v_scale; d.n = s.n;
       d.p32 = s.p_dtype == MOE_F32; d.g32 = s.g_dtype == MOE_F32;
-      // 16-byte pieces; codes come 8 bytes at a time
-      const uintptr_t all = (uintptr_t)s.p | (uintptr_t)s.g | (uintptr_t)s.master |
-                            (bits == 8 ? ((uintptr_t)s.m | (uintptr_t)s.v) << 1
-                                       : (uintptr_t)s.m | (uintptr_t)s.v);
-      d.vec = (all & 15u) == 0;
       part.first[i] = total;
       total += (uint32_t)((s.n + out->item - 1) / out->item);
     }

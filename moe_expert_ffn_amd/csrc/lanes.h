@@ -45,34 +45,86 @@ MOE_DEV float elem_f(float f) { return f; }
 MOE_DEV void elem_set(uint16_t& o, float f) { o = f2bf(f); }
 MOE_DEV void elem_set(float& o, float f) { o = f; }
 
-// N consecutive elements: 16-byte accesses where VEC (p 16-byte aligned, N * size a multiple of
-// 16), else one by one.
-template <typename T, int N, bool VEC> MOE_DEV void load_n(const T* p, T* v) {
-  if constexpr (VEC) {
-    constexpr int PER = 16 / sizeof(T);
-    static_assert(N % PER == 0, "whole 16-byte pieces");
-#pragma unroll
-    for (int i = 0; i < N / PER; ++i) {
-      const u32x4_t w = *(const MOE_GLB u32x4_t*)(p + i * PER);
-      __builtin_memcpy(v + i * PER, &w, 16);
-    }
+// N consecutive elements in 16-byte (8-byte) pieces.  Global memory takes such accesses at any
+// element's address, so rows of any stride and views of any offset go the same way.
+typedef u32x4_t u32x4_any_t __attribute__((aligned(1)));
+typedef u32x2_t u32x2_any_t __attribute__((aligned(1)));
+template <typename T, int N> MOE_DEV void load_n(const T* p, T* v) {
+  constexpr int BYTES = N * sizeof(T);
+  static_assert(BYTES % 16 == 0 || BYTES == 8, "whole pieces");
+  if constexpr (BYTES == 8) {
+    const u32x2_t w = *(const MOE_GLB u32x2_any_t*)p;
+    __builtin_memcpy(v, &w, 8);
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = *(const MOE_GLB T*)(p + i);
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const u32x4_t w = *(const MOE_GLB u32x4_any_t*)((const char*)p + 16 * i);
+      __builtin_memcpy((char*)v + 16 * i, &w, 16);
+    }
   }
 }
-template <typename T, int N, bool VEC> MOE_DEV void store_n(T* p, const T* v) {
-  if constexpr (VEC) {
-    constexpr int PER = 16 / sizeof(T);
-#pragma unroll
-    for (int i = 0; i < N / PER; ++i) {
-      u32x4_t w;
-      __builtin_memcpy(&w, v + i * PER, 16);
-      *(MOE_GLB u32x4_t*)(p + i * PER) = w;
-    }
+template <typename T, int N> MOE_DEV void store_n(T* p, const T* v) {
+  constexpr int BYTES = N * sizeof(T);
+  if constexpr (BYTES == 8) {
+    u32x2_t w;
+    __builtin_memcpy(&w, v, 8);
+    *(MOE_GLB u32x2_any_t*)p = w;
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) *(MOE_GLB T*)(p + i) = v[i];
+    for (int i = 0; i < BYTES / 16; ++i) {
+      u32x4_t w;
+      __builtin_memcpy(&w, (const char*)v + 16 * i, 16);
+      *(MOE_GLB u32x4_any_t*)((char*)p + 16 * i) = w;
+    }
+  }
+}
+// Piece c (its first element) of a row of d elements: N of them, or where the row ends inside the
+// piece, after settle_piece, the rest of the row and zeros.  The load itself has no branch on the
+// lane: a short piece reads the row's last N elements, and settle_piece moves them down once they
+// are used.  (With the short piece loaded one by one in a branch, every further load waited for it:
+// 8192 x 2047 took a third longer than 8192 x 2048.)
+template <typename T, int N> MOE_DEV void load_piece(const T* row, int c, int d, T* v) {
+  if (d >= N) {                                          // the whole launch
+    load_n<T, N>(row + min(c, d - N), v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = c + i < d ? *(const MOE_GLB T*)(row + c + i) : (T)0;
+  }
+}
+template <typename T, int N> MOE_DEV void settle_piece(int c, int d, T* v) {
+  constexpr int W = N * sizeof(T) / 4;
+  if (c + N <= d || d < N) return;
+  uint32_t w[W];
+  __builtin_memcpy(w, v, sizeof w);
+  const int bytes = min(c + N - d, N) * (int)sizeof(T);  // N: the piece lies behind the row
+#pragma unroll
+  for (int s = W; s > 0; s >>= 1)
+#pragma unroll
+    for (int i = 0; i < W; ++i) {                        // ascending: w[i + s] is still the old one
+      const uint32_t far = i + s < W ? w[i + s] : 0u;
+      w[i] = bytes & 4 * s ? far : w[i];
+    }
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t next = i + 1 < W ? w[i + 1] : 0u;
+      w[i] = bytes & 2 ? w[i] >> 16 | next << 16 : w[i];
+    }
+  }
+  __builtin_memcpy(v, w, sizeof w);
+}
+// The first n elements at p, zeros past those.
+template <typename T, int N> MOE_DEV void load_upto(const T* p, int n, T* v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = i < n ? *(const MOE_GLB T*)(p + i) : (T)0;
+}
+template <typename T, int N> MOE_DEV void store_upto(T* p, int n, const T* v) {
+  if (n >= N) {
+    store_n<T, N>(p, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) *(MOE_GLB T*)(p + i) = v[i];
   }
 }
 

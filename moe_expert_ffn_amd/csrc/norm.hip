@@ -27,38 +27,40 @@ struct NormArgs {
   float alpha, eps, inv_d;
 };
 
-template <typename T, int VE> MOE_DEV void load_f(const T* p, float* v) {
-  T raw[VE];
-  load_n<T, VE, (VE > 1)>(p, raw);
+template <typename T, int VE> MOE_DEV void settle_f(int c, int d, T* raw, float* v) {
+  settle_piece<T, VE>(c, d, raw);
 #pragma unroll
   for (int i = 0; i < VE; ++i) v[i] = elem_f(raw[i]);
 }
-template <typename T, int VE> MOE_DEV void store_f(T* p, const float* v) {
+template <typename T, int VE> MOE_DEV void load_f(const T* row, int c, int d, float* v) {
+  T raw[VE];
+  load_piece<T, VE>(row, c, d, raw);
+  settle_f<T, VE>(c, d, raw, v);
+}
+template <typename T, int VE> MOE_DEV void store_f(T* row, int c, int d, const float* v) {
   T raw[VE];
 #pragma unroll
   for (int i = 0; i < VE; ++i) elem_set(raw[i], v[i]);
-  store_n<T, VE, (VE > 1)>(p, raw);
+  store_upto<T, VE>(row + c, d - c, raw);
 }
 template <typename T, int VE> MOE_DEV void load_w(const NormArgs& a, int c, float* v) {
-  if (a.w32) load_f<float, VE>((const float*)a.w + c, v);
-  else load_f<T, VE>((const T*)a.w + c, v);
+  if (a.w32) load_f<float, VE>((const float*)a.w, c, a.d, v);
+  else load_f<T, VE>((const T*)a.w, c, a.d, v);
 }
-// alpha g for the columns from c on: g_row holds alpha (times the token's gate)
-template <int VE> MOE_DEV void load_g(const NormArgs& a, int c, float g_row, float* v) {
+// the gate of the columns from c on (1 where it is not the features')
+template <int VE> MOE_DEV void load_g(const NormArgs& a, int c, float* v) {
   if (a.kind == MOE_GATE_FEATURE) {
-    load_f<float, VE>(a.gate + c, v);
-#pragma unroll
-    for (int i = 0; i < VE; ++i) v[i] *= g_row;
+    load_f<float, VE>(a.gate, c, a.d, v);
   } else {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) v[i] = g_row;
+    for (int i = 0; i < VE; ++i) v[i] = 1.f;
   }
 }
 
 // Sum over the NT threads of a row.  More than a wave: through LDS, `red` two
 // buffers used in turn, so one barrier per sum is enough.
 template <int NT> MOE_DEV float row_sum(float s, float (*red)[16], int turn) {
-  s = group_all<64>(s, OpAdd());
+  s = group_all<(NT < 64 ? NT : 64)>(s, OpAdd());
   if constexpr (NT > 64) {
     float* r = red[turn & 1];
     if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = s;
@@ -82,25 +84,32 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(NormArgs a) {
   const float g_row = a.alpha * (a.kind == MOE_GATE_TOKEN ? a.gate[t] : 1.f);
   const T* x = (const T*)a.x + t * a.ldx;
   const T* u = (const T*)a.u + t * a.ldu;
+  // before the block: x and u make v; after: v is u, x is added at the end
+  T rx[KC][VE], ru[KC][VE];
+#pragma unroll
+  for (int q = 0; q < KC; ++q) {
+    const int c = (li + q * NT) * VE;
+    if (c >= a.d) continue;
+    load_piece<T, VE>(x, c, a.d, rx[q]);
+    if (OUT || a.u) load_piece<T, VE>(u, c, a.d, ru[q]);
+  }
   float v[KC][VE], xs[OUT ? KC : 1][VE];
   float s = 0.f;
 #pragma unroll
   for (int q = 0; q < KC; ++q) {
     const int c = (li + q * NT) * VE;
-#pragma unroll
-    for (int i = 0; i < VE; ++i) v[q][i] = 0.f;
     if (c >= a.d) continue;
     if constexpr (OUT) {
-      load_f<T, VE>(u + c, v[q]);
-      load_f<T, VE>(x + c, xs[q]);
+      settle_f<T, VE>(c, a.d, ru[q], v[q]);
+      settle_f<T, VE>(c, a.d, rx[q], xs[q]);
     } else {
-      load_f<T, VE>(x + c, v[q]);
+      settle_f<T, VE>(c, a.d, rx[q], v[q]);
       if (a.u) {
         float uu[VE], g[VE];
-        load_f<T, VE>(u + c, uu);
-        load_g<VE>(a, c, g_row, g);
+        settle_f<T, VE>(c, a.d, ru[q], uu);
+        load_g<VE>(a, c, g);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) v[q][i] += g[i] * uu[i];
+        for (int i = 0; i < VE; ++i) v[q][i] += g[i] * g_row * uu[i];
       }
     }
 #pragma unroll
@@ -117,15 +126,15 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(NormArgs a) {
     load_w<T, VE>(a, c, w);
     if constexpr (OUT) {
       float g[VE];
-      load_g<VE>(a, c, g_row, g);
+      load_g<VE>(a, c, g);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) o[i] = xs[q][i] + g[i] * (v[q][i] * rstd * w[i]);
+      for (int i = 0; i < VE; ++i) o[i] = xs[q][i] + g[i] * g_row * (v[q][i] * rstd * w[i]);
     } else {
-      if (a.r) store_f<T, VE>((T*)a.r + t * a.ldr + c, v[q]);
+      if (a.r) store_f<T, VE>((T*)a.r + t * a.ldr, c, a.d, v[q]);
 #pragma unroll
       for (int i = 0; i < VE; ++i) o[i] = v[q][i] * rstd * w[i];
     }
-    store_f<T, VE>((T*)a.n + t * a.ldn + c, o);
+    store_f<T, VE>((T*)a.n + t * a.ldn, c, a.d, o);
   }
 }
 
@@ -136,10 +145,11 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(NormArgs a) {
 constexpr int kNormWG = 1024;
 template <typename T, int VE, int NT, int KC, bool OUT, bool FEAT>
 __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
-  constexpr int RPW = kNormWG / NT, NW = NT / 64;
+  constexpr int RPW = kNormWG / NT, NW = NT / 64;        // NW 0: several rows a wave
+  constexpr int J = NT < 64 ? kNormWG / 64 : RPW;        // strands joined through LDS
   constexpr int IN = OUT ? 2 : 4;                        // row operands: x, go and (before) gr, u
-  __shared__ float red[2][RPW][16];
-  __shared__ __attribute__((aligned(16))) float join[RPW > 1 ? kNormWG * VE : 1];
+  __shared__ float red[2][NW > 1 ? RPW : 1][16];
+  __shared__ float join[J > 1 ? J * VE * NT : 1];
   const int li = threadIdx.x % NT, rg = threadIdx.x / NT;
   float dw[KC][VE], dg[FEAT ? KC : 1][VE];
 #pragma unroll
@@ -149,6 +159,31 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
       dw[q][i] = 0.f;
       if constexpr (FEAT) dg[q][i] = 0.f;
     }
+  float ws[VE], gs[VE];                                  // one piece: w and the gate stay
+  if constexpr (KC == 1) {
+#pragma unroll
+    for (int i = 0; i < VE; ++i) ws[i] = gs[i] = 0.f;
+    if (li * VE < a.d) {
+      load_w<T, VE>(a, li * VE, ws);
+      if constexpr (FEAT) load_g<VE>(a, li * VE, gs);
+    }
+  }
+  auto w_of = [&](int c, float* w) {
+    if constexpr (KC == 1) __builtin_memcpy(w, ws, sizeof ws);
+    else load_w<T, VE>(a, c, w);
+  };
+  // alpha times the gate; g_row: alpha (times the token's)
+  auto g_of = [&](int c, float g_row, float* g) {
+    if constexpr (!FEAT) {
+#pragma unroll
+      for (int i = 0; i < VE; ++i) g[i] = g_row;
+    } else {
+      if constexpr (KC == 1) __builtin_memcpy(g, gs, sizeof gs);
+      else load_g<VE>(a, c, g);
+#pragma unroll
+      for (int i = 0; i < VE; ++i) g[i] *= g_row;
+    }
+  };
   const size_t step = (size_t)gridDim.x * RPW;
   T cur[KC][IN][VE];
   float rstd = 0.f, g_row = a.alpha;
@@ -160,18 +195,18 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
     for (int q = 0; q < KC; ++q) {
       const int c = (li + q * NT) * VE;
       if (c >= a.d) continue;
-      load_n<T, VE, (VE > 1)>((const T*)a.x + t * a.ldx + c, to[q][0]);
-      load_n<T, VE, (VE > 1)>((const T*)a.go + t * a.ldgo + c, to[q][1]);
+      load_piece<T, VE>((const T*)a.x + t * a.ldx, c, a.d, to[q][0]);
+      load_piece<T, VE>((const T*)a.go + t * a.ldgo, c, a.d, to[q][1]);
       if constexpr (!OUT) {
-        if (a.gr) load_n<T, VE, (VE > 1)>((const T*)a.gr + t * a.ldgr + c, to[q][2]);
-        if (a.u) load_n<T, VE, (VE > 1)>((const T*)a.u + t * a.ldu + c, to[q][3]);
+        if (a.gr) load_piece<T, VE>((const T*)a.gr + t * a.ldgr, c, a.d, to[q][2]);
+        if (a.u) load_piece<T, VE>((const T*)a.u + t * a.ldu, c, a.d, to[q][3]);
       }
     }
   };
   int turn = 0;
   // one barrier: the next sum goes to the other buffer
   auto row_join = [&](float s) {
-    s = group_all<64>(s, OpAdd());
+    s = group_all<(NT < 64 ? NT : 64)>(s, OpAdd());
     if constexpr (NW > 1) {
       float* r = red[turn & 1][rg];
       ++turn;
@@ -194,13 +229,15 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
       for (int q = 0; q < KC; ++q) {
         const int c = (li + q * NT) * VE;
         if (c >= a.d) continue;
-        float w[VE], g[VE];
-        load_w<T, VE>(a, c, w);
-        if constexpr (OUT) load_g<VE>(a, c, g_row, g);
+        float w[VE], g[VE], xs[VE], os[VE];
+        w_of(c, w);
+        if constexpr (OUT) g_of(c, g_row, g);
+        settle_f<T, VE>(c, a.d, cur[q][0], xs);
+        settle_f<T, VE>(c, a.d, cur[q][1], os);
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
-          const float o = elem_f(cur[q][1][i]);
-          xh[q][i] = elem_f(cur[q][0][i]) * rstd;
+          const float o = os[i];
+          xh[q][i] = xs[i] * rstd;
           float dv = o;
           if constexpr (OUT) {
             dv *= g[i];
@@ -242,22 +279,25 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
         for (int i = 0; i < VE; ++i) dx[i] = rs * (p[q][i] - xh[q][i] * mean);
         if constexpr (!OUT) {
           if (a.gr) {
+            float more[VE];
+            settle_f<T, VE>(c, a.d, own[q][0], more);
 #pragma unroll
-            for (int i = 0; i < VE; ++i) dx[i] += elem_f(own[q][0][i]);
+            for (int i = 0; i < VE; ++i) dx[i] += more[i];
           }
           if (a.u) {
-            float g[VE], du[VE];
-            load_g<VE>(a, c, gr_, g);
+            float g[VE], du[VE], uu[VE];
+            g_of(c, gr_, g);
+            settle_f<T, VE>(c, a.d, own[q][1], uu);
 #pragma unroll
             for (int i = 0; i < VE; ++i) {
               du[i] = g[i] * dx[i];
-              if constexpr (FEAT) dg[q][i] += elem_f(own[q][1][i]) * dx[i];
-              else b += elem_f(own[q][1][i]) * dx[i];
+              if constexpr (FEAT) dg[q][i] += uu[i] * dx[i];
+              else b += uu[i] * dx[i];
             }
-            store_f<T, VE>((T*)a.r + t * a.ldr + c, du);
+            store_f<T, VE>((T*)a.r + t * a.ldr, c, a.d, du);
           }
         }
-        store_f<T, VE>((T*)a.n + t * a.ldn + c, dx);
+        store_f<T, VE>((T*)a.n + t * a.ldn, c, a.d, dx);
       }
     }
     if constexpr (!OUT && !FEAT)
@@ -275,22 +315,32 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
       float sum[VE];
 #pragma unroll
       for (int i = 0; i < VE; ++i) sum[i] = h ? (FEAT ? dg[FEAT ? q : 0][i] : 0.f) : dw[q][i];
-      if constexpr (RPW > 1) {
-        __syncthreads();
+      if constexpr (J > 1) {
+        if constexpr (NT < 64) {                         // the wave's rows first
 #pragma unroll
-        for (int i = 0; i < VE; ++i) join[(rg * VE + i) * NT + li] = sum[i];
+          for (int i = 0; i < VE; ++i)
+#pragma unroll
+            for (int o = NT; o < 64; o <<= 1) sum[i] += __shfl_xor(sum[i], o, 64);
+        }
+        const int strand = NT < 64 ? threadIdx.x >> 6 : rg;
+        __syncthreads();
+        if (NT >= 64 || (threadIdx.x & 63) < NT) {
+#pragma unroll
+          for (int i = 0; i < VE; ++i) join[(strand * VE + i) * NT + li] = sum[i];
+        }
         __syncthreads();
         if (rg) continue;
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
           sum[i] = 0.f;
-          for (int o = 0; o < RPW; ++o) sum[i] += join[(o * VE + i) * NT + li];
+          for (int o = 0; o < J; ++o) sum[i] += join[(o * VE + i) * NT + li];
         }
       }
       if (c >= a.d) continue;
       float* to = (h ? a.part_g : a.part_w) + (size_t)blockIdx.x * a.d + c;
 #pragma unroll
-      for (int i = 0; i < VE; ++i) to[i] = h && alone ? a.alpha * sum[i] : sum[i];
+      for (int i = 0; i < VE; ++i) sum[i] *= h && alone ? a.alpha : 1.f;
+      store_upto<float, VE>(to, a.d - c, sum);
     }
   }
 }
@@ -331,39 +381,33 @@ size_t norm_ws_bytes(int T, int d) {
   return 2 * align_up((size_t)norm_grid(T, 1) * d * sizeof(float));
 }
 
-static bool aligned16(const void* p, size_t ld_bytes) {
-  return !p || (((uintptr_t)p & 15u) == 0 && ld_bytes % 16 == 0);
-}
-
-// F::go<T, VE, NT, KC>(args...): by how many pieces of VE elements a row has
+// F::go<T, VE, NT, KC>(args...): NT threads with KC pieces of VE elements each take a row.  The
+// backward pass takes threads before pieces: with four pieces a thread (a wave or a workgroup of 256
+// a row) its sums left room for one wave a SIMD, 160 us at 4099 x 7168 against 68.
 template <class F, typename T, int VE, typename... A> static void norm_shape(int d, A&&... args) {
   const int pieces = (d + VE - 1) / VE;
-  if constexpr (F::kOnePiece) {                          // threads for a row before pieces for a thread
+  if (pieces <= 8) return F::template go<T, VE, 8, 1>(args...);
+  if (pieces <= 16) return F::template go<T, VE, 16, 1>(args...);
+  if (pieces <= 32) return F::template go<T, VE, 32, 1>(args...);
+  if constexpr (F::kOnePiece) {
     if (pieces <= 64) return F::template go<T, VE, 64, 1>(args...);
     if (pieces <= 128) return F::template go<T, VE, 128, 1>(args...);
     if (pieces <= 256) return F::template go<T, VE, 256, 1>(args...);
     if (pieces <= 512) return F::template go<T, VE, 512, 1>(args...);
     if (pieces <= 1024) return F::template go<T, VE, 1024, 1>(args...);
-  } else if (pieces <= 64) F::template go<T, VE, 64, 1>(args...);
-  else if (pieces <= 128) F::template go<T, VE, 64, 2>(args...);
-  else if (pieces <= 256) F::template go<T, VE, 64, 4>(args...);
-  else if (pieces <= 512) F::template go<T, VE, 256, 2>(args...);
-  else if (pieces <= 1024) F::template go<T, VE, 256, 4>(args...);
-  if (pieces <= 1024) return;
-  if (pieces <= 2048) F::template go<T, VE, 1024, 2>(args...);
-  else if constexpr (VE < 8) {                           // 8 elements: d ends at 2048 pieces
-    if (pieces <= 4096) F::template go<T, VE, 1024, 4>(args...);
-    else if constexpr (VE == 1) F::template go<T, VE, 1024, 16>(args...);
-  }
-}
-template <class F, typename... A> static void norm_kind(int dtype, bool vec, int d, A&&... args) {
-  if (dtype == MOE_F32) {
-    if (vec) norm_shape<F, float, 4>(d, args...);
-    else norm_shape<F, float, 1>(d, args...);
   } else {
-    if (vec) norm_shape<F, uint16_t, 8>(d, args...);
-    else norm_shape<F, uint16_t, 1>(d, args...);
+    if (pieces <= 64) return F::template go<T, VE, 64, 1>(args...);
+    if (pieces <= 128) return F::template go<T, VE, 64, 2>(args...);
+    if (pieces <= 256) return F::template go<T, VE, 64, 4>(args...);
+    if (pieces <= 512) return F::template go<T, VE, 256, 2>(args...);
+    if (pieces <= 1024) return F::template go<T, VE, 256, 4>(args...);
   }
+  if (pieces <= 2048) return F::template go<T, VE, 1024, 2>(args...);
+  if constexpr (VE == 4) F::template go<T, VE, 1024, 4>(args...);    // 8 elements: d ends at 2048 pieces
+}
+template <class F, typename... A> static void norm_kind(int dtype, int d, A&&... args) {
+  if (dtype == MOE_F32) norm_shape<F, float, 4>(d, args...);
+  else norm_shape<F, uint16_t, 8>(d, args...);
 }
 
 struct NormFwd {
@@ -409,15 +453,6 @@ static NormArgs norm_args(const moe_norm& N) {
   return a;
 }
 
-// 16-byte pieces: every row and vector starts on one, and d is whole pieces
-static bool norm_vec(const moe_norm& N, std::initializer_list<NormRows> rows) {
-  const size_t eb = N.dtype == MOE_F32 ? 4 : 2;
-  bool ok = (N.d * eb) % 16 == 0 && aligned16(N.w, 0) &&
-            (N.gate_kind != MOE_GATE_FEATURE || aligned16(N.gate, 0));
-  for (const NormRows& r : rows) ok = ok && aligned16(r.p, r.p ? (size_t)r.ld * eb : 0);
-  return ok;
-}
-
 int launch_norm(const moe_norm& N, bool out, NormRows x, NormRows u, NormRows r, NormRows n,
                 float* rstd, hipStream_t st) {
   if (N.T == 0) return MOE_OK;
@@ -426,7 +461,7 @@ int launch_norm(const moe_norm& N, bool out, NormRows x, NormRows u, NormRows r,
   a.r = const_cast<void*>(r.p); a.ldr = (size_t)r.ld;
   a.n = const_cast<void*>(n.p); a.ldn = (size_t)n.ld;
   a.rstd = rstd;
-  norm_kind<NormFwd>(N.dtype, norm_vec(N, {x, u, r, n}), N.d, a, out, st);
+  norm_kind<NormFwd>(N.dtype, N.d, a, out, st);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
@@ -442,7 +477,7 @@ int launch_norm_bwd(const moe_norm& N, bool out, NormRows dn, NormRows dr, NormR
   a.dgate = dgate;
   a.part_w = (float*)ws;
   a.part_g = (float*)((char*)ws + norm_ws_bytes(N.T, N.d) / 2);
-  norm_kind<NormBwd>(N.dtype, norm_vec(N, {dn, dr, r, u, dx, du}), N.d, a, out, dw, dgate, st);
+  norm_kind<NormBwd>(N.dtype, N.d, a, out, dw, dgate, st);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

@@ -39,7 +39,7 @@ struct RouterArgs {
   float* dots;         // [workgroups of the totals] sums of c_e prob_sum_e
   int32_t* done;       // workgroups of the totals that have written theirs
   size_t ld, ld_out;
-  int T, E, k, renorm, vec, parts;
+  int T, E, k, renorm, parts;
   float scale;
 };
 
@@ -61,16 +61,13 @@ MOE_DEV float inverse(float x) { return __builtin_amdgcn_rcpf(x); }   // 1 ulp
 
 // The lane's V logits in fp32 (-infinity past E and in a row that is off).
 template <typename T, int V>
-MOE_DEV void load_logits(const T* row, int c0, int E, bool vec, bool on, float* v) {
+MOE_DEV void load_logits(const T* row, int c0, int E, bool on, float* v) {
   T raw[V];
-  if (on && vec && c0 + V <= E) {
-    load_n<T, V, true>(row + c0, raw);
+  load_piece<T, V>(row, c0, E, raw);
+  settle_piece<T, V>(c0, E, raw);
+  const int n = on ? E - c0 : 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = elem_f(raw[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = on && c0 + i < E ? elem_f(row[c0 + i]) : -INFINITY;
-  }
+  for (int i = 0; i < V; ++i) v[i] = i < n ? elem_f(raw[i]) : -INFINITY;
 }
 
 // The row's scores.  w: the scores' exponentials up to a factor of the row,
@@ -161,7 +158,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
   for (size_t t = (size_t)blockIdx.x * G + g; t < (size_t)a.T; t += step) {
     float v[V], w[V];
     const bool on = !a.mask || a.mask[t];
-    load_logits<T, V>((const T*)a.logits + t * a.ld, c0, a.E, a.vec, on, v);
+    load_logits<T, V>((const T*)a.logits + t * a.ld, c0, a.E, on, v);
     int32_t* ids = a.ids + t * a.k;
     float* gates = a.gates + t * a.k;
     Score<SCORE> sc_;
@@ -391,7 +388,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
   for (size_t t = (size_t)blockIdx.x * G + g; t < (size_t)a.T; t += step) {
     float v[V], w[V], away[V];
     const bool on = !a.mask || a.mask[t];
-    load_logits<T, V>((const T*)a.logits + t * a.ld, c0, a.E, a.vec, on, v);
+    load_logits<T, V>((const T*)a.logits + t * a.ld, c0, a.E, on, v);
     // the choices: lane j's, and through LDS to the experts' lanes
     float d[V], H = 0.f;
     uint8_t flag[V];
@@ -482,13 +479,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
 #pragma unroll
       for (int i = 0; i < V; ++i) elem_set(o[i], 0.f);
     }
-    if (a.vec && c0 + V <= a.E) {
-      store_n<T, V, true>(out + c0, o);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (c0 + i < a.E) out[c0 + i] = o[i];
-    }
+    store_upto<T, V>(out + c0, a.E - c0, o);
   }
 }
 
@@ -510,8 +501,8 @@ __global__ __launch_bounds__(256) void k_gate_grad(const T* __restrict__ z, cons
     const size_t base = (size_t)slot * 2 * dff + dff;
     for (int c = li * VE; c < dff; c += L * VE) {
       T u[VE], du[VE];
-      load_n<T, VE, true>(z + base + c, u);
-      load_n<T, VE, true>(dz + base + c, du);
+      load_n<T, VE>(z + base + c, u);
+      load_n<T, VE>(dz + base + c, du);
 #pragma unroll
       for (int i = 0; i < VE; ++i) s += elem_f(u[i]) * elem_f(du[i]);
     }
@@ -562,10 +553,6 @@ template <typename T, int L, int V, int SCORE> struct BwdK {
   }
 };
 
-static bool rows_aligned(const void* p, size_t ld, size_t elem, int E) {
-  return ((uintptr_t)p & 15u) == 0 && (ld * elem) % 16 == 0 && E % 8 == 0;
-}
-
 int launch_router(const moe_router& R, const void* logits, int ld, const uint8_t* mask, int T,
                   int32_t* ids, float* gates, int32_t* counts, float* psum, int32_t* live,
                   float* losses, int32_t* status, void* ws, hipStream_t st) {
@@ -574,7 +561,6 @@ int launch_router(const moe_router& R, const void* logits, int ld, const uint8_t
   a.renorm = R.renorm; a.scale = R.scale;
   a.ids = ids; a.gates = gates; a.counts = counts; a.psum = psum; a.live = live;
   a.losses = losses; a.status = status;
-  a.vec = rows_aligned(logits, a.ld, R.dtype == MOE_F32 ? 4 : 2, R.E);
   const int grid = router_grid(T, R.E);
   char* w = (char*)ws;
   a.part_p = (float*)w;
@@ -600,8 +586,6 @@ int launch_router_bwd(const moe_router& R, const void* logits, int ld, const uin
   a.renorm = R.renorm; a.scale = R.scale;
   a.ids_in = ids; a.dlogp = dlogp; a.counts_in = counts; a.live_in = live; a.dlosses = dlosses;
   a.dlogits = dlogits; a.ld_out = (size_t)ld_out;
-  const size_t eb = R.dtype == MOE_F32 ? 4 : 2;
-  a.vec = rows_aligned(logits, a.ld, eb, R.E) && rows_aligned(dlogits, a.ld_out, eb, R.E);
   const int G = kRouterThreads / router_lanes(R.E);
   const int grid = (int)std::min<long long>(((long long)T + G - 1) / G, 256 * 8);
   router_kind<BwdK>(R, a, grid, st);
