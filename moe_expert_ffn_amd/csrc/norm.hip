@@ -57,17 +57,19 @@ template <int VE> MOE_DEV void load_g(const NormArgs& a, int c, float* v) {
   }
 }
 
-// Sum over the NT threads of a row.  More than a wave: through LDS, `red` two
-// buffers used in turn, so one barrier per sum is enough.
-template <int NT> MOE_DEV float row_sum(float s, float (*red)[16], int turn) {
+// Forward workgroups: several rows of up to a wave, or one row of NT threads.
+template <int NT> struct RowsOf {
+  static constexpr int WG = NT <= 64 ? 256 : NT, RPW = WG / NT;
+};
+// Sum over the NT threads of a row, once.
+template <int NT> MOE_DEV float row_sum(float s, float* red) {
   s = group_all<(NT < 64 ? NT : 64)>(s, OpAdd());
   if constexpr (NT > 64) {
-    float* r = red[turn & 1];
-    if ((threadIdx.x & 63) == 0) r[threadIdx.x >> 6] = s;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
     __syncthreads();
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < NT / 64; ++i) s += r[i];
+    for (int i = 0; i < NT / 64; ++i) s += red[i];
   }
   return s;
 }
@@ -75,12 +77,12 @@ template <int NT> MOE_DEV float row_sum(float s, float (*red)[16], int turn) {
 // NT threads take a row, KC pieces of VE elements each, which stay in
 // registers between the sum and the output: every row is read once.
 template <typename T, int VE, int NT, int KC, bool OUT>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(NormArgs a) {
-  constexpr int RPW = NT < 256 ? 256 / NT : 1;
-  __shared__ float red[2][16];
+__global__ __launch_bounds__(RowsOf<NT>::WG) void k_norm(NormArgs a) {
+  constexpr int RPW = RowsOf<NT>::RPW;
+  __shared__ float red[16];
   const int li = threadIdx.x % NT;
   const size_t t = (size_t)blockIdx.x * RPW + threadIdx.x / NT;
-  if (t >= (size_t)a.T) return;                          // a whole wave
+  if (t >= (size_t)a.T) return;                          // only where a row has no barrier
   const float g_row = a.alpha * (a.kind == MOE_GATE_TOKEN ? a.gate[t] : 1.f);
   const T* x = (const T*)a.x + t * a.ldx;
   const T* u = (const T*)a.u + t * a.ldu;
@@ -115,7 +117,12 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(NormArgs a) {
 #pragma unroll
     for (int i = 0; i < VE; ++i) s += v[q][i] * v[q][i];
   }
-  s = row_sum<NT>(s, red, 0);
+  float ws[VE], gs[VE];                                  // on their way during the sum
+  if (KC == 1 && li * VE < a.d) {
+    load_w<T, VE>(a, li * VE, ws);
+    if (OUT) load_g<VE>(a, li * VE, gs);
+  }
+  s = row_sum<NT>(s, red);
   const float rstd = 1.f / sqrtf(s * a.inv_d + a.eps);
   if (li == 0) a.rstd[t] = rstd;
 #pragma unroll
@@ -123,10 +130,12 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void k_norm(NormArgs a) {
     const int c = (li + q * NT) * VE;
     if (c >= a.d) continue;
     float w[VE], o[VE];
-    load_w<T, VE>(a, c, w);
+    if constexpr (KC == 1) __builtin_memcpy(w, ws, sizeof w);
+    else load_w<T, VE>(a, c, w);
     if constexpr (OUT) {
       float g[VE];
-      load_g<VE>(a, c, g);
+      if constexpr (KC == 1) __builtin_memcpy(g, gs, sizeof g);
+      else load_g<VE>(a, c, g);
 #pragma unroll
       for (int i = 0; i < VE; ++i) o[i] = xs[q][i] + g[i] * g_row * (v[q][i] * rstd * w[i]);
     } else {
@@ -148,17 +157,34 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
   constexpr int RPW = kNormWG / NT, NW = NT / 64;        // NW 0: several rows a wave
   constexpr int J = NT < 64 ? kNormWG / 64 : RPW;        // strands joined through LDS
   constexpr int IN = OUT ? 2 : 4;                        // row operands: x, go and (before) gr, u
+  // with several pieces a thread the registers hold one row (four: without gr and u until they are used)
+  constexpr bool AHEAD = KC == 1, LATE = KC == 4;
   __shared__ float red[2][NW > 1 ? RPW : 1][16];
   __shared__ float join[J > 1 ? J * VE * NT : 1];
   const int li = threadIdx.x % NT, rg = threadIdx.x / NT;
-  float dw[KC][VE], dg[FEAT ? KC : 1][VE];
+  // a thread's sums: in registers, with several pieces in LDS (its own places, in 16-byte pieces;
+  // in registers they spilled: 3000 x 12000 bf16 191 us)
+  extern __shared__ __attribute__((aligned(16))) float sums[];
+  float dw[VE], dg[VE];
 #pragma unroll
-  for (int q = 0; q < KC; ++q)
+  for (int i = 0; i < VE; ++i) dw[i] = dg[i] = 0.f;
+  auto sum_at = [&](int h, int q, int i) { return sums + (((h * KC + q) * VE + i) / 4 * kNormWG + (int)threadIdx.x) * 4; };
+  auto add_to = [&](int h, int q, const float* more) {
+    if constexpr (KC == 1) {
 #pragma unroll
-    for (int i = 0; i < VE; ++i) {
-      dw[q][i] = 0.f;
-      if constexpr (FEAT) dg[q][i] = 0.f;
+      for (int i = 0; i < VE; ++i) (h ? dg : dw)[i] += more[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VE; i += 4) {
+        float4* at = (float4*)sum_at(h, q, i);
+        float4 v = *at;
+        v.x += more[i]; v.y += more[i + 1]; v.z += more[i + 2]; v.w += more[i + 3];
+        *at = v;
+      }
     }
+  };
+  if constexpr (KC > 1)
+    for (int q = 0; q < KC * (FEAT ? 2 : 1) * VE; q += 4) *(float4*)sum_at(0, 0, q) = make_float4(0.f, 0.f, 0.f, 0.f);
   float ws[VE], gs[VE];                                  // one piece: w and the gate stay
   if constexpr (KC == 1) {
 #pragma unroll
@@ -187,21 +213,29 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
   const size_t step = (size_t)gridDim.x * RPW;
   T cur[KC][IN][VE];
   float rstd = 0.f, g_row = a.alpha;
-  auto fetch = [&](size_t t, T (*to)[IN][VE], float* rs, float* gr_) {
+  auto fetch_more = [&](size_t t) {
+#pragma unroll
+    for (int q = 0; q < KC; ++q) {
+      const int c = (li + q * NT) * VE;
+      if (c >= a.d || t >= (size_t)a.T) continue;
+      if constexpr (!OUT) {
+        if (a.gr) load_piece<T, VE>((const T*)a.gr + t * a.ldgr, c, a.d, cur[q][2]);
+        if (a.u) load_piece<T, VE>((const T*)a.u + t * a.ldu, c, a.d, cur[q][3]);
+      }
+    }
+  };
+  auto fetch = [&](size_t t) {
     if (t >= (size_t)a.T) return;
-    *rs = a.rstd[t];
-    if (a.kind == MOE_GATE_TOKEN) *gr_ = a.alpha * a.gate[t];
+    rstd = a.rstd[t];
+    if (a.kind == MOE_GATE_TOKEN) g_row = a.alpha * a.gate[t];
 #pragma unroll
     for (int q = 0; q < KC; ++q) {
       const int c = (li + q * NT) * VE;
       if (c >= a.d) continue;
-      load_piece<T, VE>((const T*)a.x + t * a.ldx, c, a.d, to[q][0]);
-      load_piece<T, VE>((const T*)a.go + t * a.ldgo, c, a.d, to[q][1]);
-      if constexpr (!OUT) {
-        if (a.gr) load_piece<T, VE>((const T*)a.gr + t * a.ldgr, c, a.d, to[q][2]);
-        if (a.u) load_piece<T, VE>((const T*)a.u + t * a.ldu, c, a.d, to[q][3]);
-      }
+      load_piece<T, VE>((const T*)a.x + t * a.ldx, c, a.d, cur[q][0]);
+      load_piece<T, VE>((const T*)a.go + t * a.ldgo, c, a.d, cur[q][1]);
     }
+    if constexpr (!LATE) fetch_more(t);
   };
   int turn = 0;
   // one barrier: the next sum goes to the other buffer
@@ -218,10 +252,11 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
     }
     return s;
   };
-  fetch((size_t)blockIdx.x * RPW + rg, cur, &rstd, &g_row);
+  if constexpr (AHEAD) fetch((size_t)blockIdx.x * RPW + rg);
   for (size_t t0 = (size_t)blockIdx.x * RPW; t0 < (size_t)a.T; t0 += step) {
     const size_t t = t0 + rg;
     const bool on = t < (size_t)a.T;
+    if constexpr (!AHEAD) fetch(t);
     float xh[KC][VE], p[KC][VE];       // x / rms, and the gradient of that
     float s = 0.f;
     if (on) {
@@ -234,6 +269,7 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
         if constexpr (OUT) g_of(c, g_row, g);
         settle_f<T, VE>(c, a.d, cur[q][0], xs);
         settle_f<T, VE>(c, a.d, cur[q][1], os);
+        float mw[VE], mg[VE];
 #pragma unroll
         for (int i = 0; i < VE; ++i) {
           const float o = os[i];
@@ -241,28 +277,25 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
           float dv = o;
           if constexpr (OUT) {
             dv *= g[i];
-            if constexpr (FEAT) dg[q][i] += o * (w[i] * xh[q][i]);
+            mg[i] = o * (w[i] * xh[q][i]);
           }
-          dw[q][i] += dv * xh[q][i];
+          mw[i] = dv * xh[q][i];
           p[q][i] = dv * w[i];
           // after the block, a token's gate: the sum without it, which is also its gradient
           s += (OUT && !FEAT ? o * w[i] : p[q][i]) * xh[q][i];
         }
+        add_to(0, q, mw);
+        if constexpr (OUT && FEAT) add_to(1, q, mg);
       }
     }
     const float rs = rstd, gr_ = g_row;
-    T own[OUT ? 1 : KC][2][VE];                          // gr and u of this row
-    if constexpr (!OUT) {
-#pragma unroll
-      for (int q = 0; q < KC; ++q)
-#pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          own[q][0][i] = cur[q][2][i];
-          own[q][1][i] = cur[q][3][i];
-        }
+    T kept[AHEAD && !OUT ? KC : 1][2][VE];               // gr and u of this row
+    if constexpr (AHEAD) {
+      if constexpr (!OUT) __builtin_memcpy(kept, &cur[0][2], sizeof kept);
+      fetch(t + step);
     }
-    fetch(t + step, cur, &rstd, &g_row);
     s = row_join(s);
+    if constexpr (LATE) fetch_more(t);
     if constexpr (OUT && !FEAT) {
       if (on && a.kind == MOE_GATE_TOKEN && li == 0) a.dgate[t] = a.alpha * s;
       s *= gr_;
@@ -278,22 +311,24 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < VE; ++i) dx[i] = rs * (p[q][i] - xh[q][i] * mean);
         if constexpr (!OUT) {
+          T(*own)[VE] = AHEAD ? kept[AHEAD ? q : 0] : &cur[q][2];
           if (a.gr) {
             float more[VE];
-            settle_f<T, VE>(c, a.d, own[q][0], more);
+            settle_f<T, VE>(c, a.d, own[0], more);
 #pragma unroll
             for (int i = 0; i < VE; ++i) dx[i] += more[i];
           }
           if (a.u) {
             float g[VE], du[VE], uu[VE];
             g_of(c, gr_, g);
-            settle_f<T, VE>(c, a.d, own[q][1], uu);
+            settle_f<T, VE>(c, a.d, own[1], uu);
 #pragma unroll
             for (int i = 0; i < VE; ++i) {
               du[i] = g[i] * dx[i];
-              if constexpr (FEAT) dg[q][i] += uu[i] * dx[i];
-              else b += uu[i] * dx[i];
+              uu[i] *= dx[i];
+              if constexpr (!FEAT) b += uu[i];
             }
+            if constexpr (FEAT) add_to(1, q, uu);
             store_f<T, VE>((T*)a.r + t * a.ldr, c, a.d, du);
           }
         }
@@ -314,7 +349,7 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
     for (int h = 0; h < (FEAT ? 2 : 1); ++h) {
       float sum[VE];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) sum[i] = h ? (FEAT ? dg[FEAT ? q : 0][i] : 0.f) : dw[q][i];
+      for (int i = 0; i < VE; ++i) sum[i] = KC > 1 ? sum_at(h, q, i)[i % 4] : h ? dg[i] : dw[i];
       if constexpr (J > 1) {
         if constexpr (NT < 64) {                         // the wave's rows first
 #pragma unroll
@@ -381,27 +416,21 @@ size_t norm_ws_bytes(int T, int d) {
   return 2 * align_up((size_t)norm_grid(T, 1) * d * sizeof(float));
 }
 
-// F::go<T, VE, NT, KC>(args...): NT threads with KC pieces of VE elements each take a row.  The
-// backward pass takes threads before pieces: with four pieces a thread (a wave or a workgroup of 256
-// a row) its sums left room for one wave a SIMD, 160 us at 4099 x 7168 against 68.
+// F::go<T, VE, NT, KC>(args...): NT threads with KC pieces of VE elements each take a row, threads
+// before pieces.  Four pieces a thread (a wave, or 256 threads, a row) save the sums' barriers but
+// wait for a row alone: before the block in bf16 1 x 7168 5.3 us against 2.9, 1024 x 2048 6.8 against
+// 4.2, 8192 x 2048 21.8 against 23.0, 8192 x 7168 92.6 against 88.9; in the backward pass its sums left
+// room for one wave a SIMD, 4099 x 7168 160 us against 68.
 template <class F, typename T, int VE, typename... A> static void norm_shape(int d, A&&... args) {
   const int pieces = (d + VE - 1) / VE;
   if (pieces <= 8) return F::template go<T, VE, 8, 1>(args...);
   if (pieces <= 16) return F::template go<T, VE, 16, 1>(args...);
   if (pieces <= 32) return F::template go<T, VE, 32, 1>(args...);
-  if constexpr (F::kOnePiece) {
-    if (pieces <= 64) return F::template go<T, VE, 64, 1>(args...);
-    if (pieces <= 128) return F::template go<T, VE, 128, 1>(args...);
-    if (pieces <= 256) return F::template go<T, VE, 256, 1>(args...);
-    if (pieces <= 512) return F::template go<T, VE, 512, 1>(args...);
-    if (pieces <= 1024) return F::template go<T, VE, 1024, 1>(args...);
-  } else {
-    if (pieces <= 64) return F::template go<T, VE, 64, 1>(args...);
-    if (pieces <= 128) return F::template go<T, VE, 64, 2>(args...);
-    if (pieces <= 256) return F::template go<T, VE, 64, 4>(args...);
-    if (pieces <= 512) return F::template go<T, VE, 256, 2>(args...);
-    if (pieces <= 1024) return F::template go<T, VE, 256, 4>(args...);
-  }
+  if (pieces <= 64) return F::template go<T, VE, 64, 1>(args...);
+  if (pieces <= 128) return F::template go<T, VE, 128, 1>(args...);
+  if (pieces <= 256) return F::template go<T, VE, 256, 1>(args...);
+  if (pieces <= 512) return F::template go<T, VE, 512, 1>(args...);
+  if (pieces <= 1024) return F::template go<T, VE, 1024, 1>(args...);
   if (pieces <= 2048) return F::template go<T, VE, 1024, 2>(args...);
   if constexpr (VE == 4) F::template go<T, VE, 1024, 4>(args...);    // 8 elements: d ends at 2048 pieces
 }
@@ -411,10 +440,9 @@ template <class F, typename... A> static void norm_kind(int dtype, int d, A&&...
 }
 
 struct NormFwd {
-  static constexpr bool kOnePiece = false;
   template <typename T, int VE, int NT, int KC>
   static void go(const NormArgs& a, bool out, hipStream_t st) {
-    constexpr int RPW = NT < 256 ? 256 / NT : 1, WG = NT < 256 ? 256 : NT;
+    constexpr int RPW = RowsOf<NT>::RPW, WG = RowsOf<NT>::WG;
     const dim3 grid((unsigned)(((size_t)a.T + RPW - 1) / RPW));
     if (out) hipLaunchKernelGGL((k_norm<T, VE, NT, KC, true>), grid, dim3(WG), 0, st, a);
     else hipLaunchKernelGGL((k_norm<T, VE, NT, KC, false>), grid, dim3(WG), 0, st, a);
@@ -422,7 +450,6 @@ struct NormFwd {
 };
 
 struct NormBwd {
-  static constexpr bool kOnePiece = true;
   template <typename T, int VE, int NT, int KC>
   static void go(NormArgs& a, bool out, float* dw, float* dgate, hipStream_t st) {
     constexpr int RPW = kNormWG / NT, WG = kNormWG;
@@ -434,11 +461,17 @@ struct NormBwd {
       a.part_w = dw;
       a.part_g = dgate;
     }
-    const dim3 grid(parts), wg(WG);
-    if (out && feat) hipLaunchKernelGGL((k_norm_bwd<T, VE, NT, KC, true, true>), grid, wg, 0, st, a);
-    else if (out) hipLaunchKernelGGL((k_norm_bwd<T, VE, NT, KC, true, false>), grid, wg, 0, st, a);
-    else if (feat) hipLaunchKernelGGL((k_norm_bwd<T, VE, NT, KC, false, true>), grid, wg, 0, st, a);
-    else hipLaunchKernelGGL((k_norm_bwd<T, VE, NT, KC, false, false>), grid, wg, 0, st, a);
+    const size_t lds = KC > 1 ? sizeof(float) * KC * VE * kNormWG * (feat ? 2 : 1) : 0;
+    auto launch = [&](auto kernel) {
+      if (lds > 48 * 1024)
+        (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)lds);
+      hipLaunchKernelGGL(kernel, dim3(parts), dim3(WG), lds, st, a);
+    };
+    if (out && feat) launch(k_norm_bwd<T, VE, NT, KC, true, true>);
+    else if (out) launch(k_norm_bwd<T, VE, NT, KC, true, false>);
+    else if (feat) launch(k_norm_bwd<T, VE, NT, KC, false, true>);
+    else launch(k_norm_bwd<T, VE, NT, KC, false, false>);
     if (parts > 1)
       hipLaunchKernelGGL(k_norm_cols, dim3((a.d + 63) / 64, feat ? 2 : 1), dim3(1024), 0, st, pw,
                          pg, parts, a.d, a.alpha, dw, dgate);
