@@ -552,6 +552,10 @@ def _ws_at(ws):
 
 def _rows(t, T, cols, dtype, name):
     """Row stride of a [T][cols] matrix whose rows' elements lie side by side."""
+    if t.dtype == dtype and t.shape == (T, cols):
+        stride = t.stride()
+        if stride[1] == 1 and stride[0] >= cols:
+            return stride[0]
     if t.dtype != dtype:
         raise MoeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols:
@@ -570,12 +574,14 @@ def _vector(t, n, dtype, name):
                        f"{tuple(t.shape)} of {t.dtype}")
 
 
+_CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
 def _dtype_code(dtype, name):
-    if dtype == torch.float32:
-        return MOE_F32
-    if dtype == torch.bfloat16:
-        return MOE_BF16
-    raise MoeError(f"{name}: unsupported element type {dtype}")
+    code = _CODES.get(dtype)
+    if code is None:
+        raise MoeError(f"{name}: unsupported element type {dtype}")
+    return code
 
 
 def make_router(E, k, dtype=torch.float32, score="softmax", renorm=True, scale=1.0) -> Router:
@@ -683,26 +689,29 @@ def _norm_desc(rows, w, gate, alpha, eps, name):
         raise MoeError(f"{name}: expected [T][d], got {tuple(rows.shape)}")
     T, d = rows.shape
     code = _dtype_code(rows.dtype, name)
-    if w.dtype not in (torch.float32, rows.dtype):
+    w_code = _dtype_code(w.dtype, "w")
+    if w_code != code and w_code != MOE_F32:
         raise MoeError(f"w: expected float32 or {rows.dtype}, got {w.dtype}")
-    if tuple(w.shape) != (d,) or not w.is_contiguous():
+    if w.shape != (d,) or not w.is_contiguous():
         raise MoeError(f"w: expected {d} contiguous elements, got {tuple(w.shape)}")
     kind = GATE_NONE
     if gate is not None:
-        if tuple(gate.shape) == (T, 1):
+        if gate.shape == (T, 1):
             kind = GATE_TOKEN
-        elif tuple(gate.shape) == (d,):
+        elif gate.shape == (d,):
             kind = GATE_FEATURE
         else:
             raise MoeError(f"gate: expected {(T, 1)} or {(d,)}, got {tuple(gate.shape)}")
-        _vector(gate, gate.numel(), torch.float32, "gate")
-    N = Norm(T, d, code, _dtype_code(w.dtype, "w"), kind, alpha, eps, w.data_ptr(),
+        _vector(gate, 0, torch.float32, "gate")
+    N = Norm(T, d, code, w_code, kind, alpha, eps, w.data_ptr(),
              None if gate is None else gate.data_ptr())
     return N, T, d, _rows(rows, T, d, rows.dtype, name)
 
 
 def _opt_rows(t, T, d, dtype, name):
-    return (None, 0) if t is None else (t.data_ptr(), _rows(t, T, d, dtype, name))
+    if t is None:
+        return None, 0
+    return t.data_ptr(), _rows(t, T, d, dtype, name)
 
 
 def norm_in(x, w, eps, n, rstd, u=None, gate=None, alpha=1.0, r=None):

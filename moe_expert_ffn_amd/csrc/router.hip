@@ -13,7 +13,10 @@ namespace moe {
 // (L * V >= E, V a multiple of 8 so that a lane's logits are whole 16-byte
 // pieces); a workgroup of four waves holds 256 / L rows at a time.
 constexpr int kRouterThreads = 256;
-constexpr int kRouterMaxWG = 512;       // workgroups, and so partial sums, of the forward
+#ifndef RMW
+#define RMW 512
+#endif
+constexpr int kRouterMaxWG = RMW;       // workgroups, and so partial sums, of the forward
 constexpr int kTotalThreads = 1024, kTotalCols = 16;
 
 struct RouterArgs {
@@ -59,13 +62,23 @@ MOE_DEV float key_value(uint32_t key) {
 MOE_DEV float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 MOE_DEV float inverse(float x) { return __builtin_amdgcn_rcpf(x); }   // 1 ulp
 
+// A row on its way: the lane's V logits as stored, and the row's mask.
+template <typename T, int V> struct NextRow {
+  T raw[V];
+  uint8_t on;
+  MOE_DEV void fetch(const RouterArgs& a, size_t t, int c0) {
+    if (t >= (size_t)a.T) return;
+    load_piece<T, V>((const T*)a.logits + t * a.ld, c0, a.E, raw);
+    on = a.mask ? a.mask[t] : 1;
+  }
+};
 // The lane's V logits in fp32 (-infinity past E and in a row that is off).
 template <typename T, int V>
-MOE_DEV void load_logits(const T* row, int c0, int E, bool on, float* v) {
+MOE_DEV void logits_of(const NextRow<T, V>& row, int c0, int E, float* v) {
   T raw[V];
-  load_piece<T, V>(row, c0, E, raw);
+  __builtin_memcpy(raw, row.raw, sizeof raw);
   settle_piece<T, V>(c0, E, raw);
-  const int n = on ? E - c0 : 0;
+  const int n = row.on ? E - c0 : 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = i < n ? elem_f(raw[i]) : -INFINITY;
 }
@@ -155,10 +168,12 @@ __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
   float z = 0.f;
   int n = 0;
   const size_t step = (size_t)gridDim.x * G;
+  NextRow<T, V> next;
+  next.fetch(a, (size_t)blockIdx.x * G + g, c0);
   for (size_t t = (size_t)blockIdx.x * G + g; t < (size_t)a.T; t += step) {
     float v[V], w[V];
-    const bool on = !a.mask || a.mask[t];
-    load_logits<T, V>((const T*)a.logits + t * a.ld, c0, a.E, on, v);
+    logits_of<T, V>(next, c0, a.E, v);
+    next.fetch(a, t + step, c0);
     int32_t* ids = a.ids + t * a.k;
     float* gates = a.gates + t * a.k;
     Score<SCORE> sc_;
@@ -304,65 +319,71 @@ __global__ __launch_bounds__(kTotalThreads) void k_router_totals(RouterArgs a) {
   __shared__ int sc[S][kTotalCols];
   __shared__ float red[kTotalThreads / 64];
   __shared__ int redn[kTotalThreads / 64];
-  __shared__ int last;
   const int tid = threadIdx.x, col = tid % kTotalCols, q = tid / kTotalCols;
   const int e = blockIdx.x * kTotalCols + col;
-  float s = 0.f;
-  int c = 0;
-  if (e < a.E)
+  float s = 0.f, z = 0.f;
+  int c = 0, n = 0;
+  if (e < a.E) {
+#pragma unroll 8
     for (int b = q; b < a.parts; b += S) {
       s += a.part_p[(size_t)b * a.E + e];
       c += a.part_c[(size_t)b * a.E + e];
     }
+  }
+  if (tid < a.parts) {                                   // at most kTotalThreads; only the last uses them
+    z = a.part_z[tid];
+    n = a.part_n[tid];
+  }
   sp[q][col] = s;
   sc[q][col] = c;
-  __syncthreads();
-  if (tid < 64) {                                        // four lanes a column, 16 strands each
-    const int cc = tid >> 2, e4 = blockIdx.x * kTotalCols + cc;
-    s = 0.f;
-    c = 0;
-    for (int i = tid & 3; i < S; i += 4) {
-      s += sp[i][cc];
-      c += sc[i][cc];
-    }
-    s += dpp_of<0xB1>(s);
-    s += dpp_of<0x4E>(s);
-    c += dpp_of<0xB1>(c);
-    c += dpp_of<0x4E>(c);
-    const bool mine = e4 < a.E && (tid & 3) == 0;
-    if (mine) {
-      a.psum[e4] = s;
-      a.counts[e4] = c;
-    }
-    const float dot = group_all<64>(mine ? (float)c * s : 0.f, OpAdd());
-    if (tid == 0) {
-      __hip_atomic_store(a.dots + blockIdx.x, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-             (int)gridDim.x - 1;
-    }
-  }
-  __syncthreads();
-  if (!last) return;
-  float z = 0.f;
-  int n = 0;
-  for (int b = tid; b < a.parts; b += kTotalThreads) {
-    z += a.part_z[b];
-    n += a.part_n[b];
-  }
+  z = group_all<64>(z, OpAdd());
   n = group_all<64>(n, OpAdd());
-  if ((tid & 63) == 0) redn[tid >> 6] = n;
-  z = block_sum(z, red, kTotalThreads / 64);
-  if (tid < 64) {                                        // at most 1024 / 16 workgroups
-    const float mine = tid < (int)gridDim.x ? __hip_atomic_load(a.dots + tid, __ATOMIC_RELAXED,
-                                                                __HIP_MEMORY_SCOPE_AGENT) : 0.f;
-    const float dot = group_all<64>(mine, OpAdd());
-    if (tid == 0) {
-      n = 0;
-      for (int i = 0; i < kTotalThreads / 64; ++i) n += redn[i];
-      a.live[0] = n;
-      a.losses[0] = balance_of(dot, a.E, a.k, n);
-      a.losses[1] = n > 0 ? z / (float)n : 0.f;
+  if ((tid & 63) == 0) {
+    red[tid >> 6] = z;
+    redn[tid >> 6] = n;
+  }
+  __syncthreads();
+  if (tid >= 64) return;
+  const int cc = tid >> 2, e4 = blockIdx.x * kTotalCols + cc;      // four lanes a column, 16 strands each
+  s = 0.f;
+  c = 0;
+#pragma unroll
+  for (int i = 0; i < S; i += 4) {
+    s += sp[i + (tid & 3)][cc];
+    c += sc[i + (tid & 3)][cc];
+  }
+  s += dpp_of<0xB1>(s);
+  s += dpp_of<0x4E>(s);
+  c += dpp_of<0xB1>(c);
+  c += dpp_of<0x4E>(c);
+  const bool mine = e4 < a.E && (tid & 3) == 0;
+  if (mine) {
+    a.psum[e4] = s;
+    a.counts[e4] = c;
+  }
+  float dot = group_all<64>(mine ? (float)c * s : 0.f, OpAdd());
+  int last = 0;
+  if (tid == 0) {
+    __hip_atomic_store(a.dots + blockIdx.x, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+           (int)gridDim.x - 1;
+  }
+  if (!__builtin_amdgcn_readfirstlane(last)) return;
+  // at most 1024 / 16 workgroups
+  dot = tid < (int)gridDim.x
+            ? __hip_atomic_load(a.dots + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.f;
+  dot = group_all<64>(dot, OpAdd());
+  if (tid == 0) {
+    z = 0.f;
+    n = 0;
+#pragma unroll
+    for (int i = 0; i < kTotalThreads / 64; ++i) {
+      z += red[i];
+      n += redn[i];
     }
+    a.live[0] = n;
+    a.losses[0] = balance_of(dot, a.E, a.k, n);
+    a.losses[1] = n > 0 ? z / (float)n : 0.f;
   }
 }
 
@@ -385,10 +406,31 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
   for (int i = 0; i < V; ++i)
     ge[i] = c0 + i < a.E ? (float)a.counts_in[c0 + i] * (db * ((float)a.E / a.k) / many / many) : 0.f;
   const size_t step = (size_t)gridDim.x * G;
+  constexpr int KQ = (kRouterMaxK + L - 1) / L;          // choices a lane holds
+  NextRow<T, V> next;
+  int id_next[KQ];
+  float h_next[KQ];
+  auto fetch = [&](size_t t) {
+    next.fetch(a, t, c0);
+#pragma unroll
+    for (int q = 0; q < KQ; ++q) {
+      const int j = q * L + li;
+      id_next[q] = -1;
+      h_next[q] = 0.f;
+      if (j < a.k && t < (size_t)a.T) {
+        id_next[q] = a.ids_in[t * a.k + j];
+        if (a.dlogp) h_next[q] = a.dlogp[t * a.k + j];
+      }
+    }
+  };
+  fetch((size_t)blockIdx.x * G + g);
   for (size_t t = (size_t)blockIdx.x * G + g; t < (size_t)a.T; t += step) {
-    float v[V], w[V], away[V];
-    const bool on = !a.mask || a.mask[t];
-    load_logits<T, V>((const T*)a.logits + t * a.ld, c0, a.E, on, v);
+    float v[V], w[V], away[V], h[KQ];
+    int id[KQ];
+    logits_of<T, V>(next, c0, a.E, v);
+    __builtin_memcpy(id, id_next, sizeof id);
+    __builtin_memcpy(h, h_next, sizeof h);
+    fetch(t + step);
     // the choices: lane j's, and through LDS to the experts' lanes
     float d[V], H = 0.f;
     uint8_t flag[V];
@@ -401,32 +443,28 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
     __builtin_memcpy(&sf[g][c0], flag, sizeof flag);
     __builtin_amdgcn_wave_barrier();
     bool twice = false;
-    for (int j = li; j < a.k; j += L) {
-      const int id = a.ids_in[t * a.k + j];
-      if ((uint32_t)id < (uint32_t)a.E) {
-        const float h = a.dlogp ? a.dlogp[t * a.k + j] : 0.f;
-        H += h;
-        sh[g][id] = h;
-        sf[g][id] = (uint8_t)(j + 1);
+#pragma unroll
+    for (int q = 0; q < KQ; ++q)
+      if ((uint32_t)id[q] < (uint32_t)a.E) {
+        H += h[q];
+        sh[g][id[q]] = h[q];
+        sf[g][id[q]] = (uint8_t)(q * L + li + 1);
       }
-    }
     __builtin_amdgcn_wave_barrier();
-    for (int j = li; j < a.k; j += L) {
-      const int id = a.ids_in[t * a.k + j];
-      if ((uint32_t)id < (uint32_t)a.E) twice |= sf[g][id] != (uint8_t)(j + 1);
-    }
+#pragma unroll
+    for (int q = 0; q < KQ; ++q)
+      if ((uint32_t)id[q] < (uint32_t)a.E) twice |= sf[g][id[q]] != (uint8_t)(q * L + li + 1);
     if (__any(twice)) {                                  // an expert given twice: its gradients in order
-      if (li == 0) {
-        for (int j = 0; j < a.k; ++j) {
-          const int id = a.ids_in[t * a.k + j];
-          if ((uint32_t)id < (uint32_t)a.E) sh[g][id] = 0.f;
-        }
-        for (int j = 0; j < a.k; ++j) {
-          const int id = a.ids_in[t * a.k + j];
-          if ((uint32_t)id < (uint32_t)a.E && a.dlogp) sh[g][id] += a.dlogp[t * a.k + j];
-        }
-      }
+#pragma unroll
+      for (int q = 0; q < KQ; ++q)
+        if ((uint32_t)id[q] < (uint32_t)a.E) sh[g][id[q]] = 0.f;
       __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int q = 0; q < KQ; ++q)
+        for (int j = 0; j < L; ++j) {
+          if (li == j && (uint32_t)id[q] < (uint32_t)a.E) sh[g][id[q]] += h[q];
+          __builtin_amdgcn_wave_barrier();
+        }
     }
     __builtin_memcpy(d, &sh[g][c0], sizeof d);
     __builtin_memcpy(flag, &sf[g][c0], sizeof flag);

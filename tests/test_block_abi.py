@@ -173,7 +173,8 @@ def test_rows_that_are_no_rows(make, why):
 def test_row_strides():
     t = torch.zeros(6, 20)
     assert B._rows(t[:, 3:11], 6, 8, torch.float32, "x") == 20
-    assert B._rows(t[2:3, :8], 1, 8, torch.float32, "x") == 8
+    assert B._rows(t[2:3, :8], 1, 8, torch.float32, "x") == 20
+    assert B._rows(torch.zeros(8).as_strided((1, 8), (3, 1)), 1, 8, torch.float32, "x") == 8
     assert B._rows(t[::2, :8], 3, 8, torch.float32, "x") == 40
     assert B._rows(torch.zeros(0, 8), 0, 8, torch.float32, "x") == 8
     assert B._rows(torch.zeros(5, 1), 5, 1, torch.float32, "x") == 1
