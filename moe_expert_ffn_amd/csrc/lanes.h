@@ -20,12 +20,12 @@ template <int CTRL, typename V> MOE_DEV V dpp_of(V v) {
                                                         true));
 }
 
-// All lanes of a group of L (8, 16, 32 or 64) aligned lanes receive op over the
+// All lanes of a group of L (a power of two up to 64) aligned lanes receive op over the
 // group.  The tree is the same for every lane, so all receive the same bits.
 template <int L, typename V, typename Op> MOE_DEV V group_all(V v, Op op) {
-  v = op(v, dpp_of<0xB1>(v));                            // lane ^ 1 (quad [1, 0, 3, 2])
-  v = op(v, dpp_of<0x4E>(v));                            // lane ^ 2 (quad [2, 3, 0, 1])
-  v = op(v, dpp_of<0x141>(v));                           // the other quad (mirror of 8)
+  if constexpr (L >= 2) v = op(v, dpp_of<0xB1>(v));      // lane ^ 1 (quad [1, 0, 3, 2])
+  if constexpr (L >= 4) v = op(v, dpp_of<0x4E>(v));      // lane ^ 2 (quad [2, 3, 0, 1])
+  if constexpr (L >= 8) v = op(v, dpp_of<0x141>(v));     // the other quad (mirror of 8)
   if constexpr (L >= 16) v = op(v, dpp_of<0x140>(v));    // the other 8 (mirror of 16)
   if constexpr (L >= 32) {
     const uint32_t b = __builtin_bit_cast(uint32_t, v);

@@ -423,6 +423,9 @@ size_t norm_ws_bytes(int T, int d) {
 // room for one wave a SIMD, 4099 x 7168 160 us against 68.
 template <class F, typename T, int VE, typename... A> static void norm_shape(int d, A&&... args) {
   const int pieces = (d + VE - 1) / VE;
+  if (pieces <= 1) return F::template go<T, VE, 1, 1>(args...);
+  if (pieces <= 2) return F::template go<T, VE, 2, 1>(args...);
+  if (pieces <= 4) return F::template go<T, VE, 4, 1>(args...);
   if (pieces <= 8) return F::template go<T, VE, 8, 1>(args...);
   if (pieces <= 16) return F::template go<T, VE, 16, 1>(args...);
   if (pieces <= 32) return F::template go<T, VE, 32, 1>(args...);

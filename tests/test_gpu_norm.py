@@ -42,7 +42,7 @@ def _close(name, got, ref, tol):
     assert worst <= 1.0, f"{name}: {worst:.2f} times the tolerance"
 
 
-SHAPES = [(1, 1), (1, 2048), (1, 7168), (2, 7), (5, 64), (3, 65), (9, 512), (4, 513), (17, 1000), (300, 1023),
+SHAPES = [(1, 1), (3000, 2), (2100, 5), (1500, 9), (700, 17), (1025, 31), (1, 2048), (1, 7168), (2, 7), (5, 64), (3, 65), (9, 512), (4, 513), (17, 1000), (300, 1023),
           (1030, 128), (40, 2048), (21, 2056), (13, 4096), (6, 4104), (7, 7168), (5, 8200), (3, 16384),
           (2, 16381), (0, 64)]
 
