@@ -628,7 +628,8 @@ size_t moe_adamw_workspace_size(int tensors);
  *   misaligned pointer of a tensor with n > 0, an unknown dtype, a master of a
  *   tensor that is not bf16, or memory that two of the buffers written or a
  *   buffer written and a gradient share; MOE_ERR_UNSUPPORTED for state_bits
- *   other than 8 or 32 or above 2^43 elements; MOE_ERR_WORKSPACE. */
+ *   other than 8 or 32 or for a list of 2^24 items of 2048 elements (8-bit
+ *   states: 8192) and more; MOE_ERR_WORKSPACE.  moe_adamw is ordered after it. */
 int moe_adamw_prepare(const moe_adamw_tensor* tensors, int count, int state_bits,
                       moe_adamw_list* out, void* ws, size_t ws_bytes, void* stream);
 

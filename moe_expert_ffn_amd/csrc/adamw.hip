@@ -331,6 +331,10 @@ int launch_adamw_table(const moe_adamw_tensor* t, int count, moe_adamw_list* out
   long long elements = 0;
   for (int i = 0; i < count; ++i) elements += t[i].n;
   out->item = bits == 8 && elements >= 2048ll * 4 * kAdamPass ? 4 * kAdamPass : kAdamPass;
+  // an item is a workgroup, and a launch holds fewer than 2^32 threads
+  long long all = 0;
+  for (int i = 0; i < count; ++i) all += (t[i].n + out->item - 1) / out->item;
+  if (all >= (1ll << 32) / kAdamThreads) return MOE_ERR_UNSUPPORTED;
   uint32_t total = 0;
   for (int base = 0; base < count; base += kAdamPart) {
     AdamPart part{};

@@ -40,6 +40,14 @@ template <int L, typename V, typename Op> MOE_DEV V group_all(V v, Op op) {
   return v;
 }
 
+// Orders a wave's LDS accesses between its lanes: the hardware keeps them in order, the compiler has
+// to be told that another lane may have written.
+MOE_DEV void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 MOE_DEV float elem_f(uint16_t h) { return bf2f(h); }
 MOE_DEV float elem_f(float f) { return f; }
 MOE_DEV void elem_set(uint16_t& o, float f) { o = f2bf(f); }
@@ -82,7 +90,9 @@ template <typename T, int N> MOE_DEV void store_n(T* p, const T* v) {
 // piece, after settle_piece, the rest of the row and zeros.  The load itself has no branch on the
 // lane: a short piece reads the row's last N elements, and settle_piece moves them down once they
 // are used.  (With the short piece loaded one by one in a branch, every further load waited for it:
-// 8192 x 2047 took a third longer than 8192 x 2048.)
+// 8192 x 2047 took a third longer than 8192 x 2048.)  settle_piece also waits for the load: the
+// elements it read belong to another lane, which may write an output over them; call it before the
+// barrier (or in the wave) that the outputs come after.
 template <typename T, int N> MOE_DEV void load_piece(const T* row, int c, int d, T* v) {
   if (d >= N) {                                          // the whole launch
     load_n<T, N>(row + min(c, d - N), v);
@@ -96,6 +106,8 @@ template <typename T, int N> MOE_DEV void settle_piece(int c, int d, T* v) {
   if (c + N <= d || d < N) return;
   uint32_t w[W];
   __builtin_memcpy(w, v, sizeof w);
+#pragma unroll
+  for (int i = 0; i < W; ++i) asm volatile("" : "+v"(w[i]));
   const int bytes = min(c + N - d, N) * (int)sizeof(T);  // N: the piece lies behind the row
 #pragma unroll
   for (int s = W; s > 0; s >>= 1)

@@ -24,6 +24,7 @@ struct NormArgs {
   float* part_g;
   size_t ldx, ldu, ldgo, ldgr, ldr, ldn;
   int T, d, w32, kind;
+  int row0;            // forward: the launch's first row
   float alpha, eps, inv_d;
 };
 
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(RowsOf<NT>::WG) void k_norm(NormArgs a) {
   constexpr int RPW = RowsOf<NT>::RPW;
   __shared__ float red[16];
   const int li = threadIdx.x % NT;
-  const size_t t = (size_t)blockIdx.x * RPW + threadIdx.x / NT;
+  const size_t t = a.row0 + (size_t)blockIdx.x * RPW + threadIdx.x / NT;
   if (t >= (size_t)a.T) return;                          // only where a row has no barrier
   const float g_row = a.alpha * (a.kind == MOE_GATE_TOKEN ? a.gate[t] : 1.f);
   const T* x = (const T*)a.x + t * a.ldx;
@@ -294,8 +295,23 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
       if constexpr (!OUT) __builtin_memcpy(kept, &cur[0][2], sizeof kept);
       fetch(t + step);
     }
+    auto settle_more = [&](T (*own)[VE], int c) {
+      settle_piece<T, VE>(c, a.d, own[0]);
+      settle_piece<T, VE>(c, a.d, own[1]);
+    };
+    if constexpr (AHEAD && !OUT) {
+      settle_more(kept[0], li * VE);
+    } else if constexpr (!OUT && !LATE) {
+#pragma unroll
+      for (int q = 0; q < KC; ++q) settle_more(&cur[q][2], (li + q * NT) * VE);
+    }
     s = row_join(s);
-    if constexpr (LATE) fetch_more(t);
+    if constexpr (LATE && !OUT) {
+      fetch_more(t);
+#pragma unroll
+      for (int q = 0; q < KC; ++q) settle_more(&cur[q][2], (li + q * NT) * VE);
+      __syncthreads();
+    }
     if constexpr (OUT && !FEAT) {
       if (on && a.kind == MOE_GATE_TOKEN && li == 0) a.dgate[t] = a.alpha * s;
       s *= gr_;
@@ -313,19 +329,16 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
         if constexpr (!OUT) {
           T(*own)[VE] = AHEAD ? kept[AHEAD ? q : 0] : &cur[q][2];
           if (a.gr) {
-            float more[VE];
-            settle_f<T, VE>(c, a.d, own[0], more);
 #pragma unroll
-            for (int i = 0; i < VE; ++i) dx[i] += more[i];
+            for (int i = 0; i < VE; ++i) dx[i] += elem_f(own[0][i]);
           }
           if (a.u) {
             float g[VE], du[VE], uu[VE];
             g_of(c, gr_, g);
-            settle_f<T, VE>(c, a.d, own[1], uu);
 #pragma unroll
             for (int i = 0; i < VE; ++i) {
               du[i] = g[i] * dx[i];
-              uu[i] *= dx[i];
+              uu[i] = elem_f(own[1][i]) * dx[i];
               if constexpr (!FEAT) b += uu[i];
             }
             if constexpr (FEAT) add_to(1, q, uu);
@@ -444,11 +457,18 @@ template <class F, typename... A> static void norm_kind(int dtype, int d, A&&...
 
 struct NormFwd {
   template <typename T, int VE, int NT, int KC>
-  static void go(const NormArgs& a, bool out, hipStream_t st) {
+  static void go(NormArgs a, bool out, hipStream_t st) {
     constexpr int RPW = RowsOf<NT>::RPW, WG = RowsOf<NT>::WG;
-    const dim3 grid((unsigned)(((size_t)a.T + RPW - 1) / RPW));
-    if (out) hipLaunchKernelGGL((k_norm<T, VE, NT, KC, true>), grid, dim3(WG), 0, st, a);
-    else hipLaunchKernelGGL((k_norm<T, VE, NT, KC, false>), grid, dim3(WG), 0, st, a);
+    // a launch holds fewer than 2^32 threads: more rows go in several
+    constexpr int most = (1 << 30) / WG * RPW;
+    for (const int T_ = a.T; ; a.row0 += most) {
+      const int rows = std::min(T_ - a.row0, most);
+      a.T = a.row0 + rows;
+      const dim3 grid((unsigned)((rows + RPW - 1) / RPW));
+      if (out) hipLaunchKernelGGL((k_norm<T, VE, NT, KC, true>), grid, dim3(WG), 0, st, a);
+      else hipLaunchKernelGGL((k_norm<T, VE, NT, KC, false>), grid, dim3(WG), 0, st, a);
+      if (a.T == T_) return;
+    }
   }
 };
 

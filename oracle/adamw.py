@@ -22,9 +22,10 @@ def _mix(x):
     return x ^ (x >> 15)
 
 
-def words(seed, step, tensor, n):
+def words(seed, step, tensor, n, start=0):
+    """Of elements start .. start + n."""
     key = _mix((seed + step * GOLD + tensor * ROOT3) & _M)
-    i = np.arange(n, dtype=np.uint64)
+    i = np.arange(start, start + n, dtype=np.uint64)
     x = (i * np.uint64(GOLD) + np.uint64(key)) & np.uint64(_M)
     x = x ^ (x >> np.uint64(16))
     x = (x * np.uint64(ROOT2)) & np.uint64(_M)

@@ -132,6 +132,8 @@ def test_adamw_refusals():
     assert lib.moe_adamw_prepare(arr, 1, 32, ctypes.byref(B.AdamwList()), P, 1 << 20, None) == ARG
     arr = (B.AdamwTensor * 1)(B.AdamwTensor(p=4096, g=8192, m=12288, v=16384, n=(1 << 43) + 1))
     assert lib.moe_adamw_prepare(arr, 1, 32, ctypes.byref(B.AdamwList()), P, 1 << 20, None) == UNSUP
+    arr = (B.AdamwTensor * 1)(B.AdamwTensor(p=1 << 50, g=1 << 51, m=1 << 52, v=1 << 53, n=(1 << 24) * 2048))
+    assert lib.moe_adamw_prepare(arr, 1, 32, ctypes.byref(B.AdamwList()), P, 1 << 20, None) == UNSUP
     assert lib.moe_adamw_prepare(None, 1, 32, ctypes.byref(B.AdamwList()), P, 1 << 20, None) == ARG
     assert lib.moe_adamw_workspace_size(-1) == 0 and lib.moe_adamw_workspace_size(4097) == 0
     L = B.AdamwList(256, 1, 32, 0)

@@ -236,6 +236,30 @@ def test_eight_bit_states_follow_slow_changes():
     assert -0.01 < v.mean() - 1 < 0.125
 
 
+def test_elements_past_2_to_the_31():
+    say("[adamw-far]")
+    n, tail = (1 << 31) + 1000, 1000
+    s = {"p": [torch.zeros(n, device=DEV)], "g": [torch.zeros(n, dtype=BF16, device=DEV)],
+         "m": [torch.zeros(n, dtype=torch.uint8, device=DEV)], "v": [torch.zeros(n, dtype=torch.uint8, device=DEV)],
+         "m_scale": [torch.zeros(-(-n // 128), device=DEV)], "v_scale": [torch.zeros(-(-n // 128), device=DEV)]}
+    s["g"][0][-tail:] = torch.randn(tail, device=DEV).to(BF16)
+    B.adamw(B.make_adamw(**s), lr=1e-3, step=1, seed=4, **HY)
+    torch.cuda.synchronize()
+    start = n - tail
+    assert start % 128 == 0
+    g = _np(s["g"][0][start:])
+    p, m, v = oadam.step(0 * g, g, 0 * g, 0 * g, 1, 1e-3, 0.9, 0.999, 1e-8, 0.1)
+    assert (np.abs(_np(s["p"][0][start:]) - p) <= 40 * U * np.abs(p)).all()
+    word = oadam.words(4, 1, 0, tail, start)
+    for x, name, u16 in ((m, "m", word & 0xFFFF), (np.sqrt(v), "v", word >> 16)):
+        codes, scales, dist = oadam.encode(x, u16)
+        got = _np(s[name][0][start:])
+        # x in 32 bits is off by 8 u, 16 units of the sum that is cut: 16 * 16 u with the quotient's
+        assert (got == codes)[dist > 2.0 ** -14].all() and (dist > 2.0 ** -14).mean() > 0.99
+        np.testing.assert_allclose(_np(s[name + "_scale"][0][start // 128:]), scales, rtol=16 * U)
+    assert (s["p"][0][:start:4097] == 0).all() and (s["m"][0][:start:4097] == 0).all()
+
+
 def test_lists_that_are_empty_or_long():
     say("[adamw-long]")
     B.adamw(B.make_adamw([], [], [], []), lr=1.0, step=1)

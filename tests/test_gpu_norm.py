@@ -19,7 +19,10 @@ HALF = {torch.float32: U, torch.bfloat16: 2.0 ** -8}
 EPS = 1e-6
 
 
-def _rows(rng, T, d, dtype, pad=0, off=0):
+def _rows(rng, T, d, dtype, pad=0, off=0, big=False):
+    if big:                                                       # only the rows are written
+        out = torch.empty((T, d + pad), dtype=dtype, device=DEV)[:, off:off + d]
+        return out.copy_(_rows(rng, T, d, dtype))
     full = torch.from_numpy(rng.standard_normal((T, d + pad)).astype(np.float32)).to(dtype).to(DEV)
     return full[:, off:off + d]
 
@@ -61,15 +64,15 @@ def test_norm_out(T, d, dtype, wide, kind):
     _norm_out(T, d, dtype, wide, kind)
 
 
-def _norm_in(T, d, dtype, wide, kind, pad=0, off=0, residual=True):
+def _norm_in(T, d, dtype, wide, kind, pad=0, off=0, residual=True, big=False):
     say(f"[norm_in] T={T} d={d} {dtype} w32={wide} gate={kind} pad={pad} residual={residual}")
     rng = np.random.default_rng(T * 17 + d)
-    x, dn, dr = (_rows(rng, T, d, dtype, pad, off) for _ in range(3))
-    u = _rows(rng, T, d, dtype, pad, off) if residual else None
+    x, dn, dr = (_rows(rng, T, d, dtype, pad, off, big) for _ in range(3))
+    u = _rows(rng, T, d, dtype, pad, off, big) if residual else None
     w = torch.from_numpy(rng.standard_normal(d).astype(np.float32)).to(DEV)
     w = w if wide else w.to(dtype)
     g, alpha, half = _gate(rng, kind, T, d) if residual else None, 0.7, HALF[dtype]
-    new = lambda: _rows(rng, T, d, dtype, pad, off)
+    new = lambda: _rows(rng, T, d, dtype, pad, off, big)
     n, r, rstd = new(), new() if residual else None, torch.full((T,), 9.0, device=DEV)
     B.norm_in(x, w, EPS, n, rstd, u=u, gate=g, alpha=alpha, r=r)
     torch.cuda.synchronize()
@@ -111,14 +114,14 @@ def _norm_in(T, d, dtype, wide, kind, pad=0, off=0, residual=True):
         _close("dgate", dg, DG, a32 * (np.abs(Un) * (eDX + (many + 44 * U) * np.abs(DX))).sum(**axis))
 
 
-def _norm_out(T, d, dtype, wide, kind, pad=0, off=0):
+def _norm_out(T, d, dtype, wide, kind, pad=0, off=0, big=False):
     say(f"[norm_out] T={T} d={d} {dtype} w32={wide} gate={kind} pad={pad}")
     rng = np.random.default_rng(T * 13 + d)
-    y, x, do = (_rows(rng, T, d, dtype, pad, off) for _ in range(3))
+    y, x, do = (_rows(rng, T, d, dtype, pad, off, big) for _ in range(3))
     w = torch.from_numpy(rng.standard_normal(d).astype(np.float32)).to(DEV)
     w = w if wide else w.to(dtype)
     g, alpha, half = _gate(rng, kind, T, d), -1.3, HALF[dtype]
-    new = lambda: _rows(rng, T, d, dtype, pad, off)
+    new = lambda: _rows(rng, T, d, dtype, pad, off, big)
     out, rstd = new(), torch.full((T,), 9.0, device=DEV)
     B.norm_out(y, x, w, EPS, out, rstd, gate=g, alpha=alpha)
     torch.cuda.synchronize()
@@ -167,6 +170,13 @@ def test_many_tokens():
     _norm_out(9001, 512, torch.float32, True, "token")
 
 
+def test_offsets_past_32_bits():
+    """Rows far apart in buffers of more than 2^32 bytes."""
+    say("[norm-far]")
+    _norm_in(600, 129, torch.bfloat16, True, "feature", pad=4_000_000, off=7, big=True)
+    _norm_out(600, 129, torch.bfloat16, True, "token", pad=4_000_000, off=7, big=True)
+
+
 def test_zero_rows_and_rows_that_are_not_finite_stay_alone():
     say("[norm-odd]")
     T, d = 6, 256
@@ -201,7 +211,7 @@ def test_zero_rows_and_rows_that_are_not_finite_stay_alone():
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("d", [96, 2048, 7168])
+@pytest.mark.parametrize("d", [3, 96, 509, 2047, 7168, 8199, 12001])
 def test_norms_in_place_repeat_and_replay(dtype, d):
     say(f"[norm-inplace] {dtype} d={d}")
     T = 700

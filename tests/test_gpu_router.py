@@ -123,9 +123,10 @@ def test_router_strided_rows(dtype, pad, offset):
 
 @pytest.mark.parametrize("E", [8, 100, 256, 700])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
-def test_router_ties_extremes_and_masks(E, score):
-    say(f"[router-odd] E={E} {score}")
-    inf, low = float("inf"), torch.finfo(torch.float32).min
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_router_ties_extremes_and_masks(E, score, dtype):
+    say(f"[router-odd] E={E} {score} {dtype}")
+    inf, low = float("inf"), torch.finfo(dtype).min
     k = 4
     rows = [[0.0] * E,                                            # all equal: the lowest indexes
             [-0.0 if e % 2 else 0.0 for e in range(E)],           # -0 equals 0
@@ -136,12 +137,12 @@ def test_router_ties_extremes_and_masks(E, score):
             [0.0] * (E - 1) + [inf],
             [80.0] + [-80.0] * (E - 1),
             [-300.0 - e % 7 for e in range(E)]]                   # sigmoid underflows in 32 bits
-    logits = torch.tensor(rows, dtype=torch.float32, device=DEV)
+    logits = torch.tensor(rows, dtype=dtype, device=DEV)
     mask = torch.ones(len(rows), dtype=torch.uint8, device=DEV)
     T = len(rows)
     for renorm in (True, False):
         for m in (None, mask, torch.tensor([1, 1, 1, 1, 0, 0, 0, 1, 0], dtype=torch.bool, device=DEV)):
-            R = B.make_router(E, k, torch.float32, score, renorm)
+            R = B.make_router(E, k, dtype, score, renorm)
             out, st = _forward(R, logits, m)
             l = logits.double().cpu().numpy()
             mn = None if m is None else m.cpu().numpy()
@@ -155,14 +156,15 @@ def test_router_ties_extremes_and_masks(E, score):
             np.testing.assert_allclose(out["prob_sum"].cpu().numpy(), o["prob_sum"], rtol=6200 * U,
                                        atol=1e-37)
             h = torch.ones((T, k), device=DEV)
-            d = torch.full((T, E), 9.0, device=DEV)
+            d = torch.full((T, E), 9.0, dtype=dtype, device=DEV)
             B.router_backward(R, logits, out, h, torch.tensor([0.5, 0.0], device=DEV), d, mask=m)
             torch.cuda.synchronize()
             with np.errstate(all="ignore"):
                 ref = orouter.backward(l, o["topk_ids"], np.ones((T, k)), o["counts"], o["live"], 0.5,
                                        0.0, score == "sigmoid", renorm, mn)
-            # h terms up to 2 k = 8, the same relative error
-            np.testing.assert_allclose(d.cpu().numpy(), ref, rtol=0, atol=6200 * U * 16)
+            # h terms up to 2 k = 8, the same relative error, and half a step of the output's type
+            np.testing.assert_allclose(d.double().cpu().numpy(), ref, rtol=HALF[dtype] * 1.01,
+                                       atol=6200 * U * 16)
 
 
 def test_router_nothing_routed_and_no_tokens():
@@ -255,6 +257,43 @@ def test_router_is_repeatable_on_a_side_stream_and_in_a_graph():
     g.replay()
     for a, b in zip(outs(), ref):
         assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits():
+    """Rows far apart and far into their buffers: the last bytes lie beyond 2^32."""
+    say("[router-far]")
+    rng = np.random.default_rng(10)
+    T, E, k, ld = 1100, 72, 4, 1 << 20
+    logits = torch.empty((T, ld), dtype=torch.float32, device=DEV)[:, 5:5 + E]
+    logits.copy_(_logits(rng, T, E, torch.float32))
+    assert T * ld * 4 > 1 << 32
+    R, out, o = _check_forward(logits, k, "softmax", True)
+    dlogits = torch.empty((T, ld), dtype=torch.float32, device=DEV)[:, 3:3 + E]
+    _check_backward(R, logits, out, o, torch.randn((T, k), device=DEV), None, "softmax", True, dlogits=dlogits)
+    del logits, dlogits
+    slots, d_ff = 600_000, 2048
+    z = torch.empty((slots, 2 * d_ff), dtype=torch.bfloat16, device=DEV)
+    dz = torch.empty_like(z)
+    at = [0, slots // 2, slots - 1]
+    for s in at:
+        z[s].normal_()
+        dz[s].normal_()
+    got = torch.empty(3, device=DEV)
+    B.gate_grad(z, dz, torch.tensor(at, dtype=torch.int32, device=DEV), got)
+    torch.cuda.synchronize()
+    for i, s in enumerate(at):
+        u, du = z[s, d_ff:].double(), dz[s, d_ff:].double()
+        assert abs(float(got[i]) - float(u @ du)) <= (d_ff / 16 + 8) * U * float(u.abs() @ du.abs())
+
+
+def test_another_device_is_refused(monkeypatch):
+    R = B.make_router(8, 2)
+    x = torch.zeros((4, 8), device=DEV)
+    out, ws = B.alloc_router(R, 4, DEV), B.router_workspace(R, 4, DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(B.MoeError, match="current device"):
+        B.router_forward(R, x, out, ws, st)
 
 
 # ---- gate gradients: a dot of d_ff products, summed by a lane in turn and a tree of 16:
