@@ -586,7 +586,9 @@ static int router_lanes(int E) { return E <= 64 ? 8 : E <= 128 ? 16 : E <= 256 ?
 
 static int router_grid(int T, int E) {
   const int G = kRouterThreads / router_lanes(E);
-  return std::max(1, std::min((int)(((long long)T + G - 1) / G), kRouterMaxWG));
+  // one workgroup writes the totals itself: two rounds of its rows cost less than the second launch
+  if (T <= 2 * G) return 1;
+  return std::min((int)(((long long)T + G - 1) / G), kRouterMaxWG);
 }
 
 size_t router_ws_bytes(int T, int E) {
