@@ -263,8 +263,7 @@ MOE_DEV void adam8(const AdamArgs& a, const AdamTensor& t, const AdamRates& h, u
   uint16_t o[8];
   if (t.master) {
     store8<float, FULL>(t.master + at, n, p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = f2bf(p[i]);
+    to_elems<8>(p, o);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)

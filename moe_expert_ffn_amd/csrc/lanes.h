@@ -50,8 +50,16 @@ MOE_DEV void wave_lds_order() {
 
 MOE_DEV float elem_f(uint16_t h) { return bf2f(h); }
 MOE_DEV float elem_f(float f) { return f; }
-MOE_DEV void elem_set(uint16_t& o, float f) { o = f2bf(f); }
-MOE_DEV void elem_set(float& o, float f) { o = f; }
+// N (even) values to the rows' type; bf16 in pairs, one instruction each
+template <int N> MOE_DEV void to_elems(const float* v, uint16_t* o) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const bf16x2_t h = __builtin_convertvector(f32x2_t{v[i], v[i + 1]}, bf16x2_t);
+    __builtin_memcpy(o + i, &h, 4);
+  }
+}
+template <int N> MOE_DEV void to_elems(const float* v, float* o) { __builtin_memcpy(o, v, sizeof(float) * N); }
 
 // N consecutive elements in 16-byte (8-byte) pieces.  Global memory takes such accesses at any
 // element's address, so rows of any stride and views of any offset go the same way.

@@ -40,8 +40,7 @@ template <typename T, int VE> MOE_DEV void load_f(const T* row, int c, int d, fl
 }
 template <typename T, int VE> MOE_DEV void store_f(T* row, int c, int d, const float* v) {
   T raw[VE];
-#pragma unroll
-  for (int i = 0; i < VE; ++i) elem_set(raw[i], v[i]);
+  to_elems<VE>(v, raw);
   store_upto<T, VE>(row + c, d - c, raw);
 }
 template <typename T, int VE> MOE_DEV void load_w(const NormArgs& a, int c, float* v) {

@@ -15,6 +15,8 @@ namespace moe {
 constexpr int kRouterThreads = 256;
 constexpr int kRouterMaxWG = 1024;       // workgroups, and so partial sums, of the forward
 constexpr int kTotalThreads = 1024, kTotalCols = 16;
+static_assert(kRouterMaxWG <= kTotalThreads, "a thread for every partial of the totals' small sums");
+static_assert(kMaxExperts <= 64 * kTotalCols, "a lane for every workgroup of the totals");
 
 struct RouterArgs {
   const void* logits;
@@ -510,6 +512,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
     sum = group_all<L>(sum, OpAdd());
     T* out = (T*)a.dlogits + t * a.ld_out;
     T o[V];
+    float x[V];
     if (row_live(sc.top, sum)) {                         // the whole group
       const float inv = inverse(sum);
       float Q = 0.f, pg = 0.f;
@@ -532,19 +535,19 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float x = d[i] + w[i] * (ge[i] - pg - (flag[i] ? hq : rest));
+        x[i] = d[i] + w[i] * (ge[i] - pg - (flag[i] ? hq : rest));
         if constexpr (SCORE == MOE_SCORE_SIGMOID) {
-          x *= away[i];
-          if (zmul != 0.f) x += zs * e[i];
+          x[i] *= away[i];
+          if (zmul != 0.f) x[i] += zs * e[i];
         } else {
-          x += zs * w[i];
+          x[i] += zs * w[i];
         }
-        elem_set(o[i], x);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) elem_set(o[i], 0.f);
+      for (int i = 0; i < V; ++i) x[i] = 0.f;
     }
+    to_elems<V>(x, o);
     store_upto<T, V>(out + c0, a.E - c0, o);
   }
 }
