@@ -83,6 +83,22 @@ def test_router_forward_and_backward(T, E, k, dtype, score, renorm):
     _check_backward(R, logits, out, o, h, dl, score, renorm)
 
 
+@pytest.mark.parametrize("T,E,k,dtype,score", [(8200, 256, 8, torch.bfloat16, "sigmoid"),
+                                               (4100, 400, 5, torch.float32, "softmax"),
+                                               (8300, 157, 12, torch.float32, "sigmoid"),
+                                               (5000, 512, 32, torch.bfloat16, "softmax")])
+def test_router_of_many_rows(T, E, k, dtype, score):
+    """Enough rows for the forward pass that puts 16 experts into a lane."""
+    say(f"[router-many] T={T} E={E} k={k} {dtype} {score}")
+    rng = np.random.default_rng(T)
+    logits = _logits(rng, T, E, dtype, pad=3, offset=1)
+    logits[torch.rand(logits.shape, device=DEV) < 0.02] = float("-inf")
+    mask = torch.from_numpy((rng.random(T) < 0.9).astype(np.uint8)).to(DEV)
+    R, out, o = _check_forward(logits, k, score, True, 1.0, mask)
+    _check_backward(R, logits, out, o, torch.randn((T, k), device=DEV), torch.tensor([0.8, 0.05], device=DEV),
+                    score, True, mask)
+
+
 def _check_backward(R, logits, out, o, h, dl, score, renorm, mask=None, dlogits=None):
     T, E = logits.shape
     if dlogits is None:
