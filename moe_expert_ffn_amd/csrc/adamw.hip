@@ -282,10 +282,10 @@ MOE_DEV void adam8(const AdamArgs& a, const AdamTensor& t, const AdamRates& h, u
 }
 
 // One pass over everything a step touches; a workgroup an item.  Bound by HBM: with 8-bit states,
-// bf16 parameters and fp32 gradients 12.1 bytes an element, 604M elements in 1.35 ms (5.4 TB/s; a
+// bf16 parameters and fp32 gradients 12.1 bytes an element, 604M elements in 1.37 ms (5.3 TB/s; a
 // 1 GiB copy reaches 4.96), with 32-bit states 24 bytes, 2.63 ms (5.5 TB/s).  The 8-bit path issues
-// some 60 VALU cycles-of-four an element, about 1 ms of the chip, which is why codes are converted by
-// hardware, rounded as whole numbers and never divided.  A persistent grid was slower (1.46 ms),
+// some 72 VALU slots an element, about 1.1 ms of the chip, which is why codes are converted by
+// hardware, rounded as whole numbers and never divided.  A persistent grid was 8% slower,
 // non-temporal accesses 3% faster here but 20% slower where the tensors fit the caches.
 template <int BITS>
 __global__ __launch_bounds__(kAdamThreads, 4) void k_adamw(AdamArgs a) {
@@ -325,8 +325,8 @@ int launch_adamw_table(const moe_adamw_tensor* t, int count, moe_adamw_list* out
   const AdamTable tab = adamw_table(out->table, count);
   const int bits = out->state_bits;
   // 32-bit states are bound by HBM at any item; 8-bit ones spend their time in the VALU too, where the
-  // search at a workgroup's start shows: 604M elements 1495 us at 2048, 1354 at 8192 (1376 at 16384),
-  // 20M 47.8 and 45.5; 5M 17.7 at 2048 and 20.7 at 8192, which leaves too few workgroups.
+  // search at a workgroup's start shows: 604M elements 1598 us at 2048, 1499 at 8192 (1481 at 16384),
+  // 20M 53.3 and 50.1 (52.5); 5M 20.3 at 2048 and 22.3 at 8192, which leaves too few workgroups.
   long long elements = 0;
   for (int i = 0; i < count; ++i) elements += t[i].n;
   out->item = bits == 8 && elements >= 2048ll * 4 * kAdamPass ? 4 * kAdamPass : kAdamPass;

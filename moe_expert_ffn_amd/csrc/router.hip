@@ -173,7 +173,11 @@ MOE_DEV float block_sum(float s, float* red, int waves) {
 // Forward.  Each group takes rows in turn; its lanes keep the sums of P of
 // their own experts in registers, so the sums' order is fixed by the grid,
 // which follows from T and E alone.  One workgroup writes the totals itself;
-// more leave partial sums for k_router_totals.
+// more leave partial sums for k_router_totals.  16 x 128 bf16, k 8: 3.9 us, the
+// latency of one row; 8192 x 128 fp32 6.6 us (4.2 MB, 0.85 us at HBM's rate) and
+// 65521 x 256 bf16 36 us (33.5 MB): bound by the VALU, some 40 instructions a
+// choice and wave of two or four rows, 35 a logit of a lane.  The next row is
+// fetched while this one is worked on.
 template <typename T, int L, int V, int SCORE>
 __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
   constexpr int G = kRouterThreads / L;                  // rows at a time
@@ -342,7 +346,8 @@ __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
 
 // Totals of the workgroups' partial sums.  A workgroup takes 16 experts, 64
 // strands of partials joined through LDS; the last one to finish joins their
-// products c_e prob_sum_e, in order, into the losses.
+// products c_e prob_sum_e, in order, into the losses.  3.5-4.5 us at 512 partials
+// of 128 experts, latency alone (one workgroup for all: 11 us).
 __global__ __launch_bounds__(kTotalThreads) void k_router_totals(RouterArgs a) {
   constexpr int S = kTotalThreads / kTotalCols;
   __shared__ float sp[S][kTotalCols];
@@ -420,7 +425,11 @@ __global__ __launch_bounds__(kTotalThreads) void k_router_totals(RouterArgs a) {
 // Backward: the row's scores again from its logits (they have to be read for
 // it in any case), every term in registers, one pass.  The k gate gradients
 // reach the lanes of their experts through LDS, a row's C places zeroed,
-// written and read by the row's own lanes (LDS keeps a wave's order).
+// written and read by the row's own lanes (LDS keeps a wave's order).  4096 x 64
+// fp32 4.7 us; 65521 x 256 bf16 with sigmoid scores and a z loss 32.6 us (71 MB, 14
+// at HBM's rate): bound by the VALU, about 440 instructions and 27 transcendental
+// ones for two rows.  Comparing every expert with every choice instead of LDS,
+// and library exponentials: 105 us.
 template <typename T, int L, int V, int SCORE>
 __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
   constexpr int G = kRouterThreads / L, C = L * V;
