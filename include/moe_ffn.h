@@ -525,7 +525,10 @@ int moe_backward_gates(const moe_layer* L, const void* x, const float* gates, co
  *   after the block:   out = x + alpha g w y / rms(y)
  * Sums are fp32, over a row and over the tokens in a fixed order; r's rounding
  * does not enter n.  An output may be the same memory as an input with the same
- * row stride. */
+ * row stride.
+ * A row whose token_mask (nullable) is 0 is padding, and passes the stream alone,
+ * whatever it, u, y and the gradients hold there: r = x, n = 0, out = x, rstd = 0;
+ * dx = dr, du = dy = 0, a token's dgate 0, nothing to dw or a feature's dgate. */
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_FEATURE = 2 } moe_gate_kind;
 typedef struct {
   int T, d;
@@ -534,6 +537,7 @@ typedef struct {
   float alpha, eps;
   const void* w;
   const float* gate;
+  const uint8_t* token_mask;
 } moe_norm;
 
 /* Workspace of the norms' backward passes; 0 for invalid arguments. */
@@ -629,7 +633,8 @@ size_t moe_adamw_workspace_size(int tensors);
  *   tensor that is not bf16, or memory that two of the buffers written or a
  *   buffer written and a gradient share; MOE_ERR_UNSUPPORTED for state_bits
  *   other than 8 or 32 or for a list of 2^24 items of 2048 elements (8-bit
- *   states: 8192) and more; MOE_ERR_WORKSPACE.  moe_adamw is ordered after it. */
+ *   states: 8192) and more; MOE_ERR_WORKSPACE.  A moe_adamw on another stream has
+ *   to be ordered after it by the caller. */
 int moe_adamw_prepare(const moe_adamw_tensor* tensors, int count, int state_bits,
                       moe_adamw_list* out, void* ws, size_t ws_bytes, void* stream);
 

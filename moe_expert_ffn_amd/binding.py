@@ -75,7 +75,8 @@ class Router(ctypes.Structure):
 class Norm(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int), ("d", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("w_dtype", ctypes.c_int), ("gate_kind", ctypes.c_int), ("alpha", ctypes.c_float),
-                ("eps", ctypes.c_float), ("w", ctypes.c_void_p), ("gate", ctypes.c_void_p)]
+                ("eps", ctypes.c_float), ("w", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("token_mask", ctypes.c_void_p)]
 
 
 class AdamwTensor(ctypes.Structure):
@@ -574,6 +575,15 @@ def _vector(t, n, dtype, name):
                        f"{tuple(t.shape)} of {t.dtype}")
 
 
+def _mask_at(mask, T):
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.uint8, torch.bool):
+        raise MoeError(f"mask: expected uint8 or bool, got {mask.dtype}")
+    _vector(mask, T, mask.dtype, "mask")
+    return mask.data_ptr()
+
+
 _CODES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
@@ -614,10 +624,7 @@ def _router_args(router, logits, mask):
     T = logits.shape[0]
     dt = torch.float32 if router.dtype == MOE_F32 else torch.bfloat16
     ld = _rows(logits, T, router.E, dt, "logits")
-    if mask is not None:
-        if mask.dtype not in (torch.uint8, torch.bool):
-            raise MoeError(f"mask: expected uint8 or bool, got {mask.dtype}")
-        _vector(mask, T, mask.dtype, "mask")
+    _mask_at(mask, T)
     return T, ld, dt
 
 
@@ -683,7 +690,7 @@ def norm_workspace(T, d, device) -> torch.Tensor:
     return torch.empty(n + 256, dtype=torch.uint8, device=device)
 
 
-def _norm_desc(rows, w, gate, alpha, eps, name):
+def _norm_desc(rows, w, gate, alpha, eps, mask, name):
     """The moe_norm of rows [T][d] of the tensor `rows`, and their row stride."""
     if rows.dim() != 2:
         raise MoeError(f"{name}: expected [T][d], got {tuple(rows.shape)}")
@@ -704,7 +711,7 @@ def _norm_desc(rows, w, gate, alpha, eps, name):
             raise MoeError(f"gate: expected {(T, 1)} or {(d,)}, got {tuple(gate.shape)}")
         _vector(gate, 0, torch.float32, "gate")
     N = Norm(T, d, code, w_code, kind, alpha, eps, w.data_ptr(),
-             None if gate is None else gate.data_ptr())
+             None if gate is None else gate.data_ptr(), _mask_at(mask, T))
     return N, T, d, _rows(rows, T, d, rows.dtype, name)
 
 
@@ -714,10 +721,11 @@ def _opt_rows(t, T, d, dtype, name):
     return t.data_ptr(), _rows(t, T, d, dtype, name)
 
 
-def norm_in(x, w, eps, n, rstd, u=None, gate=None, alpha=1.0, r=None):
-    """Before the block: r = x + alpha gate u, n = w r / rms(r); rstd [T] for the backward pass."""
-    st = _here(x, w, n, rstd, u, gate, r)
-    N, T, d, ldx = _norm_desc(x, w, gate, alpha, eps, "x")
+def norm_in(x, w, eps, n, rstd, u=None, gate=None, alpha=1.0, r=None, mask=None):
+    """Before the block: r = x + alpha gate u, n = w r / rms(r); rstd [T] for the backward pass.
+    mask [T]: 0 where a row is padding (r = x, n = 0); the gradients take the same."""
+    st = _here(x, w, n, rstd, u, gate, r, mask)
+    N, T, d, ldx = _norm_desc(x, w, gate, alpha, eps, mask, "x")
     _vector(rstd, T, torch.float32, "rstd")
     _check(load().moe_norm_in(ctypes.byref(N), _at(x), ldx, *_opt_rows(u, T, d, x.dtype, "u"),
                               *_opt_rows(r, T, d, x.dtype, "r"), _at(n),
@@ -733,10 +741,10 @@ def _norm_grads(T, d, gate, dw, dgate, ws):
 
 
 def norm_in_backward(dn, r, w, rstd, dx, dw, ws, dr=None, u=None, gate=None, alpha=1.0, du=None,
-                     dgate=None):
+                     dgate=None, mask=None):
     """Gradients of norm_in: dx (r's and x's), dw, and with u also du and dgate (shaped like gate)."""
-    st = _here(dn, r, w, rstd, dx, dw, ws, dr, u, gate, du, dgate)
-    N, T, d, ldr = _norm_desc(r, w, gate, alpha, 1.0, "r")
+    st = _here(dn, r, w, rstd, dx, dw, ws, dr, u, gate, du, dgate, mask)
+    N, T, d, ldr = _norm_desc(r, w, gate, alpha, 1.0, mask, "r")
     dt = r.dtype
     _vector(rstd, T, torch.float32, "rstd")
     wsp, wsn = _norm_grads(T, d, gate, dw, dgate, ws)
@@ -748,10 +756,11 @@ def norm_in_backward(dn, r, w, rstd, dx, dw, ws, dr=None, u=None, gate=None, alp
     return dx
 
 
-def norm_out(y, x, w, eps, out, rstd, gate=None, alpha=1.0):
-    """After the block: out = x + alpha gate w y / rms(y); rstd [T] for the backward pass."""
-    st = _here(y, x, w, out, rstd, gate)
-    N, T, d, ldy = _norm_desc(y, w, gate, alpha, eps, "y")
+def norm_out(y, x, w, eps, out, rstd, gate=None, alpha=1.0, mask=None):
+    """After the block: out = x + alpha gate w y / rms(y); rstd [T] for the backward pass.
+    mask [T]: 0 where a row is padding (out = x); the gradients take the same."""
+    st = _here(y, x, w, out, rstd, gate, mask)
+    N, T, d, ldy = _norm_desc(y, w, gate, alpha, eps, mask, "y")
     _vector(rstd, T, torch.float32, "rstd")
     _check(load().moe_norm_out(ctypes.byref(N), _at(y), ldy, _at(x),
                                _rows(x, T, d, y.dtype, "x"), _at(out),
@@ -759,10 +768,10 @@ def norm_out(y, x, w, eps, out, rstd, gate=None, alpha=1.0):
     return out
 
 
-def norm_out_backward(dout, y, w, rstd, dy, dw, ws, gate=None, alpha=1.0, dgate=None):
+def norm_out_backward(dout, y, w, rstd, dy, dw, ws, gate=None, alpha=1.0, dgate=None, mask=None):
     """Gradients of norm_out: dy, dw and dgate (shaped like gate); x's is dout."""
-    st = _here(dout, y, w, rstd, dy, dw, ws, gate, dgate)
-    N, T, d, ldy = _norm_desc(y, w, gate, alpha, 1.0, "y")
+    st = _here(dout, y, w, rstd, dy, dw, ws, gate, dgate, mask)
+    N, T, d, ldy = _norm_desc(y, w, gate, alpha, 1.0, mask, "y")
     _vector(rstd, T, torch.float32, "rstd")
     wsp, wsn = _norm_grads(T, d, gate, dw, dgate, ws)
     _check(load().moe_norm_out_backward(

@@ -14,6 +14,7 @@ struct NormArgs {
   const void* u;       // before: what the stream takes up (nullable); after: y
   const void* w;
   const float* gate;
+  const uint8_t* mask; // rows that are not padding (nullable: all)
   const void* go;      // backward: the gradient of the output
   const void* gr;      // backward: what reaches r from elsewhere (nullable)
   void* r;             // forward: the updated stream (nullable).  backward: du
@@ -87,6 +88,7 @@ __global__ __launch_bounds__(RowsOf<NT>::WG) void k_norm(NormArgs a) {
   const size_t t = a.row0 + (size_t)blockIdx.x * RPW + threadIdx.x / NT;
   if (t >= (size_t)a.T) return;                          // only where a row has no barrier
   const float g_row = a.alpha * (a.kind == MOE_GATE_TOKEN ? a.gate[t] : 1.f);
+  const bool live = !a.mask || a.mask[t];                // padding may hold NaN: chosen away, not multiplied
   const T* x = (const T*)a.x + t * a.ldx;
   const T* u = (const T*)a.u + t * a.ldu;
   // before the block: x and u make v; after: v is u, x is added at the end
@@ -114,7 +116,7 @@ __global__ __launch_bounds__(RowsOf<NT>::WG) void k_norm(NormArgs a) {
         settle_f<T, VE>(c, a.d, ru[q], uu);
         load_g<VE>(a, c, g);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) v[q][i] += g[i] * g_row * uu[i];
+        for (int i = 0; i < VE; ++i) v[q][i] += live ? g[i] * g_row * uu[i] : 0.f;
       }
     }
 #pragma unroll
@@ -126,7 +128,7 @@ __global__ __launch_bounds__(RowsOf<NT>::WG) void k_norm(NormArgs a) {
     if (OUT) load_g<VE>(a, li * VE, gs);
   }
   s = row_sum<NT>(s, red);
-  const float rstd = 1.f / sqrtf(s * a.inv_d + a.eps);
+  const float rstd = live ? 1.f / sqrtf(s * a.inv_d + a.eps) : 0.f;
   if (li == 0) a.rstd[t] = rstd;
 #pragma unroll
   for (int q = 0; q < KC; ++q) {
@@ -140,11 +142,11 @@ __global__ __launch_bounds__(RowsOf<NT>::WG) void k_norm(NormArgs a) {
       if constexpr (KC == 1) __builtin_memcpy(g, gs, sizeof g);
       else load_g<VE>(a, c, g);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) o[i] = xs[q][i] + g[i] * g_row * (v[q][i] * rstd * w[i]);
+      for (int i = 0; i < VE; ++i) o[i] = xs[q][i] + (live ? g[i] * g_row * (v[q][i] * rstd * w[i]) : 0.f);
     } else {
       if (a.r) store_f<T, VE>((T*)a.r + t * a.ldr, c, a.d, v[q]);
 #pragma unroll
-      for (int i = 0; i < VE; ++i) o[i] = v[q][i] * rstd * w[i];
+      for (int i = 0; i < VE; ++i) o[i] = live ? v[q][i] * rstd * w[i] : 0.f;
     }
     store_f<T, VE>((T*)a.n + t * a.ldn, c, a.d, o);
   }
@@ -219,6 +221,7 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
   const size_t step = (size_t)gridDim.x * RPW;
   T cur[KC][IN][VE];
   float rstd = 0.f, g_row = a.alpha;
+  bool live = true;
   auto fetch_more = [&](size_t t) {
 #pragma unroll
     for (int q = 0; q < KC; ++q) {
@@ -233,6 +236,7 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
   auto fetch = [&](size_t t) {
     if (t >= (size_t)a.T) return;
     rstd = a.rstd[t];
+    if (a.mask) live = a.mask[t];
     if (a.kind == MOE_GATE_TOKEN) g_row = a.alpha * a.gate[t];
 #pragma unroll
     for (int q = 0; q < KC; ++q) {
@@ -265,7 +269,8 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
     if constexpr (!AHEAD) fetch(t);
     float xh[KC][VE], p[KC][VE];       // x / rms, and the gradient of that
     float s = 0.f;
-    if (on) {
+    const bool use = on && live;       // padding adds to no sum and its own terms are 0
+    if (use) {
 #pragma unroll
       for (int q = 0; q < KC; ++q) {
         const int c = (li + q * NT) * VE;
@@ -330,7 +335,7 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
         if (c >= a.d) continue;
         float dx[VE];
 #pragma unroll
-        for (int i = 0; i < VE; ++i) dx[i] = rs * (p[q][i] - xh[q][i] * mean);
+        for (int i = 0; i < VE; ++i) dx[i] = use ? rs * (p[q][i] - xh[q][i] * mean) : 0.f;
         if constexpr (!OUT) {
           T(*own)[VE] = AHEAD ? kept[AHEAD ? q : 0] : &cur[q][2];
           if (a.gr) {
@@ -342,8 +347,8 @@ __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {
             g_of(c, gr_, g);
 #pragma unroll
             for (int i = 0; i < VE; ++i) {
-              du[i] = g[i] * dx[i];
-              uu[i] = elem_f(own[1][i]) * dx[i];
+              du[i] = use ? g[i] * dx[i] : 0.f;
+              uu[i] = use ? elem_f(own[1][i]) * dx[i] : 0.f;
               if constexpr (!FEAT) b += uu[i];
             }
             if constexpr (FEAT) add_to(1, q, uu);
@@ -509,7 +514,7 @@ struct NormBwd {
 
 static NormArgs norm_args(const moe_norm& N) {
   NormArgs a{};
-  a.w = N.w; a.gate = N.gate; a.T = N.T; a.d = N.d; a.kind = N.gate_kind;
+  a.w = N.w; a.gate = N.gate; a.mask = N.token_mask; a.T = N.T; a.d = N.d; a.kind = N.gate_kind;
   a.w32 = N.w_dtype == MOE_F32 ? 1 : 0;
   a.alpha = N.alpha; a.eps = N.eps; a.inv_d = 1.f / (float)N.d;
   return a;

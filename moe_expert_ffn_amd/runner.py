@@ -164,10 +164,11 @@ class BlockRunner(LayerRunner):
             self.dgate = None if gate is None else torch.empty(d, **f32)
 
     def block_forward(self, x, mask=None):
-        """out [T][d] of x [T][d]; mask [T] (optional): 0 where a row is padding, which passes the
-        residual alone.  The routing's losses are in self.routed["losses"]."""
+        """out [T][d] of x [T][d]; mask [T] (optional): 0 where a row is padding, which, whatever it
+        holds, passes the residual alone and reaches no weight's gradient.  The routing's losses are
+        in self.routed["losses"]."""
         self.x, self.mask = x, mask
-        B.norm_in(x, self.w_in, self.eps, self.n, self.rstd_in)
+        B.norm_in(x, self.w_in, self.eps, self.n, self.rstd_in, mask=mask)
         torch.mm(self.n, self.w_router.t(), out=self.logits)
         r = B.router_forward(self.router, self.logits, self.routed, self.router_ws, self.status, mask)
         self.route(r["topk_ids"])
@@ -178,20 +179,20 @@ class BlockRunner(LayerRunner):
         if self.with_backward:                 # the next call rewrites what the plan reads
             self.join_bwd_plan()
         return B.norm_out(self.y, x, self.w_out, self.eps, self.out, self.rstd_out, self.gate,
-                          self.alpha)
+                          self.alpha, mask)
 
     def block_backward(self, dout, dlosses=None):
         """Gradients of block_forward's last call from dout [T][d] and (optional) dlosses [2], those
         of the balance and z losses: dx, and dw1, dw2, dw_router, dw_in, dw_out, dgate in self."""
         r = self.routed
         B.norm_out_backward(dout, self.y, self.w_out, self.rstd_out, self.dy, self.dw_out,
-                            self.norm_ws, self.gate, self.alpha, self.dgate)
+                            self.norm_ws, self.gate, self.alpha, self.dgate, self.mask)
         self.backward(self.n, r["gates"], self.dy, r["topk_ids"], dlogp=self.dlogp)
         B.router_backward(self.router, self.logits, r, self.dlogp, dlosses, self.dlogits, self.mask)
         torch.mm(self.dlogits.t(), self.n, out=self.dw_router)
         torch.addmm(self.dx, self.dlogits, self.w_router, out=self.dn)
         return B.norm_in_backward(self.dn, self.x, self.w_in, self.rstd_in, self.dx_block, self.dw_in,
-                                  self.norm_ws, dr=dout)
+                                  self.norm_ws, dr=dout, mask=self.mask)
 
     def make_optimizer(self, state_bits=32):
         """AdamW states (zeros) for the block's weights; state_bits 32 (fp32) or 8 (e4m3 codes and

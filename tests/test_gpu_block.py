@@ -181,6 +181,34 @@ def test_block_forward_and_backward(name, score, renorm, masked):
         assert err <= (tol if w.act == "f32" or key not in ("dw_router", "dx_block", "dw_in") else 3e-2), key
 
 
+@pytest.mark.parametrize("name", ["small_f32", "small_bf16", "stream_bf16"])
+def test_block_padding_holds_anything(name):
+    """Padding rows of NaN: every weight's gradient, the losses and the other rows stay bit for bit."""
+    w = PATHS[name]
+    say(f"[block-padding] {name}")
+    dl = torch.tensor([0.02, 0.01], device=DEV)
+    mask = torch.ones(w.T, dtype=torch.bool, device=DEV)
+    mask[::7] = False
+    keys = ("out", "dx_block", "dw1", "dw2", "dw_router", "dw_in", "dw_out", "dgate")
+    res = []
+    for pad in (False, True):
+        b, par, x, dout = _block(w, w.T, 11, "softmax", True)
+        dout[~mask] = 0
+        if pad:
+            x[~mask] = float("nan")
+        b.block_forward(x, mask)
+        b.block_backward(dout, dl)
+        torch.cuda.synchronize()
+        assert int(b.status.item()) == 0
+        res.append({k: getattr(b, k).clone() for k in keys} | {"losses": b.routed["losses"].clone()})
+    clean, padded = res
+    assert padded["out"][~mask].isnan().all() and not padded["dx_block"][~mask].any()
+    for k in ("out", "dx_block"):
+        assert torch.equal(padded[k][mask], clean[k][mask]), k
+    for k in ("dw1", "dw2", "dw_router", "dw_in", "dw_out", "dgate", "losses"):
+        assert torch.equal(padded[k], clean[k]), k
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("name", ["small_f32", "stream_bf16"])
 def test_block_trains_and_its_step_replays(name, bits):

@@ -260,3 +260,63 @@ def test_norms_in_place_repeat_and_replay(dtype, d):
         for a, b in zip(outs(), ref):
             assert torch.equal(a, b), rep
         both()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kind", ["none", "token", "feature"])
+@pytest.mark.parametrize("T,d", [(1, 8), (50, 5), (700, 96), (37, 509), (300, 2047), (9, 8199), (5, 12001)])
+def test_padding_rows_hold_anything(dtype, kind, T, d):
+    """NaN in every input of the padding rows: they pass the stream alone, the other rows and the sums
+    over tokens are, bit for bit, those of the same rows with zeros as padding."""
+    say(f"[norm-padding] {dtype} gate={kind} T={T} d={d}")
+    rng = np.random.default_rng(T + d)
+    mask = torch.ones(T, dtype=torch.bool, device=DEV)
+    mask[::3] = False
+    x, u, do, dr = (_rows(rng, T, d, dtype) for _ in range(4))
+    for t in (u, do):
+        t[~mask] = 0
+    fill = lambda t: t.masked_fill(~mask[:, None], float("nan"))
+    g = _gate(rng, kind, T, d)
+    gn = fill(g) if kind == "token" else g
+    w = torch.randn(d, device=DEV)
+    ws = B.norm_workspace(T, d, DEV)
+    rows = lambda: torch.full_like(x, 7)
+    vec = lambda n: torch.full((n,), 7.0, device=DEV)
+
+    def all_of(x, u, do, dr, g, y, mask):
+        n, r, dx, du, out, dy = (rows() for _ in range(6))
+        s, s2, dw, dw2 = vec(T), vec(T), vec(d), vec(d)
+        dg = dg2 = None
+        if g is not None:
+            dg, dg2 = torch.full_like(g, 7), torch.full_like(g, 7)
+        B.norm_in(x, w, EPS, n, s, u=u, gate=g, alpha=0.7, r=r, mask=mask)
+        B.norm_in_backward(do, r, w, s, dx, dw, ws, dr=dr, u=u, gate=g, alpha=0.7, du=du, dgate=dg,
+                           mask=mask)
+        B.norm_out(y, x, w, EPS, out, s2, gate=g, alpha=0.7, mask=mask)
+        B.norm_out_backward(do, y, w, s2, dy, dw2, ws, gate=g, alpha=0.7, dgate=dg2, mask=mask)
+        torch.cuda.synchronize()
+        return dict(n=n, r=r, s=s, dx=dx, du=du, out=out, dy=dy, s2=s2, dw=dw, dw2=dw2, dg=dg, dg2=dg2)
+
+    got = all_of(fill(x), fill(u), fill(do), dr, gn, fill(u), mask.to(torch.uint8))
+    ref = all_of(x, u, do, dr, g, u, None)
+    off = ~mask
+    assert got["r"][off].isnan().all() and got["out"][off].isnan().all()      # x's own
+    assert torch.equal(got["dx"][off], dr[off])
+    for key in ("n", "du", "dy", "s", "s2"):
+        assert not got[key][off].any(), key
+    for key in ("n", "r", "s", "dx", "du", "out", "dy", "s2"):
+        assert torch.equal(got[key][mask], ref[key][mask]), key
+    # zeros add nothing to dw and dgate but to dgate before the block, which takes dr: u is 0 there
+    for key in ("dw", "dw2", "dg", "dg2"):
+        if ref[key] is not None:
+            assert torch.equal(got[key], ref[key]), key
+
+
+def test_padding_mask_is_checked():
+    x, w, s = torch.zeros((4, 8), device=DEV), torch.ones(8, device=DEV), torch.zeros(4, device=DEV)
+    for mask in (torch.ones(3, dtype=torch.uint8, device=DEV), torch.ones(4, device=DEV),
+                 torch.ones(4, dtype=torch.uint8)):
+        with pytest.raises(B.MoeError):
+            B.norm_in(x, w, EPS, x.clone(), s, mask=mask)
+        with pytest.raises(B.MoeError):
+            B.norm_out_backward(x, x, w, s, x.clone(), w.clone(), B.norm_workspace(4, 8, DEV), mask=mask)
