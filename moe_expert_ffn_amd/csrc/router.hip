@@ -145,14 +145,44 @@ template <int L, int V> MOE_DEV float row_top(const float* v) {
 // -infinities anywhere (inf - inf).
 MOE_DEV bool row_live(float top, float sum) { return top < INFINITY && sum < INFINITY; }
 
-// e^(l - top) summed over the row
-template <int L, int V> MOE_DEV float row_exp_sum(const float* v, float top, float* e) {
+// A lane's scores, e^(l - top) among them, and the row's sum of w.  Sigmoid scores of a row whose
+// largest logit is near 0 need no exponential of their own: sigmoid(l) = e / (e + e^-top) with e =
+// e^(l - top), sigmoid(-l) = e^-top / (e + e^-top).  (Off by a rounding of l - top and of top instead of
+// l's; a share below e^-87 becomes 0.)
+constexpr float kNearTop = 16.f;
+template <int L, int V, int SCORE, bool AWAY>
+MOE_DEV float row_scores(const Score<SCORE>& sc, const float* v, float* w, float* e, float* away) {
+  float sum = 0.f;
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[i] = e[i] = exp_of(v[i] - sc.top);
+      sum += w[i];
+    }
+  } else if (fabsf(sc.top) <= kNearTop) {                // the whole group
+    const float et = exp_of(-sc.top);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      e[i] = exp_of(v[i] - sc.top);
+      const float r = inverse(e[i] + et);
+      w[i] = e[i] * r;
+      if constexpr (AWAY) away[i] = et * r;
+      sum += w[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      e[i] = exp_of(v[i] - sc.top);
+      w[i] = sc.weight(v[i], AWAY ? away + i : nullptr);
+      sum += w[i];
+    }
+  }
+  return group_all<L>(sum, OpAdd());
+}
+template <int L, int V> MOE_DEV float lane_sum(const float* e) {
   float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    e[i] = exp_of(v[i] - top);
-    s += e[i];
-  }
+  for (int i = 0; i < V; ++i) s += e[i];
   return group_all<L>(s, OpAdd());
 }
 
@@ -207,16 +237,9 @@ __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
     float* gates = a.gates + t * a.k;
     Score<SCORE> sc_;
     sc_.at_top(row_top<L, V>(v));
-    float lsum = row_exp_sum<L, V>(v, sc_.top, w), sum = lsum;
-    if constexpr (SCORE == MOE_SCORE_SIGMOID) {
-      sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        w[i] = sc_.weight(v[i]);
-        sum += w[i];
-      }
-      sum = group_all<L>(sum, OpAdd());
-    }
+    float e[V];
+    const float sum = row_scores<L, V, SCORE, false>(sc_, v, w, e, nullptr);
+    const float lsum = SCORE == MOE_SCORE_SOFTMAX ? sum : lane_sum<L, V>(e);
     if (!row_live(sc_.top, sum)) {                       // the whole group
       for (int j = li; j < a.k; j += L) {
         ids[j] = -1;
@@ -426,10 +449,11 @@ __global__ __launch_bounds__(kTotalThreads) void k_router_totals(RouterArgs a) {
 // it in any case), every term in registers, one pass.  The k gate gradients
 // reach the lanes of their experts through LDS, a row's C places zeroed,
 // written and read by the row's own lanes (LDS keeps a wave's order).  4096 x 64
-// fp32 4.7 us; 65521 x 256 bf16 with sigmoid scores and a z loss 32.6 us (71 MB, 14
-// at HBM's rate): bound by the VALU, about 440 instructions and 27 transcendental
-// ones for two rows.  Comparing every expert with every choice instead of LDS,
-// and library exponentials: 105 us.
+// fp32 4.7 us; 65521 x 256 bf16 with sigmoid scores and a z loss 27.7 us (71 MB, 14
+// at HBM's rate): bound by the VALU and the latency of a row's five sums and its
+// passage through LDS.  Sigmoid scores with exponentials of their own: 31.4 us;
+// comparing every expert with every choice instead of LDS, and library
+// exponentials: 105 us.
 template <typename T, int L, int V, int SCORE>
 __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
   constexpr int G = kRouterThreads / L, C = L * V;
@@ -512,13 +536,8 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
 
     Score<SCORE> sc;
     sc.at_top(row_top<L, V>(v));
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      w[i] = sc.weight(v[i], &away[i]);
-      sum += w[i];
-    }
-    sum = group_all<L>(sum, OpAdd());
+    float e[V];
+    const float sum = row_scores<L, V, SCORE, true>(sc, v, w, e, away);
     T* out = (T*)a.dlogits + t * a.ld_out;
     T o[V];
     float x[V];
@@ -536,9 +555,9 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
       const float hq = a.renorm ? (Q > 0.f ? H / Q : 0.f)
                                 : (SCORE == MOE_SCORE_SOFTMAX ? H : 0.f);
       const float rest = a.renorm ? 0.f : hq;            // of the experts not chosen
-      float zs = 0.f, lsum = sum, e[V];
+      float zs = 0.f;
       if (zmul != 0.f) {
-        if constexpr (SCORE == MOE_SCORE_SIGMOID) lsum = row_exp_sum<L, V>(v, sc.top, e);
+        const float lsum = SCORE == MOE_SCORE_SOFTMAX ? sum : lane_sum<L, V>(e);
         zs = zmul * (sc.top + logf(lsum));
         if constexpr (SCORE == MOE_SCORE_SIGMOID) zs *= inverse(lsum);
       }
@@ -684,7 +703,9 @@ int launch_router_bwd(const moe_router& R, const void* logits, int ld, const uin
   a.ids_in = ids; a.dlogp = dlogp; a.counts_in = counts; a.live_in = live; a.dlosses = dlosses;
   a.dlogits = dlogits; a.ld_out = (size_t)ld_out;
   const int G = kRouterThreads / router_lanes(R.E);
-  const int grid = (int)std::min<long long>(((long long)T + G - 1) / G, 256 * 8);
+  // four waves a SIMD, what most variants' registers allow at once: 65521 x 256 bf16 25.8 us (sigmoid 27.7),
+  // with twice as many, the last of them alone, 25.8 (28.5), with one round of rows each 40.8 (43.5)
+  const int grid = (int)std::min<long long>(((long long)T + G - 1) / G, 256 * 4);
   router_kind<BwdK>(R, a, grid, st);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

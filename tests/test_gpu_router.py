@@ -99,6 +99,25 @@ def test_router_of_many_rows(T, E, k, dtype, score):
                     score, True, mask)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("E", [8, 60, 256, 1000])
+def test_router_sigmoid_tops(E, dtype, renorm):
+    """Rows whose largest logit lies around the bound up to which a sigmoid is made from e^(l - top),
+    far from it on both sides, and with the others far below it."""
+    say(f"[router-tops] E={E} {dtype} renorm={renorm}")
+    rng = np.random.default_rng(E)
+    tops = np.array([-60, -20, -16.25, -16, -15.75, -3, 0, 3, 15.75, 16, 16.25, 20, 60], dtype=np.float32)
+    l = -np.abs(rng.standard_normal((6 * len(tops), E))).astype(np.float32)
+    l *= np.repeat(np.array([0.5, 4, 12], dtype=np.float32), 2 * len(tops))[:, None]
+    l[np.arange(len(l)), rng.integers(0, E, len(l))] = 0
+    l += np.tile(tops, 6)[:, None]
+    logits = torch.from_numpy(l).to(dtype).to(DEV)
+    R, out, o = _check_forward(logits, min(E, 6), "sigmoid", renorm)
+    _check_backward(R, logits, out, o, torch.randn((len(l), R.k), device=DEV),
+                    torch.tensor([0.8, 0.05], device=DEV), "sigmoid", renorm)
+
+
 def _check_backward(R, logits, out, o, h, dl, score, renorm, mask=None, dlogits=None):
     T, E = logits.shape
     if dlogits is None:
