@@ -152,7 +152,7 @@ class BlockRunner(LayerRunner):
         self.n, self.out = torch.empty((T, d), **rows), torch.empty((T, d), **rows)
         self.logits = torch.empty((T, self.E), **rows)
         self.rstd_in, self.rstd_out = torch.empty(T, **f32), torch.empty(T, **f32)
-        self.optimizer = None
+        self.optimizer = self.x = None
         if self.with_backward:
             self.norm_ws = B.norm_workspace(T, d, dev)
             self.dy, self.dn = torch.empty((T, d), **rows), torch.empty((T, d), **rows)
@@ -184,6 +184,8 @@ class BlockRunner(LayerRunner):
     def block_backward(self, dout, dlosses=None):
         """Gradients of block_forward's last call from dout [T][d] and (optional) dlosses [2], those
         of the balance and z losses: dx, and dw1, dw2, dw_router, dw_in, dw_out, dgate in self."""
+        if not self.with_backward or self.x is None:
+            raise B.MoeError("block_backward needs a runner with a backward pass, after block_forward")
         r = self.routed
         B.norm_out_backward(dout, self.y, self.w_out, self.rstd_out, self.dy, self.dw_out,
                             self.norm_ws, self.gate, self.alpha, self.dgate, self.mask)

@@ -304,3 +304,15 @@ def test_block_refusals():
         BlockRunner(par["w1"], par["w2"], par["w_router"][:, :-1], par["w_in"], par["w_out"],
                     act_dtype=torch.float32, T=w.T, k=w.k, beta=w.beta, P=w.P, s=w.s,
                     owner=torch.from_numpy(contiguous_owners(w.E, w.P)))
+
+
+def test_block_backward_needs_its_forward():
+    w = PATHS["small_f32"]
+    b, par, x, dout = _block(w, w.T, 1, "softmax", True)
+    with pytest.raises(B.MoeError, match="block_forward"):
+        b.block_backward(dout)
+    only = BlockRunner(**par, act_dtype=torch.float32, T=w.T, k=w.k, beta=w.beta, P=w.P, s=w.s,
+                       owner=torch.from_numpy(contiguous_owners(w.E, w.P)))
+    only.block_forward(x)
+    with pytest.raises(B.MoeError, match="block_forward"):
+        only.block_backward(dout)
