@@ -157,7 +157,7 @@ __global__ __launch_bounds__(RowsOf<NT>::WG) void k_norm(NormArgs a) {
 // the rows' groups at the end and over the workgroups by k_norm_cols, so the order of every sum is
 // fixed by the grid.  A row's loads are issued before the sum of the row before it is joined.  Bound
 // by HBM: before the block 4099 x 7168 bf16 with residual and feature gate 353 MB and 15 MB of partial
-// sums in 66.5 us (5.5 TB/s); after it 1000 x 1023 fp32 5.2 us.  Rows of several pieces a thread (bf16
+// sums in 67 us (5.5 TB/s); after it 1000 x 1023 fp32 5.2 us.  Rows of several pieces a thread (bf16
 // above 8192 features, fp32 above 4096) reach 3.4 to 4.8 TB/s.
 constexpr int kNormWG = 1024;
 template <typename T, int VE, int NT, int KC, bool OUT, bool FEAT>
