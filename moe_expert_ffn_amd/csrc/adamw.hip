@@ -130,7 +130,11 @@ MOE_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 // above 448, which no u carries to the next code, so no clamp is needed.
 // Every operation is one fp32 rounding in this order, so that equal states give
 // equal codes wherever they are computed so.
-// SIGNED: x may be negative.  u: bits SHIFT..SHIFT + 15 of word.
+// SIGNED: x may be negative (m).  Else x is a root, of which no more than a value of 0 has the code 0:
+// m and sqrt(v) are rounded by different bits, and where m came out as a step and sqrt(v) as nothing, the
+// next update was hundreds of learning rates (the quotient of m's step by sqrt((1 - beta2) g^2) of a small
+// g).  With at least a step under it, m's step counts no more than the block's largest m by its largest
+// sqrt(v).  u: bits SHIFT..SHIFT + 15 of word.
 template <bool SIGNED, int SHIFT>
 MOE_DEV void to_e4m3(float* x, const uint32_t* word, uint8_t* codes, float* scale) {
 #pragma clang fp contract(off)
@@ -165,7 +169,8 @@ MOE_DEV void to_e4m3(float* x, const uint32_t* word, uint8_t* codes, float* scal
     const float u = __builtin_fmaf((float)(uint16_t)(word[i] >> SHIFT), 0x1p-19f, 0x1p-20f);
     const float t = __builtin_fmaf(u, octave, y);
     const int b = (int)(__float_as_uint(t) >> 20) - (120 << 3), c = (int)(t * 512.f);
-    code[i] = (uint32_t)max(min(b, c), min(max(b, c), 8));
+    const uint32_t least = SIGNED ? 0u : min(__float_as_uint(y), 1u);
+    code[i] = max((uint32_t)max(min(b, c), min(max(b, c), 8)), least);
   }
   uint32_t packed[2];
 #pragma unroll

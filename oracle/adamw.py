@@ -4,8 +4,9 @@
     p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
 in fp64.  8-bit states hold m and sqrt(v) in blocks of 128 as e4m3 codes times
 a scale, the block's largest finite magnitude over 448, rounded up with the
-probability of the part cut off; the random words are a hash of the seed, the
-step, the tensor's place in its list and the element's index.
+probability of the part cut off, a sqrt(v) that is not 0 to the code 1 at
+least; the random words are a hash of the seed, the step, the tensor's place in
+its list and the element's index.
 """
 from __future__ import annotations
 
@@ -55,9 +56,13 @@ def block_tops(x):
     return np.where(a < 2.0 ** -100, 0.0, a)
 
 
-def encode(x, u16):
+def encode(x, u16, root=None):
     """(codes, scales, distance): distance of the sum that is cut to the next whole number, in code
-    steps -- where it is within the arithmetic's error, the neighbouring code is right as well."""
+    steps -- where it is within the arithmetic's error, the neighbouring code is right as well.
+    root: x is sqrt(v), whose codes are 1 at least where it is not 0; None: where nothing in x is
+    negative (m of a block without a negative element differs from that only below one code step)."""
+    if root is None:
+        root = not (x < 0).any()
     top = block_tops(x)
     per = np.repeat(top, BLOCK)[:x.size]
     fin = np.isfinite(x)
@@ -65,6 +70,8 @@ def encode(x, u16):
     ex = np.clip(np.floor(np.log2(np.maximum(y, 2.0 ** -20))), -6, 8).astype(np.int64)
     s = np.ldexp(y, 3 - ex) + (u16 + 0.5) / 65536
     code = np.minimum((ex + 6) * 8 + np.floor(s).astype(np.int64), 126)
+    if root:
+        code = np.maximum(code, y > 0)
     code = np.where(fin, code, 127) | np.where(x < 0, 128, 0)
     return code.astype(np.uint8), top / 448, np.abs(s - np.round(s))
 

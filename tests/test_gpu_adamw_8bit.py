@@ -1,0 +1,72 @@
+"""GPU: 8-bit optimizer states over many steps, with gradients that lie far apart inside a block."""
+import numpy as np
+import pytest
+import torch
+
+from moe_expert_ffn_amd import binding as B
+from oracle import adamw as oadam
+from tests.adamw_cases import run_constant, run_normal, update_bound
+from tests.gpu_util import say
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _updates(g_of, steps, beta2, check=None):
+    """|update| / lr of every step [steps][n], from zero states; check(t, g, before, list) after each."""
+    n, lr = g_of(1).size, 1e-3
+    z8 = lambda: [torch.zeros(n, dtype=torch.uint8, device=DEV)]
+    zs = lambda: [torch.zeros(n // 128, device=DEV)]
+    s = {"p": [torch.zeros(n, device=DEV)], "g": [torch.zeros(n, device=DEV)], "m": z8(), "v": z8(),
+         "m_scale": zs(), "v_scale": zs()}
+    opt = B.make_adamw(**s)
+    out = []
+    for t in range(1, steps + 1):
+        g = g_of(t)
+        s["g"][0].copy_(torch.from_numpy(g))
+        s["p"][0].zero_()                               # the update itself, without p's rounding
+        before = {k: s[k][0].cpu().numpy() for k in ("m", "v", "m_scale", "v_scale")}
+        B.adamw(opt, lr=lr, beta1=0.9, beta2=beta2, eps=1e-8, step=t, seed=5)
+        torch.cuda.synchronize()
+        out.append(np.abs(s["p"][0].double().cpu().numpy()) / lr)
+        if check is not None:
+            check(t, g, before, {k: s[k][0].cpu().numpy() for k in before})
+    return np.stack(out)
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.99, 0.999])
+def test_updates_of_constant_gradients_are_bounded(beta2):
+    say(f"[adamw-8bit] constant beta2={beta2}")
+    g, ratio = run_constant()
+    upd = _updates(lambda t: g, 60, beta2)
+    assert (upd <= update_bound(ratio, 60, beta2)).all()
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.99, 0.999])
+def test_updates_of_noise_stay_near_those_of_32_bit_states(beta2):
+    say(f"[adamw-8bit] noise beta2={beta2}")
+    g_of, limit = run_normal(beta2)
+    assert _updates(g_of, 100, beta2)[20:].max() <= limit
+
+
+def test_codes_of_far_apart_states_are_the_definitions():
+    """Every code of sqrt(v) at each step against the oracle's from the same states; 16 u for the quotient and 16
+    for the sum that is cut, as in the tests of single steps: within 2^-15 of a whole number either code is right,
+    but no code is 0 where sqrt(v) is not."""
+    say("[adamw-8bit] codes")
+    g_of, _ = run_normal(0.99)
+    low = [0]
+
+    def check(t, g, before, after):
+        v0 = oadam.decode(before["v"], before["v_scale"]) ** 2
+        root = np.sqrt(0.99 * v0 + 0.01 * g * g)
+        codes, scales, dist = oadam.encode(root, oadam.words(5, t, 0, g.size) >> 16, root=True)
+        # the error of sqrt(v) (8 u) and of the scale (16 u), in code steps of up to 16 a value
+        near = dist <= 2.0 ** -15 + 24 * 16 * 2.0 ** -24
+        assert (after["v"] == codes)[~near].all()
+        assert (after["v"][root > 0] > 0).all()
+        np.testing.assert_allclose(after["v_scale"], scales, rtol=16 * 2.0 ** -24)
+        low[0] += int((codes == 1).sum())
+
+    _updates(g_of, 12, 0.99, check)
+    assert low[0] > 1000                                 # the elements that the floor is for are there
