@@ -117,6 +117,24 @@ MOE_DEV float sqrt_nearest(float x) {
   return high > 0.f ? up : low <= 0.f ? dn : s;
 }
 
+// Roots of eight values, to nearest (or within an ulp).  The hardware's root takes subnormal numbers for
+// 0, and the remainders of sqrt_nearest leave fp32's range below 2^-100: such values (gradients below some
+// 1e-12) go scaled by 2^64, in a branch of whole waves.
+template <bool NEAREST> MOE_DEV void roots(const float* v, float* s) {
+  auto root = [](float x) { return NEAREST ? sqrt_nearest(x) : __builtin_amdgcn_sqrtf(x); };
+  float low = v[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) low = fminf(low, v[i]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s[i] = root(v[i]);
+  if (__any(low < 0x1p-96f)) {
+    asm volatile("");
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (v[i] < 0x1p-96f) s[i] = root(v[i] * 0x1p64f) * 0x1p-32f;
+  }
+}
+
 constexpr uint32_t kInfBits = 0x7F800000u;
 MOE_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
@@ -234,12 +252,16 @@ MOE_DEV void adam8(const AdamArgs& a, const AdamTensor& t, const AdamRates& h, u
     if constexpr (BITS == 8) v[i] *= v[i];
     m[i] = a.beta1 * m[i] + a.c1 * g[i];
     v[i] = a.beta2 * v[i] + a.c2 * (g[i] * g[i]);
-    // the update is lr times a number near 1: a reciprocal of 1 ulp, and where its root is not stored
-    // a root of 1 ulp
-    const float s = BITS == 8 ? sqrt_nearest(v[i]) : __builtin_amdgcn_sqrtf(v[i]);
-    const float d = __builtin_amdgcn_rcpf(__builtin_fmaf(s, h.root, a.eps));
+  }
+  // the update is lr times a number near 1: a reciprocal of 1 ulp, and where its root is not stored
+  // a root of 1 ulp
+  float s[8];
+  roots<BITS == 8>(v, s);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float d = __builtin_amdgcn_rcpf(__builtin_fmaf(s[i], h.root, a.eps));
     p[i] = __builtin_fmaf(-h.rate * m[i], d, p[i] * h.keep);
-    if constexpr (BITS == 8) v[i] = s;
+    if constexpr (BITS == 8) v[i] = s[i];
   }
   if constexpr (BITS == 32) {
     store8<float, FULL>((float*)t.m + at, n, m);

@@ -70,3 +70,37 @@ def test_codes_of_far_apart_states_are_the_definitions():
 
     _updates(g_of, 12, 0.99, check)
     assert low[0] > 1000                                 # the elements that the floor is for are there
+
+
+@pytest.mark.parametrize("eps", [1e-8, 1e-25])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_roots_of_tiny_and_subnormal_v(bits, eps):
+    """One step from zero states with gradients whose v is near or below fp32's smallest normal number.  v is rounded
+    to a multiple of 2^-149 (its two products and their sum: 1.5 steps), half of that relative to v in its root; 24
+    roundings of 2^-24 for the rest."""
+    say(f"[adamw-tiny] bits={bits} eps={eps}")
+    u = 2.0 ** -24
+    rng = np.random.default_rng(21)
+    for G in (1e-13, 1e-17, 1e-18, 1e-19, 1e-20):
+        n = 256
+        g = (G * (1 + rng.random(n))).astype(np.float32).astype(np.float64)
+        f = lambda: torch.zeros(n, device=DEV)
+        b8 = lambda: torch.zeros(n, dtype=torch.uint8, device=DEV)
+        s = {"p": [f()], "g": [torch.from_numpy(g.astype(np.float32)).to(DEV)], "m": [f()], "v": [f()]}
+        if bits == 8:
+            s.update(m=[b8()], v=[b8()], m_scale=[f()[:2]], v_scale=[f()[:2]])
+        B.adamw(B.make_adamw(**s), lr=1e-3, beta1=0.9, beta2=0.99, eps=eps, step=1, seed=2)
+        torch.cuda.synchronize()
+        p, _, v = oadam.step(0 * g, g, 0 * g, 0 * g, 1, 1e-3, 0.9, 0.99, eps, 0.0)
+        off = 24 * u + 0.75 * 2.0 ** -149 / v
+        # g^2 is rounded in fp32 before its product with 1 - beta2
+        off = off + 0.5 * 2.0 ** -149 / (g * g)
+        got = s["p"][0].double().cpu().numpy()
+        assert (np.abs(got - p) <= off * np.abs(p) + 2.0 ** -149).all(), G
+        if bits == 8:                                    # v's code within its step, the scale within the error
+            root = np.sqrt(v)
+            top = root.reshape(-1, 128).max(1)
+            scale = s["v_scale"][0].double().cpu().numpy()
+            assert (np.abs(scale - top / 448) <= np.max(off) * top / 448 + 2.0 ** -149).all(), G
+            back = oadam.decode(s["v"][0].cpu().numpy(), scale)
+            assert (np.abs(back - root) <= root / 8 + np.max(off) * root * 2).all(), G
