@@ -391,8 +391,8 @@ int moe_gate_grad(const void* z, const void* dz, int dtype, const int32_t* row_t
   if (d_ff % 64) return MOE_ERR_UNSUPPORTED;
   if (rows > 0 && (!row_to_slot || !dlogp)) return MOE_ERR_ARG;
   if (slots > 0 && (!z || !dz)) return MOE_ERR_ARG;
-  return launch_gate_grad(z, dz, dtype, row_to_slot, rows, slots, d_ff, dlogp,
-                          (hipStream_t)stream);
+  launch_gate_grad(z, dz, dtype, row_to_slot, rows, slots, d_ff, dlogp, (hipStream_t)stream);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 static int check_norm(const moe_norm* N) {

@@ -2480,8 +2480,8 @@ int launch_forward(const Sizes& z, const LayerPtrs& Lp, const void* x, const flo
 static void gate_grads(const Sizes& z, const ExecArgs& a, int dtype, const int32_t* row_to_slot,
                        hipStream_t st) {
   if (a.dlogp)
-    (void)launch_gate_grad(a.z_save, a.bufA, dtype, row_to_slot, z.T * z.k, (int)z.max_slots,
-                           z.dff, a.dlogp, st);
+    launch_gate_grad(a.z_save, a.bufA, dtype, row_to_slot, z.T * z.k, (int)z.max_slots, z.dff,
+                     a.dlogp, st);
 }
 
 // With e4m3 weights (FP8): D = p dy per slot is requantized along the tokens

@@ -86,8 +86,8 @@ int launch_router_bwd(const moe_router& R, const void* logits, int ld, const uin
                       const int32_t* ids, const float* dlogp, const int32_t* counts,
                       const int32_t* live, const float* dlosses, void* dlogits, int ld_out,
                       hipStream_t st);
-int launch_gate_grad(const void* z, const void* dz, int dtype, const int32_t* row_to_slot,
-                     int rows, int slots, int dff, float* dlogp, hipStream_t st);
+void launch_gate_grad(const void* z, const void* dz, int dtype, const int32_t* row_to_slot,
+                      int rows, int slots, int dff, float* dlogp, hipStream_t st);
 
 constexpr int kNormMaxD = 16384;
 struct NormRows { const void* p; int ld; };
