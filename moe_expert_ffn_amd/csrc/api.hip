@@ -192,9 +192,10 @@ int moe_quantize_token_blocks(const void* src, int ld, int src_rows, const int32
   if ((!row_map || !gather) && src_rows < rows) return MOE_ERR_ARG;
   if (!src || !codes || !scales) return MOE_ERR_ARG;
   const long long lim = (long long)src_rows * row_div;
-  return launch_quant_tok((const uint16_t*)src, ld, row_map, gather ? 1 : 0, row_div, row_scale,
-                          lim < INT32_MAX ? (int)lim : INT32_MAX, rows, cols, block_rows, codes,
-                          scales, (hipStream_t)stream);
+  launch_quant_tok((const uint16_t*)src, ld, row_map, gather ? 1 : 0, row_div, row_scale,
+                   lim < INT32_MAX ? (int)lim : INT32_MAX, rows, cols, block_rows, codes, scales,
+                   (hipStream_t)stream);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int moe_quantize_act_rows(const void* src, int rows, int cols, uint8_t* codes, int32_t* exps,
@@ -202,7 +203,8 @@ int moe_quantize_act_rows(const void* src, int rows, int cols, uint8_t* codes, i
   if (rows < 0 || cols < 128 || cols % 128) return MOE_ERR_ARG;
   if (rows > 0 && (!src || !codes || !exps)) return MOE_ERR_ARG;
   if (rows == 0) return MOE_OK;
-  return launch_quant_act((const uint16_t*)src, rows, cols, codes, exps, (hipStream_t)stream);
+  launch_quant_act((const uint16_t*)src, rows, cols, codes, exps, (hipStream_t)stream);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 int moe_predict_cost(const int32_t* counts, const int32_t* block_offsets,

@@ -53,12 +53,12 @@ int launch_plan(const int32_t* bcnt, const int32_t* boff, const int32_t* owner, 
                 int32_t* info, int32_t* status, hipStream_t st);
 constexpr int kQtMaxCols = 65535 * 128;   // column tiles of the quantizer grid
 // map_lim: map values m >= map_lim read as zero rows (src rows * div)
-int launch_quant_act(const uint16_t* x, int rows, int cols, uint8_t* codes, int32_t* exps,
-                     hipStream_t st, const int32_t* blk_end = nullptr, int blk_rows = 0);
-int launch_quant_tok(const uint16_t* src, int ld, const int32_t* map, int gather, int div,
-                     const float* rscale, int map_lim, int rows, int cols, int brows,
-                     uint8_t* codes, float* scales, hipStream_t st,
-                     const int32_t* blk_end = nullptr);
+void launch_quant_act(const uint16_t* x, int rows, int cols, uint8_t* codes, int32_t* exps,
+                      hipStream_t st, const int32_t* blk_end = nullptr, int blk_rows = 0);
+void launch_quant_tok(const uint16_t* src, int ld, const int32_t* map, int gather, int div,
+                      const float* rscale, int map_lim, int rows, int cols, int brows,
+                      uint8_t* codes, float* scales, hipStream_t st,
+                      const int32_t* blk_end = nullptr);
 int launch_predict_cost(const int32_t* counts, const int32_t* boff, const int32_t* bw_f,
                         const int32_t* bw_b, const int32_t* owner, int E, int beta, int P, int d,
                         int dff, int G, long long* cost, int32_t* status, hipStream_t st);

@@ -29,9 +29,9 @@ sys.path.insert(0, sys.argv[2])
 from moe_expert_ffn_amd import binding as B
 lib = B.load()
 P = ctypes.c_void_p(256)
-act, w, flags, call = int(sys.argv[3]), int(sys.argv[4]), int(sys.argv[5]), sys.argv[6]
+act, w, flags, d, dff, call = *map(int, sys.argv[3:8]), sys.argv[8]
 scale = 256 if w == B.MOE_FP8_E4M3 else None
-L = B.Layer(8, 512, 256, act, w, 256, 256, scale, scale)
+L = B.Layer(8, d, dff, act, w, 256, 256, scale, scale)
 sizes = (300, 2, 128, 4, 1)
 def once():
     if call == "forward":
@@ -66,8 +66,8 @@ def shim(tmp_path_factory):
     return str(at / "shim.so")
 
 
-def _every_launch(shim, call, act, w, flags):
-    r = subprocess.run([sys.executable, "-c", RUN, shim, ROOT, str(act), str(w), str(flags), call],
+def _every_launch(shim, call, act, w, flags, d=512, dff=256):
+    r = subprocess.run([sys.executable, "-c", RUN, shim, ROOT, *map(str, (act, w, flags, d, dff)), call],
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
 
@@ -76,3 +76,12 @@ def _every_launch(shim, call, act, w, flags):
 @pytest.mark.parametrize("act,w,flags", [(F32, F32, 0), (BF16, BF16, 0), (BF16, BF16, 1)])
 def test_failed_launches_of_the_backward_pass(shim, call, act, w, flags):
     _every_launch(shim, call, act, w, flags)
+
+
+@pytest.mark.parametrize("call,flags,d,dff", [
+    ("forward", 0, 512, 256), ("forward", 2, 512, 256), ("forward", 0, 384, 128),
+    ("backward", 0, 512, 256), ("backward", 2, 512, 256), ("backward_gates", 0, 512, 256),
+    ("backward_gates", 2, 512, 256), ("backward_gates", 0, 256, 128), ("backward", 0, 384, 128)])
+def test_failed_launches_of_e4m3_layers(shim, call, flags, d, dff):
+    """Their quantizers are launches of the same calls."""
+    _every_launch(shim, call, BF16, FP8, flags, d, dff)
