@@ -449,7 +449,7 @@ typedef struct {
   float scale;
 } moe_router;
 
-/* Workspace of moe_router_forward for T tokens; 0 for invalid arguments. */
+/* Workspace of moe_router_forward for up to T tokens; 0 for invalid arguments. */
 size_t moe_router_workspace_size(const moe_router* R, int T);
 
 /* Routing of T tokens and the losses that balance it.
@@ -540,7 +540,7 @@ typedef struct {
   const uint8_t* token_mask;
 } moe_norm;
 
-/* Workspace of the norms' backward passes; 0 for invalid arguments. */
+/* Workspace of the norms' backward passes for up to T rows of d features; 0 for invalid arguments. */
 size_t moe_norm_workspace_size(int T, int d);
 
 /* Before the block.  u (nullable) [T][d]: what the residual stream takes up, r

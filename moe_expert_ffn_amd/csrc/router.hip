@@ -623,15 +623,17 @@ static bool router_halved(int T, int E) {
 }
 static int router_lanes_fwd(int T, int E) { return router_lanes(E) / (router_halved(T, E) ? 2 : 1); }
 
-static int router_grid(int T, int E) {
-  const int G = kRouterThreads / router_lanes_fwd(T, E);
+static int router_grid(int T, int lanes) {
+  const int G = kRouterThreads / lanes;
   // one workgroup writes the totals itself: two rounds of its rows cost less than the second launch
   if (T <= 2 * G) return 1;
   return std::min((int)(((long long)T + G - 1) / G), kRouterMaxWG);
 }
 
+// Of what T rows need and any fewer: with 8 experts a lane, whose workgroups never decrease with T (where
+// 16 experts a lane begin they halve), so that a workspace for the largest batch serves the others.
 size_t router_ws_bytes(int T, int E) {
-  const size_t wg = (size_t)router_grid(T, E);
+  const size_t wg = (size_t)router_grid(T, router_lanes(E));
   return align_up(wg * E * 4) * 2 + align_up(wg * 4) * 2 + 2 * align_up(64 * 4);
 }
 
@@ -677,7 +679,7 @@ int launch_router(const moe_router& R, const void* logits, int ld, const uint8_t
   a.renorm = R.renorm; a.scale = R.scale;
   a.ids = ids; a.gates = gates; a.counts = counts; a.psum = psum; a.live = live;
   a.losses = losses; a.status = status;
-  const int grid = router_grid(T, R.E);
+  const int grid = router_grid(T, router_lanes_fwd(T, R.E));
   char* w = (char*)ws;
   a.part_p = (float*)w;
   a.part_c = (int32_t*)(w += align_up((size_t)grid * R.E * 4));

@@ -180,3 +180,19 @@ def test_row_strides():
     assert B._rows(t[::2, :8], 3, 8, torch.float32, "x") == 40
     assert B._rows(torch.zeros(0, 8), 0, 8, torch.float32, "x") == 8
     assert B._rows(torch.zeros(5, 1), 5, 1, torch.float32, "x") == 1
+
+
+@pytest.mark.parametrize("E", [1, 16, 64, 65, 128, 129, 160, 256, 257, 384, 512, 513, 1024])
+def test_router_workspace_serves_every_smaller_batch(E):
+    size = lambda T: B.load().moe_router_workspace_size(ctypes.byref(_router(E=E, k=1)), T)
+    Ts = sorted({max(0, b + o) for b in [0] + [1 << i for i in range(23)] for o in range(-9, 10)})
+    sizes = [size(T) for T in Ts]
+    assert all(s > 0 for s in sizes)
+    assert sizes == sorted(sizes), next((Ts[i], sizes[i - 1], sizes[i]) for i in range(1, len(Ts)) if sizes[i] < sizes[i - 1])
+
+
+def test_norm_workspace_serves_every_smaller_batch():
+    Ts = sorted({max(0, b + o) for b in [0] + [1 << i for i in range(23)] for o in (-2, -1, 0, 1, 2)})
+    for d in (1, 7, 64, 1023, 4096, 16384):
+        sizes = [B.load().moe_norm_workspace_size(T, d) for T in Ts]
+        assert sizes == sorted(sizes) and sizes[0] > 0
