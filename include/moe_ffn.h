@@ -643,8 +643,9 @@ int moe_adamw_prepare(const moe_adamw_tensor* tensors, int count, int state_bits
                       moe_adamw_list* out, void* ws, size_t ws_bytes, void* stream);
 
 /* One step on every tensor of the list.
- * Errors: MOE_ERR_ARG for a null list, beta1 or beta2 outside [0, 1), eps <= 0,
- *   step < 1 (without step_dev) or a lr or weight_decay that is not finite. */
+ * Errors: MOE_ERR_ARG for a null list, beta1 or beta2 outside [0, 1), an eps
+ *   below fp32's smallest normal number (2^-126), step < 1 (without step_dev) or
+ *   an eps, lr or weight_decay that is not finite in fp32. */
 int moe_adamw(const moe_adamw_list* list, const moe_adamw_hyper* h, void* stream);
 
 /* Timing helpers so a caller without a HIP binding can time the stages:

@@ -2,6 +2,7 @@
 // carving and kernel launches.  No allocation, no host synchronisation.
 #include <hip/hip_runtime.h>
 
+#include <float.h>
 #include <stdlib.h>
 
 #include <algorithm>
@@ -547,8 +548,11 @@ int moe_adamw(const moe_adamw_list* list, const moe_adamw_hyper* h, void* stream
   if (!list || !h || list->tensors < 0 || (list->items > 0 && !list->table) ||
       (list->state_bits != 8 && list->state_bits != 32))
     return MOE_ERR_ARG;
-  if (!(h->beta1 >= 0 && h->beta1 < 1) || !(h->beta2 >= 0 && h->beta2 < 1) || !(h->eps > 0) ||
-      !std::isfinite(h->eps) || !std::isfinite(h->weight_decay) || (!h->lr_dev && !std::isfinite(h->lr)) || (!h->step_dev && h->step < 1))
+  if (!(h->beta1 >= 0 && h->beta1 < 1) || !(h->beta2 >= 0 && h->beta2 < 1) || (!h->step_dev && h->step < 1))
+    return MOE_ERR_ARG;
+  // as the kernel holds them: an eps below fp32's normal numbers has no reciprocal, and 0 / eps would be NaN
+  if (!((float)h->eps >= FLT_MIN) || !std::isfinite((float)h->eps) ||
+      !std::isfinite((float)h->weight_decay) || (!h->lr_dev && !std::isfinite((float)h->lr)))
     return MOE_ERR_ARG;
   return launch_adamw(*list, *h, (hipStream_t)stream);
 }

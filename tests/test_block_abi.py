@@ -196,3 +196,14 @@ def test_norm_workspace_serves_every_smaller_batch():
     for d in (1, 7, 64, 1023, 4096, 16384):
         sizes = [B.load().moe_norm_workspace_size(T, d) for T in Ts]
         assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+def test_adamw_numbers_that_fp32_does_not_hold():
+    L = B.AdamwList(256, 1, 32, 0)
+    ok = dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, weight_decay=0.0, step=1)
+    rc = lambda **kw: B.load().moe_adamw(ctypes.byref(L), ctypes.byref(B.AdamwHyper(**{**ok, **kw})), None)
+    for bad in (dict(eps=1e-46), dict(eps=1e-38), dict(eps=1e39), dict(lr=1e39), dict(lr=-1e39),
+                dict(weight_decay=1e39), dict(eps=-1e-8)):
+        assert rc(**bad) == ARG, bad
+    for good in (dict(), dict(eps=2.0 ** -126), dict(lr=0.0), dict(lr=-1e-3), dict(lr=1e38), dict(weight_decay=1e38)):
+        assert rc(**good) == B.MOE_OK, good

@@ -104,3 +104,22 @@ def test_roots_of_tiny_and_subnormal_v(bits, eps):
             assert (np.abs(scale - top / 448) <= np.max(off) * top / 448 + 2.0 ** -149).all(), G
             back = oadam.decode(s["v"][0].cpu().numpy(), scale)
             assert (np.abs(back - root) <= root / 8 + np.max(off) * root * 2).all(), G
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_the_smallest_eps_leaves_what_has_no_gradient(bits):
+    say(f"[adamw-eps] bits={bits}")
+    n = 300
+    f = lambda m=n: torch.zeros(m, device=DEV)
+    b8 = lambda: torch.zeros(n, dtype=torch.uint8, device=DEV)
+    s = {"p": [torch.randn(n, device=DEV)], "g": [f()], "m": [f()], "v": [f()]}
+    if bits == 8:
+        s.update(m=[b8()], v=[b8()], m_scale=[f(3)], v_scale=[f(3)])
+    was = s["p"][0].clone()
+    opt = B.make_adamw(**s)
+    with pytest.raises(B.MoeError, match="invalid argument"):
+        B.adamw(opt, lr=1e-3, eps=1e-40)
+    for t in (1, 2):
+        B.adamw(opt, lr=1e-3, eps=2.0 ** -126, step=t)
+    torch.cuda.synchronize()
+    assert torch.equal(s["p"][0], was)
