@@ -551,22 +551,34 @@ def _ws_at(ws):
     return p + off, max(ws.numel() - off, 0)
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _int(n, name):
+    """n, refused where a C int does not hold it: ctypes would cut it down without a word."""
+    if not -_INT_MAX <= n <= _INT_MAX:
+        raise MoeError(f"{name}: {n} is beyond a 32-bit int")
+    return n
+
+
 def _rows(t, T, cols, dtype, name):
     """Row stride of a [T][cols] matrix whose rows' elements lie side by side."""
-    if t.dtype == dtype and t.shape == (T, cols):
+    if t.dtype == dtype and t.shape == (T, cols) and T <= _INT_MAX:
         stride = t.stride()
-        if stride[1] == 1 and stride[0] >= cols:
+        if stride[1] == 1 and cols <= stride[0] <= _INT_MAX:
             return stride[0]
     if t.dtype != dtype:
         raise MoeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.dim() != 2 or t.shape[0] != T or t.shape[1] != cols:
         raise MoeError(f"{name}: expected {(T, cols)}, got {tuple(t.shape)}")
+    _int(T, f"rows of {name}")
+    _int(cols, f"columns of {name}")
     if T == 0 or (T == 1 and (cols <= 1 or t.stride(1) == 1)):
         return cols
     ld = t.stride(0)
     if (cols > 1 and t.stride(1) != 1) or ld < cols:
         raise MoeError(f"{name}: strides {tuple(t.stride())} are not those of rows of {cols}")
-    return ld
+    return _int(ld, f"row stride of {name}")
 
 
 def _vector(t, n, dtype, name):
@@ -598,7 +610,7 @@ def make_router(E, k, dtype=torch.float32, score="softmax", renorm=True, scale=1
     """A top-k router of logits [T][E] of this dtype (moe_router)."""
     if score not in SCORES:
         raise MoeError(f"score {score!r}: one of {sorted(SCORES)}")
-    r = Router(E, k, _dtype_code(dtype, "logits"), SCORES[score], int(bool(renorm)), scale)
+    r = Router(_int(E, "E"), _int(k, "k"), _dtype_code(dtype, "logits"), SCORES[score], int(bool(renorm)), scale)
     if load().moe_router_workspace_size(ctypes.byref(r), 0) == 0:
         raise MoeError(f"router of E={E}, k={k}, scale={scale} is not supported")
     return r
@@ -612,7 +624,7 @@ def alloc_router(router: Router, T, device):
 
 
 def router_workspace(router: Router, T, device) -> torch.Tensor:
-    n = int(load().moe_router_workspace_size(ctypes.byref(router), T))
+    n = int(load().moe_router_workspace_size(ctypes.byref(router), _int(T, "T")))
     if n == 0:
         raise MoeError("moe_router_workspace_size rejected the sizes")
     return torch.empty(n + 256, dtype=torch.uint8, device=device)
@@ -675,7 +687,9 @@ def gate_grad(z, dz, row_to_slot, dlogp):
     code = _dtype_code(z.dtype, "z")
     _vector(z, z.numel(), z.dtype, "z")
     _vector(dz, z.numel(), z.dtype, "dz")
-    rows = row_to_slot.numel()
+    rows = _int(row_to_slot.numel(), "rows")
+    _int(slots, "slots")
+    _int(two, "columns of z")
     _vector(row_to_slot, rows, torch.int32, "row_to_slot")
     _vector(dlogp, rows, torch.float32, "dlogp")
     _check(load().moe_gate_grad(_at(z), _at(dz), code, _at(row_to_slot), rows, slots, two // 2,
@@ -684,7 +698,7 @@ def gate_grad(z, dz, row_to_slot, dlogp):
 
 
 def norm_workspace(T, d, device) -> torch.Tensor:
-    n = int(load().moe_norm_workspace_size(T, d))
+    n = int(load().moe_norm_workspace_size(_int(T, "T"), _int(d, "d")))
     if n == 0:
         raise MoeError("moe_norm_workspace_size rejected the sizes")
     return torch.empty(n + 256, dtype=torch.uint8, device=device)
@@ -847,7 +861,7 @@ def adamw(prepared: PreparedAdamw, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_
         _vector(step, 1, torch.int32, "step")
         h.step_dev = step.data_ptr()
     else:
-        h.step = step
+        h.step = _int(step, "step")
     if isinstance(lr, torch.Tensor):
         _here(lr)
         _vector(lr, 1, torch.float32, "lr")

@@ -207,3 +207,27 @@ def test_adamw_numbers_that_fp32_does_not_hold():
         assert rc(**bad) == ARG, bad
     for good in (dict(), dict(eps=2.0 ** -126), dict(lr=0.0), dict(lr=-1e-3), dict(lr=1e38), dict(weight_decay=1e38)):
         assert rc(**good) == B.MOE_OK, good
+
+
+@pytest.mark.parametrize("make,T,cols", [
+    (lambda: torch.empty((2 ** 32 + 5, 1), device="meta"), 2 ** 32 + 5, 1),              # 5 rows in 32 bits
+    (lambda: torch.empty((2 ** 31, 2), device="meta"), 2 ** 31, 2),
+    (lambda: torch.empty((1, 2 ** 32 + 8), device="meta"), 1, 2 ** 32 + 8),
+    (lambda: torch.empty_strided((3, 8), (2 ** 32 + 8, 1), device="meta"), 3, 8),        # rows 8 apart
+    (lambda: torch.empty_strided((2 ** 32 + 5, 1), (1, 2), device="meta"), 2 ** 32 + 5, 1)])
+def test_sizes_beyond_32_bits_are_refused(make, T, cols):
+    with pytest.raises(B.MoeError, match="32-bit"):
+        B._rows(make(), T, cols, torch.float32, "x")
+
+
+def test_numbers_beyond_32_bits_are_refused():
+    R = _router()
+    for call in (lambda: B.router_workspace(R, 2 ** 32 + 5, "cpu"), lambda: B.norm_workspace(2 ** 32 + 5, 8, "cpu"),
+                 lambda: B.norm_workspace(5, 2 ** 32 + 8, "cpu"), lambda: B.make_router(2 ** 32 + 16, 2),
+                 lambda: B.make_router(16, 2 ** 32 + 2)):
+        with pytest.raises(B.MoeError, match="32-bit"):
+            call()
+    big = torch.empty_strided((3, 8), (2 ** 31 - 1, 1), device="meta")
+    assert B._rows(big, 3, 8, torch.float32, "x") == 2 ** 31 - 1
+    one = torch.empty_strided((1, 8), (2 ** 40, 1), device="meta")       # one row has no stride
+    assert B._rows(one, 1, 8, torch.float32, "x") == 8
