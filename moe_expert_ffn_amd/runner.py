@@ -124,6 +124,12 @@ class LayerRunner:
         torch.cuda.current_stream(self.dev).wait_stream(self.side)
 
 
+def _share(a, others):
+    """Whether tensor a lies in the memory of one of the others (all of them allocations of their own)."""
+    at = a.untyped_storage().data_ptr()
+    return any(t.untyped_storage().data_ptr() == at for t in others)
+
+
 class BlockRunner(LayerRunner):
     """The expert layer as a block of a model, trained: norm -> router -> layer -> norm, gate and
     residual, its gradients, and AdamW on its weights.
@@ -166,8 +172,12 @@ class BlockRunner(LayerRunner):
     def block_forward(self, x, mask=None):
         """out [T][d] of x [T][d]; mask [T] (optional): 0 where a row is padding, which, whatever it
         holds, passes the residual alone and reaches no weight's gradient.  The routing's losses are
-        in self.routed["losses"]."""
-        self.x, self.mask = x, mask
+        in self.routed["losses"].  x may be the out of an earlier call, which this one overwrites: such
+        a call has no backward pass, which would read x again."""
+        own = [self.n, self.y] + ([self.dy, self.dn, self.dx, self.dx_block] if self.with_backward else [])
+        if _share(x, own):
+            raise B.MoeError("x lies in a buffer of the runner that the call overwrites")
+        self.x, self.mask = None if _share(x, [self.out]) else x, mask
         B.norm_in(x, self.w_in, self.eps, self.n, self.rstd_in, mask=mask)
         torch.mm(self.n, self.w_router.t(), out=self.logits)
         r = B.router_forward(self.router, self.logits, self.routed, self.router_ws, self.status, mask)
@@ -185,7 +195,10 @@ class BlockRunner(LayerRunner):
         """Gradients of block_forward's last call from dout [T][d] and (optional) dlosses [2], those
         of the balance and z losses: dx, and dw1, dw2, dw_router, dw_in, dw_out, dgate in self."""
         if not self.with_backward or self.x is None:
-            raise B.MoeError("block_backward needs a runner with a backward pass, after block_forward")
+            raise B.MoeError("block_backward needs a runner with a backward pass, after block_forward of an "
+                             "x that is not the runner's out")
+        if _share(dout, [self.dy, self.dn, self.dx]):
+            raise B.MoeError("dout lies in a buffer of the runner that the call overwrites")
         r = self.routed
         B.norm_out_backward(dout, self.y, self.w_out, self.rstd_out, self.dy, self.dw_out,
                             self.norm_ws, self.gate, self.alpha, self.dgate, self.mask)
