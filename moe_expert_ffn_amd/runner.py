@@ -148,6 +148,8 @@ class BlockRunner(LayerRunner):
         if tuple(w_router.shape) != (self.E, d) or w_router.dtype != dt:
             raise B.MoeError(f"w_router: expected {(self.E, d)} of {dt}, got "
                              f"{tuple(w_router.shape)} of {w_router.dtype}")
+        if gate is not None and tuple(gate.shape) != (d,):
+            raise B.MoeError(f"gate: expected {(d,)}, got {tuple(gate.shape)}")
         self.w_router, self.w_in, self.w_out, self.gate = w_router, w_in, w_out, gate
         self.alpha, self.eps = alpha, eps
         self.router = B.make_router(self.E, self.k, dt, score, renorm, scale)
