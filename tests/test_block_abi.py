@@ -231,16 +231,3 @@ def test_numbers_beyond_32_bits_are_refused():
     assert B._rows(big, 3, 8, torch.float32, "x") == 2 ** 31 - 1
     one = torch.empty_strided((1, 8), (2 ** 40, 1), device="meta")       # one row has no stride
     assert B._rows(one, 1, 8, torch.float32, "x") == 8
-
-
-def test_block_takes_a_gate_of_features_only():
-    """A gate per token went through where T <= d, into a gradient of d numbers."""
-    from moe_expert_ffn_amd.runner import BlockRunner
-    w = dict(w1=torch.zeros(4, 256, 256), w2=torch.zeros(4, 256, 128), w_router=torch.zeros(4, 256),
-             w_in=torch.ones(256), w_out=torch.ones(256))
-    how = dict(act_dtype=torch.float32, T=8, k=2, beta=16, P=2, s=1, owner=torch.zeros(4, dtype=torch.int32),
-               with_backward=True)
-    for gate in (torch.ones(8, 1), torch.ones(1, 256), torch.ones(255), torch.ones(())):
-        with pytest.raises(B.MoeError, match="gate: expected"):
-            BlockRunner(**w, gate=gate, **how)
-    BlockRunner(**w, gate=torch.ones(256), **how)

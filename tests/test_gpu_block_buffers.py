@@ -56,3 +56,17 @@ def test_buffers_that_a_call_overwrites_are_refused():
             b.block_backward(getattr(b, name))
     b.dx_block.copy_(dout)                              # in place: dx over the dout that it adds
     assert torch.equal(b.block_backward(b.dx_block), ref)
+
+
+def test_block_takes_a_gate_of_features_only():
+    """A gate per token went through where T <= d, into a gradient of d numbers."""
+    say("[block-buffers] gate")
+    one = lambda *n: torch.ones(n, device=DEV)
+    for gate in (one(W.T, 1), one(1, W.d), one(W.d - 1), one()):
+        with pytest.raises(B.MoeError, match="gate: expected"):
+            _block(gate=gate)
+    b, x, dout = _block(gate=one(W.d))
+    b.block_forward(x)
+    b.block_backward(dout)
+    torch.cuda.synchronize()
+    assert b.dgate.shape == (W.d,) and int(b.status.item()) == 0
