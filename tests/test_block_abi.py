@@ -1,5 +1,7 @@
 """Host-side checks of the operators around the layer: refusals that return before any device work."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -231,3 +233,39 @@ def test_numbers_beyond_32_bits_are_refused():
     assert B._rows(big, 3, 8, torch.float32, "x") == 2 ** 31 - 1
     one = torch.empty_strided((1, 8), (2 ** 40, 1), device="meta")       # one row has no stride
     assert B._rows(one, 1, 8, torch.float32, "x") == 8
+
+
+def test_the_library_has_no_allocator():
+    """No entry point allocates memory, the host's neither: the library imports nothing that could."""
+    B.load()
+    r = subprocess.run(["nm", "-D", "--undefined-only", os.path.join(os.path.dirname(B.__file__), "libmoe_ffn.so")],
+                       capture_output=True, text=True, check=True)
+    names = {line.split()[-1].split("@")[0] for line in r.stdout.splitlines()}
+    bad = {n for n in names if n.startswith(("malloc", "calloc", "realloc", "posix_memalign", "_Zn", "hipMalloc", "hipHostMalloc",
+                                             "hipFree", "hipStreamSynchronize", "hipDeviceSynchronize", "hipMemset"))}
+    assert not bad and "hipLaunchKernel" in names
+
+
+def test_adamw_lists_that_share_memory():
+    """Every pair of buffers of a list's first and last tensor, whole or by the last four bytes."""
+    sizes = {"p": 2, "master": 4, "g": 2, "m": 1, "v": 1, "m_scale": 4, "v_scale": 4}     # bytes of an element
+    n, far = 256, 1 << 20
+    count = {k: n if "scale" not in k else n // 128 for k in sizes}
+
+    def rc(moved, onto, by, total):
+        arr = (B.AdamwTensor * total)()
+        for i in range(total):
+            for j, k in enumerate(sizes):
+                setattr(arr[i], k, far * (7 * i + j + 1))
+            arr[i].n, arr[i].p_dtype, arr[i].g_dtype = n, B.MOE_BF16, B.MOE_BF16
+        setattr(arr[0], moved, getattr(arr[total - 1], onto) + by)
+        return B.load().moe_adamw_prepare(arr, total, 8, ctypes.byref(B.AdamwList()), P, 1 << 30, None)
+
+    for total in (2, 33):
+        for a in sizes:
+            for b in sizes:
+                end = count[b] * sizes[b]
+                if a == b == "g":
+                    continue                                     # gradients may be shared
+                assert rc(a, b, end - 4, total) == ARG, (a, b)
+                assert rc(a, b, 0, total) == ARG, (a, b)
