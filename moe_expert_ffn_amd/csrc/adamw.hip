@@ -54,7 +54,6 @@ struct AdamArgs {
   const AdamTensor* t;
   const uint32_t* first;
   int tensors, item;
-  uint32_t items;
   float lr, beta1, beta2, c1, c2, eps, wd;   // c = 1 - beta
   double log_beta1, log_beta2;   // -infinity for 0; only with step_dev
   float bias1, bias2;            // 1 - beta^step without
@@ -385,7 +384,7 @@ int launch_adamw(const moe_adamw_list& l, const moe_adamw_hyper& h, hipStream_t 
   if (l.items == 0) return MOE_OK;
   const AdamTable tab = adamw_table(l.table, l.tensors);
   AdamArgs a{};
-  a.t = tab.t; a.first = tab.first; a.tensors = l.tensors; a.items = l.items; a.item = l.item;
+  a.t = tab.t; a.first = tab.first; a.tensors = l.tensors; a.item = l.item;
   a.lr = (float)h.lr; a.eps = (float)h.eps; a.wd = (float)h.weight_decay;
   a.beta1 = (float)h.beta1; a.c1 = (float)(1.0 - h.beta1); a.log_beta1 = std::log(h.beta1);
   a.beta2 = (float)h.beta2; a.c2 = (float)(1.0 - h.beta2); a.log_beta2 = std::log(h.beta2);

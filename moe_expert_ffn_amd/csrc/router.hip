@@ -639,11 +639,12 @@ size_t router_ws_bytes(int T, int E) {
 
 template <template <typename, int, int, int> class K, typename T, int SCORE>
 static void router_shape(const RouterArgs& a, int grid, hipStream_t st) {
-  if (K<T, 64, 16, SCORE>::kForward && router_halved(a.T, a.E)) {
-    if (a.E <= 256) K<T, 16, 16, SCORE>::go(a, grid, st);
-    else K<T, 32, 16, SCORE>::go(a, grid, st);
-    return;
-  }
+  if constexpr (K<T, 64, 16, SCORE>::kForward)           // the backward pass has no such variants
+    if (router_halved(a.T, a.E)) {
+      if (a.E <= 256) K<T, 16, 16, SCORE>::go(a, grid, st);
+      else K<T, 32, 16, SCORE>::go(a, grid, st);
+      return;
+    }
   if (a.E <= 64) K<T, 8, 8, SCORE>::go(a, grid, st);
   else if (a.E <= 128) K<T, 16, 8, SCORE>::go(a, grid, st);
   else if (a.E <= 256) K<T, 32, 8, SCORE>::go(a, grid, st);
