@@ -121,12 +121,12 @@ MOE_DEV float sqrt_nearest(float x) {
 // 1e-12) go scaled by 2^64, in a branch of whole waves.
 template <bool NEAREST> MOE_DEV void roots(const float* v, float* s) {
   auto root = [](float x) { return NEAREST ? sqrt_nearest(x) : __builtin_amdgcn_sqrtf(x); };
-  float low = v[0];
+  uint32_t low = __float_as_uint(v[0]);                  // magnitudes order as their words do
 #pragma unroll
-  for (int i = 1; i < 8; ++i) low = fminf(low, v[i]);
+  for (int i = 1; i < 8; ++i) low = min(low, __float_as_uint(v[i]));
 #pragma unroll
   for (int i = 0; i < 8; ++i) s[i] = root(v[i]);
-  if (__any(low < 0x1p-96f)) {
+  if (__any(low < __float_as_uint(0x1p-96f))) {
     asm volatile("");
 #pragma unroll
     for (int i = 0; i < 8; ++i)
