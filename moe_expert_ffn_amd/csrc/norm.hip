@@ -158,7 +158,10 @@ __global__ __launch_bounds__(RowsOf<NT>::WG) void k_norm(NormArgs a) {
 // fixed by the grid.  A row's loads are issued before the sum of the row before it is joined.  Bound
 // by HBM: before the block 4099 x 7168 bf16 with residual and feature gate 353 MB and 15 MB of partial
 // sums in 67 us (5.5 TB/s); after it 1000 x 1023 fp32 5.2 us.  Rows of several pieces a thread (bf16
-// above 8192 features, fp32 above 4096) reach 3.4 to 4.8 TB/s.
+// above 8192 features, fp32 above 4096) reach 3.7 to 5.4 TB/s at 3000 rows of 8192, 12000 and 16384: x / rms
+// and its gradient of every piece stand in registers, of which the variants with FEAT spill some before the
+// block (fp32 43, bf16 14; after it fp32 8) and fp32's without it 26.  So does one more, of up to 8 bf16
+// features with FEAT before the block (3).
 constexpr int kNormWG = 1024;
 template <typename T, int VE, int NT, int KC, bool OUT, bool FEAT>
 __global__ __launch_bounds__(kNormWG) void k_norm_bwd(NormArgs a) {

@@ -203,11 +203,12 @@ MOE_DEV float block_sum(float s, float* red, int waves) {
 // Forward.  Each group takes rows in turn; its lanes keep the sums of P of
 // their own experts in registers, so the sums' order is fixed by the grid,
 // which follows from T and E alone.  One workgroup writes the totals itself;
-// more leave partial sums for k_router_totals.  16 x 128 bf16, k 8: 3.9 us, the
-// latency of one row; 8192 x 128 fp32 6.6 us (4.2 MB, 0.85 us at HBM's rate) and
-// 65521 x 256 bf16 36 us (33.5 MB): bound by the VALU, some 40 instructions a
-// choice and wave of two or four rows, 35 a logit of a lane.  The next row is
-// fetched while this one is worked on.
+// more leave partial sums for k_router_totals.  By the kernel trace 16 x 128 bf16, k 8: 3.8 us, the
+// latency of one row; 8192 x 128 fp32 6.6 us (4.2 MB, 0.85 us at HBM's rate), 65521 x 256 bf16 28 us (sigmoid
+// 31; 33.5 MB), 131072 x 512 fp32 136 us (268 MB): bound by the VALU, which works in 95 to 97% of the busy CUs'
+// cycles of the two large ones (SQ_ACTIVE_INST_VALU over SQ_BUSY_CU_CYCLES; 50% at 8192 x 128): some 40
+// instructions a choice and wave of two or four rows, 35 a logit of a lane.  The next row is fetched while
+// this one is worked on.
 template <typename T, int L, int V, int SCORE>
 __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
   constexpr int G = kRouterThreads / L;                  // rows at a time
@@ -448,11 +449,11 @@ __global__ __launch_bounds__(kTotalThreads) void k_router_totals(RouterArgs a) {
 // Backward: the row's scores again from its logits (they have to be read for
 // it in any case), every term in registers, one pass.  The k gate gradients
 // reach the lanes of their experts through LDS, a row's C places zeroed,
-// written and read by the row's own lanes (LDS keeps a wave's order).  4096 x 64
-// fp32 4.7 us; 65521 x 256 bf16 with sigmoid scores and a z loss 27.7 us (71 MB, 14
-// at HBM's rate): bound by the VALU and the latency of a row's five sums and its
-// passage through LDS.  Sigmoid scores with exponentials of their own: 31.4 us;
-// comparing every expert with every choice instead of LDS, and library
+// written and read by the row's own lanes (LDS keeps a wave's order).  By the kernel trace 4096 x 64
+// fp32 4.6 us; 65521 x 256 bf16 with both losses 26 us (sigmoid 30; 71 MB, 14 at HBM's rate): the VALU works in
+// 77% (83%) of the busy CUs' cycles, the rest is the latency of a row's five sums and its passage through
+// LDS; 131072 x 512 fp32 98 us, 5.5 TB/s of 541 MB.  Sigmoid scores with exponentials of their own: 31.4 us
+// against 27.8 in replays of a graph; comparing every expert with every choice instead of LDS, and library
 // exponentials: 105 us.
 template <typename T, int L, int V, int SCORE>
 __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
@@ -706,8 +707,8 @@ int launch_router_bwd(const moe_router& R, const void* logits, int ld, const uin
   a.ids_in = ids; a.dlogp = dlogp; a.counts_in = counts; a.live_in = live; a.dlosses = dlosses;
   a.dlogits = dlogits; a.ld_out = (size_t)ld_out;
   const int G = kRouterThreads / router_lanes(R.E);
-  // four waves a SIMD, what most variants' registers allow at once: 65521 x 256 bf16 25.8 us (sigmoid 27.7),
-  // with twice as many, the last of them alone, 25.8 (28.5), with one round of rows each 40.8 (43.5)
+  // four waves a SIMD, what most variants' registers allow at once: 65521 x 256 bf16 25.8 us (sigmoid 27.7)
+  // in replays of a graph, with twice as many, the last of them alone, 25.8 (28.5), with one round of rows each 40.8 (43.5)
   const int grid = (int)std::min<long long>(((long long)T + G - 1) / G, 256 * 4);
   router_kind<BwdK>(R, a, grid, st);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
