@@ -587,12 +587,14 @@ int moe_norm_out_backward(const moe_norm* N, const void* dout, int lddo, const v
  * v_scale [ceil(n / MOE_ADAMW_BLOCK)]): value = code * scale, scale = (largest
  * finite magnitude of the block) / 448.  Codes are rounded at random: rounded
  * to nearest, a state whose change per step is below half a code step would
- * never move.  A sqrt(v) that is not 0 is rounded to one code step (2^-9 scale) at
- * least: m is rounded apart from it, and over a sqrt(v) of 0 one step of m would be
- * an update of hundreds of lr.  (An element whose sqrt(v) is below that step, some
- * 2^-18 of its block's largest, is updated by less than without rounding.)  A block
- * whose magnitudes are all below 2^-100 is stored as zeros; a state that is not
- * finite becomes the NaN code of its element alone.
+ * never move.  Where m's code is not 0, sqrt(v)'s is 1 at least: rounded to 0 apart
+ * from m, it would make updates of thousands of lr.  (Unless |m| is above 2 C s_v +
+ * D s_m, with s the states' code steps, 2^-9 scale, C = (1 - beta1) / sqrt((1 - beta2)
+ * (1 - beta1^2 / beta2)), infinite from beta1^2 = beta2 on, and D = 2.5 / sqrt(1 -
+ * beta1^2): no gradients give it with a sqrt(v) below s_v, and codes that come from
+ * elsewhere keep their rounding.)  A block whose magnitudes are all below 2^-100 is
+ * stored as zeros; a state that is not finite becomes the NaN code of its element
+ * alone.
  * Start with zero codes and zero scales.
  * The random word of element i of the list's tensor j at step t is
  *   mix(i G + mix(seed + t G + j C3)),  mix(x): x ^= x >> 16; x *= C2; x ^= x >> 15

@@ -55,6 +55,7 @@ struct AdamArgs {
   const uint32_t* first;
   int tensors, item;
   float lr, beta1, beta2, c1, c2, eps, wd;   // c = 1 - beta
+  float under_v, under_m;        // 8-bit states: limit of root_under_m, per sqrt(v)'s over m's scale and of m alone
   double log_beta1, log_beta2;   // -infinity for 0; only with step_dev
   float bias1, bias2;            // 1 - beta^step without
   int step;
@@ -147,11 +148,7 @@ MOE_DEV uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 // above 448, which no u carries to the next code, so no clamp is needed.
 // Every operation is one fp32 rounding in this order, so that equal states give
 // equal codes wherever they are computed so.
-// SIGNED: x may be negative (m).  Else x is a root, of which no more than a value of 0 has the code 0:
-// m and sqrt(v) are rounded by different bits, and where m came out as a step and sqrt(v) as nothing, the
-// next update was hundreds of learning rates (the quotient of m's step by sqrt((1 - beta2) g^2) of a small
-// g).  With at least a step under it, m's step counts no more than the block's largest m by its largest
-// sqrt(v).  u: bits SHIFT..SHIFT + 15 of word.
+// SIGNED: x may be negative.  u: bits SHIFT..SHIFT + 15 of word.
 template <bool SIGNED, int SHIFT>
 MOE_DEV void to_e4m3(float* x, const uint32_t* word, uint8_t* codes, float* scale) {
 #pragma clang fp contract(off)
@@ -186,8 +183,7 @@ MOE_DEV void to_e4m3(float* x, const uint32_t* word, uint8_t* codes, float* scal
     const float u = __builtin_fmaf((float)(uint16_t)(word[i] >> SHIFT), 0x1p-19f, 0x1p-20f);
     const float t = __builtin_fmaf(u, octave, y);
     const int b = (int)(__float_as_uint(t) >> 20) - (120 << 3), c = (int)(t * 512.f);
-    const uint32_t least = SIGNED ? 0u : min(__float_as_uint(y), 1u);
-    code[i] = max((uint32_t)max(min(b, c), min(max(b, c), 8)), least);
+    code[i] = (uint32_t)max(min(b, c), min(max(b, c), 8));
   }
   uint32_t packed[2];
 #pragma unroll
@@ -202,6 +198,31 @@ MOE_DEV void to_e4m3(float* x, const uint32_t* word, uint8_t* codes, float* scal
     packed[h] |= nan[h];
   }
   __builtin_memcpy(codes, packed, 8);
+}
+
+// m and sqrt(v) are rounded by different bits.  Where m comes out as a step and sqrt(v) as 0, the next update
+// is m's step over sqrt((1 - beta2) g^2) of a small g: thousands of lr.  So a sqrt(v) of code 0 under an m
+// that is not 0 becomes the code 1.  `most` (of the block, in m's code units): what m may be for that.  All
+// gradients give |m| <= C sqrt(v) (Cauchy-Schwarz over the two sums' weights), here of less than a step of
+// sqrt(v) and taken twice for the rounding of larger codes, and m's own rounding adds up to D of its
+// steps, five deviations; an m above is no optimizer's, and its codes stay as they are rounded.
+// Four codes in a word, each compared in its byte's upper bit; few waves have a code of 0 at all (looking
+// first took 604M elements from 1425 to 1408 us).
+MOE_DEV void root_under_m(const AdamArgs& a, const uint8_t* mc, float ms, uint8_t* vc, float vs) {
+  constexpr uint32_t kUpper = 0x80808080u, kRest = 0x7F7F7F7Fu;
+  uint32_t m[2], v[2];
+  __builtin_memcpy(m, mc, 8);
+  __builtin_memcpy(v, vc, 8);
+  if (!__any(((v[0] + kRest) & (v[1] + kRest) & kUpper) != kUpper)) return;
+  const float most = vs > 0.f ? fminf(__builtin_fmaf(a.under_v, vs * __builtin_amdgcn_rcpf(ms), a.under_m), 448.f) : 0.f;
+  const int b = (int)(__float_as_uint(most) >> 20) - (120 << 3), c = (int)(most * 512.f);
+  const uint32_t least = kUpper | (uint32_t)max(min(b, c), min(max(b, c), 8)) * 0x01010101u;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t w = m[h] & kRest;                     // NaN's code is above every limit
+    v[h] |= ((least - w) & (w + kRest) & ~(v[h] + kRest) & kUpper) >> 7;
+  }
+  __builtin_memcpy(vc, v, 8);
 }
 
 // 1 - beta^t, from log(beta) in double: no cancellation at beta near 1
@@ -275,6 +296,7 @@ MOE_DEV void adam8(const AdamArgs& a, const AdamTensor& t, const AdamRates& h, u
     }
     to_e4m3<true, 0>(m, word, mc, &ms);
     to_e4m3<false, 16>(v, word, vc, &vs);
+    root_under_m(a, mc, ms, vc, vs);
     store8<uint8_t, FULL>((uint8_t*)t.m + at, n, mc);
     store8<uint8_t, FULL>((uint8_t*)t.v + at, n, vc);
     if (n > 0 && (threadIdx.x & 15) == 0) {
@@ -309,10 +331,9 @@ MOE_DEV void adam8(const AdamArgs& a, const AdamTensor& t, const AdamRates& h, u
 
 // One pass over everything a step touches; a workgroup an item.  By the kernel trace, with 32-bit states
 // 24 bytes an element, 604M elements in 2.63 ms (5.5 TB/s; a 1 GiB copy reaches 4.96): bound by HBM.  With 8-bit
-// states, bf16 parameters and fp32 gradients 12.1 bytes, 1.39 ms (5.2 TB/s), bound by HBM and the VALU
+// states, bf16 parameters and fp32 gradients 12.1 bytes, 1.41 ms (5.2 TB/s), bound by HBM and the VALU
 // alike: 80 VALU instructions an element (SQ_INSTS_VALU) are 1.23 ms of the chip at 2.4 GHz, which is why
-// codes are converted by hardware, rounded as whole numbers and never divided.  (The code of 1 under a
-// small root and the roots of subnormal v took 1.375 to 1.394 ms.)  A persistent grid was 8% slower,
+// codes are converted by hardware, rounded as whole numbers and never divided.  A persistent grid was 8% slower,
 // non-temporal accesses 3% faster here but 20% slower where the tensors fit the caches.
 template <int BITS>
 __global__ __launch_bounds__(kAdamThreads, 4) void k_adamw(AdamArgs a) {
@@ -389,6 +410,10 @@ int launch_adamw(const moe_adamw_list& l, const moe_adamw_hyper& h, hipStream_t 
   a.lr = (float)h.lr; a.eps = (float)h.eps; a.wd = (float)h.weight_decay;
   a.beta1 = (float)h.beta1; a.c1 = (float)(1.0 - h.beta1); a.log_beta1 = std::log(h.beta1);
   a.beta2 = (float)h.beta2; a.c2 = (float)(1.0 - h.beta2); a.log_beta2 = std::log(h.beta2);
+  const double b1 = h.beta1, b2 = h.beta2;
+  const double C = b1 * b1 < b2 ? (1 - b1) / std::sqrt((1 - b2) * (1 - b1 * b1 / b2)) : HUGE_VAL;
+  a.under_v = (float)(2 * C / 512);
+  a.under_m = (float)(2.5 / std::sqrt(1 - b1 * b1) / 512);
   a.bias1 = h.step_dev ? 1.f : bias(a.log_beta1, h.step);
   a.bias2 = h.step_dev ? 1.f : bias(a.log_beta2, h.step);
   a.step = h.step; a.seed = h.seed;

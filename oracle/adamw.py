@@ -4,9 +4,9 @@
     p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
 in fp64.  8-bit states hold m and sqrt(v) in blocks of 128 as e4m3 codes times
 a scale, the block's largest finite magnitude over 448, rounded up with the
-probability of the part cut off, a sqrt(v) that is not 0 to the code 1 at
-least; the random words are a hash of the seed, the step, the tensor's place in
-its list and the element's index.
+probability of the part cut off, a sqrt(v) under an m that is not 0 to the code
+1 at least; the random words are a hash of the seed, the step, the tensor's
+place in its list and the element's index.
 """
 from __future__ import annotations
 
@@ -56,13 +56,24 @@ def block_tops(x):
     return np.where(a < 2.0 ** -100, 0.0, a)
 
 
-def encode(x, u16, root=None):
+def under_m(m_codes, m_scales, v_scales, b1, b2):
+    """Where a sqrt(v) of code 0 becomes 1: m's code is not 0 and no more than gradients give with a sqrt(v) below a
+    code step, |m| <= C sqrt(v) by Cauchy-Schwarz (twice, for the rounding of larger codes), and five deviations of
+    m's own rounding.  (Which of them, the limit in m's code units)."""
+    C = (1 - b1) / np.sqrt((1 - b2) * (1 - b1 * b1 / b2)) if b1 * b1 < b2 else np.inf
+    with np.errstate(divide="ignore", invalid="ignore"):
+        most = 2 * C / 512 * (v_scales / m_scales) + 2.5 / np.sqrt(1 - b1 * b1) / 512
+    most = np.minimum(np.where((v_scales > 0) & (m_scales > 0), most, 0.0), 480.0)      # above every code but NaN's
+    most = np.repeat(most, BLOCK)[:m_codes.size]
+    mag = np.abs(decode(m_codes, np.ones(m_scales.size)))
+    return (mag > 0) & (mag <= most), most
+
+
+def encode(x, u16, m=None):
     """(codes, scales, distance): distance of the sum that is cut to the next whole number, in code
     steps -- where it is within the arithmetic's error, the neighbouring code is right as well.
-    root: x is sqrt(v), whose codes are 1 at least where it is not 0; None: where nothing in x is
-    negative (m of a block without a negative element differs from that only below one code step)."""
-    if root is None:
-        root = not (x < 0).any()
+    m: of x = sqrt(v), (m's codes, m's scales, b1, b2).  Without it the codes of 0 of an x that has no negative
+    element, which may be such roots, have a distance of 0: the code 1 may be right too."""
     top = block_tops(x)
     per = np.repeat(top, BLOCK)[:x.size]
     fin = np.isfinite(x)
@@ -70,10 +81,13 @@ def encode(x, u16, root=None):
     ex = np.clip(np.floor(np.log2(np.maximum(y, 2.0 ** -20))), -6, 8).astype(np.int64)
     s = np.ldexp(y, 3 - ex) + (u16 + 0.5) / 65536
     code = np.minimum((ex + 6) * 8 + np.floor(s).astype(np.int64), 126)
-    if root:
-        code = np.maximum(code, y > 0)
+    dist = np.abs(s - np.round(s))
+    if m is not None:
+        code = np.maximum(code, under_m(*m[:2], top / 448, *m[2:])[0])
+    elif not (x < 0).any():
+        dist = np.where((code == 0) & (y > 0), 0.0, dist)
     code = np.where(fin, code, 127) | np.where(x < 0, 128, 0)
-    return code.astype(np.uint8), top / 448, np.abs(s - np.round(s))
+    return code.astype(np.uint8), top / 448, dist
 
 
 def random_bf16(p, word):

@@ -21,10 +21,11 @@ def update_bound(ratio, steps, beta2):
     In units of the block's largest, whose code is always the last one and which follows m and sqrt(v) of a
     constant gradient without rounding, m and v after a step are weighted means of their last values and of
     the ratio r (of r^2).  Rounded to neighbours, m never leaves r's code cell upwards and sqrt(v) never
-    downwards; sqrt(v) is one step at least.  So the update's m is at most up(r) of the largest's m and its
-    sqrt(v) at least sqrt(beta2) of down(r) of the largest's the step before:
-      |update| <= up(r) / down(r) * sqrt((1 - beta2^t) / (beta2 (1 - beta2^(t - 1)))),
-    and 1 at t = 1, where no state is read.  2^-10 for 60 steps of 32-bit arithmetic: each state a few
+    downwards; under an m that is not 0 sqrt(v) is one step at least.  So the update's m is at most up(r) of the
+    largest's m and its sqrt(v) at least sqrt(beta2) of down(r) of the largest's the step before:
+      |update| <= up(r) / down(r) * sqrt((1 - beta2^t) / (beta2 (1 - beta2^(t - 1)))).
+    Where m's code is 0 the update's m is 0.1 g, its v at least (1 - beta2) g^2:
+      |update| <= 0.1 / (1 - 0.9^t) * sqrt((1 - beta2^t) / (1 - beta2)), which is 1 at t = 1.  2^-10 for 60 steps of 32-bit arithmetic: each state a few
     roundings (2^-24 each) a step."""
     cell = np.exp2(np.maximum(np.floor(np.log2(ratio * 448)), -6) - 3) / 448
     down = np.maximum(np.floor(ratio / cell * (1 - 1e-6)), 1) * cell
@@ -32,7 +33,8 @@ def update_bound(ratio, steps, beta2):
     t = np.arange(1, steps + 1, dtype=np.float64)
     with np.errstate(divide="ignore"):
         grow = np.sqrt((1 - beta2 ** t) / (beta2 * (1 - beta2 ** (t - 1))))
-    bound = (up / down)[None] * grow[:, None]
+        fresh = 0.1 / (1 - 0.9 ** t) * np.sqrt((1 - beta2 ** t) / (1 - beta2))
+    bound = np.maximum((up / down)[None] * grow[:, None], fresh[:, None])
     bound[0] = 1.0
     return bound * (1 + 2.0 ** -10)
 
@@ -48,7 +50,7 @@ def run_normal(beta2):
     the sqrt((1 - beta2) g^2) of a g below it is STEP / (sqrt(1 - beta2) 1e-7) = 200 and more."""
     i = np.arange(2000)
     w, u = 0.1 * 0.9 ** i, (1 - beta2) * beta2 ** i
-    exact = np.sqrt((w * w / u).sum())
+    exact = np.sqrt((w[u > 0] ** 2 / u[u > 0]).sum())
     rng = np.random.default_rng(12)
     scale = np.exp(rng.uniform(np.log(1e-7), np.log(1e-4), 128 * 64))
     scale[::128] = 1.0

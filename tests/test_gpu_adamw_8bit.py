@@ -49,27 +49,61 @@ def test_updates_of_noise_stay_near_those_of_32_bit_states(beta2):
     assert _updates(g_of, 100, beta2)[20:].max() <= limit
 
 
-def test_codes_of_far_apart_states_are_the_definitions():
+@pytest.mark.parametrize("beta2", [0.5, 0.99, 0.9999])
+def test_codes_of_far_apart_states_are_the_definitions(beta2):
     """Every code of sqrt(v) at each step against the oracle's from the same states; 16 u for the quotient and 16
-    for the sum that is cut, as in the tests of single steps: within 2^-15 of a whole number either code is right,
-    but no code is 0 where sqrt(v) is not."""
-    say("[adamw-8bit] codes")
-    g_of, _ = run_normal(0.99)
-    low = [0]
+    for the sum that is cut, as in the tests of single steps: within 2^-15 of a whole number either code is right
+    (u = 2^-24).  The limit of m carries some 6 u (two scales, a reciprocal, a sum); no code of m is as near to it."""
+    say(f"[adamw-8bit] codes beta2={beta2}")
+    g_of, _ = run_normal(beta2)
+    low = [0, 0]
+    b2, c2 = (float(np.float32(x)) for x in (beta2, 1 - beta2))
 
     def check(t, g, before, after):
         v0 = oadam.decode(before["v"], before["v_scale"]) ** 2
-        root = np.sqrt(0.99 * v0 + 0.01 * g * g)
-        codes, scales, dist = oadam.encode(root, oadam.words(5, t, 0, g.size) >> 16, root=True)
+        root = np.sqrt(b2 * v0 + c2 * g * g)
+        m = (after["m"], after["m_scale"].astype(np.float64))
+        codes, scales, dist = oadam.encode(root, oadam.words(5, t, 0, g.size) >> 16, (*m, 0.9, beta2))
+        under, most = oadam.under_m(*m, after["v_scale"].astype(np.float64), 0.9, beta2)
+        mag = np.abs(oadam.decode(m[0], np.ones(m[1].size)))
+        assert (np.abs(mag - most)[mag > 0] > 8 * 2.0 ** -24 * most[mag > 0]).all()
         # the error of sqrt(v) (8 u) and of the scale (16 u), in code steps of up to 16 a value
         near = dist <= 2.0 ** -15 + 24 * 16 * 2.0 ** -24
         assert (after["v"] == codes)[~near].all()
-        assert (after["v"][root > 0] > 0).all()
+        assert (after["v"][under] > 0).all()
         np.testing.assert_allclose(after["v_scale"], scales, rtol=16 * 2.0 ** -24)
-        low[0] += int((codes == 1).sum())
+        low[0] += int((under & (codes == 1)).sum())
+        low[1] += int(((codes == 0) & (root > 0)).sum())
 
-    _updates(g_of, 12, 0.99, check)
-    assert low[0] > 1000                                 # the elements that the floor is for are there
+    _updates(g_of, 12, beta2, check)
+    assert low[0] > 1000 and low[1] > 1000               # both sides of the rule are there
+
+
+def test_states_that_no_gradients_give_keep_their_codes():
+    """Codes at random, m's far above what gradients give with a sqrt(v) of 0: rounded as they are, and the others."""
+    say("[adamw-8bit] any codes")
+    n = 1 << 20
+    rng = np.random.default_rng(41)
+    dev = lambda a: [torch.from_numpy(a).to(DEV)]
+    for beta2, vs in ((0.99, 1e-3), (0.999, 1e-5), (0.5, 1e-3)):
+        mc = (rng.integers(0, 127, n) | rng.integers(0, 2, n) << 7).astype(np.uint8)
+        vc = (rng.integers(0, 127, n) * (rng.random(n) < 0.5)).astype(np.uint8)
+        sc = [((rng.random(n // 128) + 0.5) * x / 448).astype(np.float32) for x in (1e-4, vs)]
+        g = (rng.standard_normal(n) * 1e-8).astype(np.float32)       # sqrt(v) far below a step where its code was 0
+        s = {"p": dev(np.zeros(n, np.float32)), "g": dev(g), "m": dev(mc), "v": dev(vc), "m_scale": dev(sc[0]),
+             "v_scale": dev(sc[1])}
+        B.adamw(B.make_adamw(**s), lr=1e-3, beta1=0.9, beta2=beta2, step=3, seed=8)
+        torch.cuda.synchronize()
+        b2, c2 = (float(np.float32(x)) for x in (beta2, 1 - beta2))
+        root = np.sqrt(b2 * oadam.decode(vc, sc[1]) ** 2 + c2 * g.astype(np.float64) ** 2)
+        m = (s["m"][0].cpu().numpy(), s["m_scale"][0].double().cpu().numpy())
+        codes, _, dist = oadam.encode(root, oadam.words(8, 3, 0, n) >> 16, (*m, 0.9, beta2))
+        _, most = oadam.under_m(*m, s["v_scale"][0].double().cpu().numpy(), 0.9, beta2)
+        mag = np.abs(oadam.decode(m[0], np.ones(m[1].size)))
+        near = (dist <= 2.0 ** -15 + 24 * 16 * 2.0 ** -24) | ((mag > 0) & (np.abs(mag - most) <= 8 * 2.0 ** -24 * most))
+        got = s["v"][0].cpu().numpy()
+        assert (got == codes)[~near].all() and near.mean() < 0.01
+        assert ((codes == 0) & (mag > 0)).any() == (beta2 > 0.5) and ((codes == 1) & (root < 1e-8)).any()
 
 
 @pytest.mark.parametrize("eps", [1e-8, 1e-25])
