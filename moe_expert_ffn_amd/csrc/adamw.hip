@@ -332,7 +332,7 @@ MOE_DEV void adam8(const AdamArgs& a, const AdamTensor& t, const AdamRates& h, u
 // One pass over everything a step touches; a workgroup an item.  By the kernel trace, with 32-bit states
 // 24 bytes an element, 604M elements in 2.63 ms (5.5 TB/s; a 1 GiB copy reaches 4.96): bound by HBM.  With 8-bit
 // states, bf16 parameters and fp32 gradients 12.1 bytes, 1.41 ms (5.2 TB/s), bound by HBM and the VALU
-// alike: 80 VALU instructions an element (SQ_INSTS_VALU) are 1.23 ms of the chip at 2.4 GHz, which is why
+// alike: 78 VALU instructions an element (SQ_INSTS_VALU) are 1.21 ms of the chip at 2.4 GHz, which is why
 // codes are converted by hardware, rounded as whole numbers and never divided.  A persistent grid was 8% slower,
 // non-temporal accesses 3% faster here but 20% slower where the tensors fit the caches.
 template <int BITS>
