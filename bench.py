@@ -316,7 +316,7 @@ def reduce_bytes(case, w):
 # WRITE_SIZE per dispatch, scaled by the reading of a plain copy kernel of
 # known size), valid only for the kernel sources it was measured on.
 PROFILED_TRAFFIC = {"kernel": "bwd.dW", "workload": "qwen3_bf16_fwdbwd", "kappa": 1.0, "fixed": False,
-                    "source": "cfca93aee4a0fe6e", "bytes": 3336512503,
+                    "source": "1cc3733573d0afe0", "bytes": 3330899617,
                     "summary": "profiles/k_stream_SrcDwT_qwen3_bf16_fwdbwd_hbm_traffic.md"}
 
 

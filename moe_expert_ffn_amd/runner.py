@@ -213,7 +213,9 @@ class BlockRunner(LayerRunner):
 
     def make_optimizer(self, state_bits=32):
         """AdamW states (zeros) for the block's weights; state_bits 32 (fp32) or 8 (e4m3 codes and
-        a scale for 128 of them)."""
+        a scale for 128 of them).  One list: all weights, the norms' and the gate too, take the same rate
+        and decay, and bf16 ones have no fp32 copy.  Where they shall not, binding.make_adamw takes lists of
+        any of these weights and gradients."""
         if not self.with_backward or self.layer.w_dtype == B.MOE_FP8_E4M3:
             raise B.MoeError("the optimizer needs a runner with a backward pass and fp32 or bf16 weights")
         w1, w2 = self.keep[:2]
