@@ -126,8 +126,8 @@ class LayerRunner:
 
 def _share(a, others):
     """Whether tensor a lies in the memory of one of the others (all of them allocations of their own)."""
-    at = a.untyped_storage().data_ptr()
-    return any(t.untyped_storage().data_ptr() == at for t in others)
+    at = a.untyped_storage().data_ptr()                  # 0: empty
+    return at != 0 and any(t.untyped_storage().data_ptr() == at for t in others)
 
 
 class BlockRunner(LayerRunner):

@@ -19,7 +19,7 @@ def _block(**kw):
     par = dict(w1=rnd(W.E, 2 * W.d_ff, W.d, scale=W.d ** -0.5), w2=rnd(W.E, W.d, W.d_ff, scale=W.d ** -0.5),
                w_router=rnd(W.E, W.d, scale=W.d ** -0.5), w_in=1 + 0.1 * rnd(W.d), w_out=1 + 0.1 * rnd(W.d))
     owner = torch.from_numpy(contiguous_owners(W.E, W.P))
-    b = BlockRunner(**par, act_dtype=torch.float32, T=W.T, k=W.k, beta=W.beta, P=W.P, s=W.s, owner=owner,
+    b = BlockRunner(**par, act_dtype=torch.float32, T=kw.pop("T", W.T), k=W.k, beta=W.beta, P=W.P, s=W.s, owner=owner,
                     with_backward=True, **kw)
     return b, rnd(W.T, W.d), rnd(W.T, W.d)
 
@@ -70,3 +70,17 @@ def test_block_takes_a_gate_of_features_only():
     b.block_backward(dout)
     torch.cuda.synchronize()
     assert b.dgate.shape == (W.d,) and int(b.status.item()) == 0
+
+
+def test_block_of_no_tokens():
+    """Empty tensors share no memory, though all of them stand at address 0."""
+    say("[block-buffers] empty")
+    b, x, dout = _block(T=0)
+    assert b.block_forward(x[:0]).shape == (0, W.d)
+    assert b.block_backward(dout[:0]).shape == (0, W.d)
+    assert b.block_forward(torch.empty((0, W.d), device=DEV)).shape == (0, W.d)
+    assert b.block_backward(torch.empty((0, W.d), device=DEV)).shape == (0, W.d)
+    torch.cuda.synchronize()
+    assert int(b.status.item()) == 0
+    for t in (b.dw1, b.dw2, b.dw_router, b.dw_in, b.dw_out):
+        assert (t == 0).all()
