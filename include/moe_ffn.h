@@ -650,6 +650,55 @@ int moe_adamw_prepare(const moe_adamw_tensor* tensors, int count, int state_bits
  *   an eps, lr or weight_decay that is not finite in fp32. */
 int moe_adamw(const moe_adamw_list* list, const moe_adamw_hyper* h, void* stream);
 
+/* Global norm of a list of gradients, and clipping by it.  With s the sum of the squares of every
+ * element of the list and m = mult (*mult_dev where given):
+ *   norm = |m| sqrt(s),   scale = m where norm <= max_norm, else m max_norm / norm
+ * Squares and sums are made in 64 bits, in an order that the sizes fix.  scale is what moe_adamw
+ * takes as grad_scale, so that gradients are clipped without being written; m undoes a loss scale.
+ * A gradient that is not finite makes norm infinite or NaN (scale 0 or NaN, by the formula) and sets
+ * MOE_DEV_BAD_GRAD in *status_dev. */
+#define MOE_DEV_BAD_GRAD 32
+#define MOE_GRAD_MAX_TENSORS 4096
+typedef struct {
+  void* g;
+  int64_t n;
+  int dtype;             /* MOE_F32 or MOE_BF16 */
+} moe_grad_tensor;
+
+/* A prepared list (host): made by moe_grad_prepare, valid while its workspace and tensors are. */
+typedef struct {
+  const void* table;     /* device */
+  int tensors;
+  uint32_t items;        /* of consecutive elements of one tensor each */
+  int apart;             /* no two tensors share memory */
+} moe_grad_list;
+
+typedef struct {
+  double max_norm;       /* infinity: never clipped */
+  double mult;           /* not read when mult_dev is given */
+  const float* mult_dev; /* device, nullable */
+} moe_clip;
+
+size_t moe_grad_workspace_size(int tensors);
+
+/* Writes the list's table into ws on `stream`; *out (host) is what the calls below take.  Tensors may
+ * share memory (each counts in the norm) where they are not scaled in place.  The norm keeps its partial
+ * sums in ws: calls on one list must not overlap in time.
+ * Errors: MOE_ERR_ARG for a count outside [0, MOE_GRAD_MAX_TENSORS], n < 0, an unknown dtype or a null
+ *   or misaligned pointer of a tensor with n > 0; MOE_ERR_UNSUPPORTED for a list of 2^24 items of 8192
+ *   elements and more; MOE_ERR_WORKSPACE. */
+int moe_grad_prepare(const moe_grad_tensor* tensors, int count, moe_grad_list* out, void* ws,
+                     size_t ws_bytes, void* stream);
+
+/* norm [1], scale [1] fp32 (device).
+ * Errors: MOE_ERR_ARG for a null pointer, a max_norm that is not positive or a mult that is not finite. */
+int moe_grad_norm(const moe_grad_list* list, const moe_clip* clip, float* norm, float* scale,
+                  int32_t* status_dev, void* stream);
+
+/* Every element of the list times *scale (device), rounded to nearest; untouched where it is 1.
+ * Errors: MOE_ERR_ARG for a null pointer or a list whose tensors share memory. */
+int moe_grad_scale(const moe_grad_list* list, const float* scale, void* stream);
+
 /* Timing helpers so a caller without a HIP binding can time the stages:
  * create / destroy a hipEvent_t, and the milliseconds between two recorded
  * events (waits for `b`). */

@@ -20,7 +20,7 @@ MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0, -1
 MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
 PLAN_FWD, PLAN_BWD, PLAN_QUOTA = 0, 1, 2
 DEV_BAD_EXPERT, DEV_BAD_PLAN, DEV_BAD_OWNER, DEV_WAIT_TIMEOUT = 1, 2, 4, 8
-DEV_BAD_LOGIT = 16
+DEV_BAD_LOGIT, DEV_BAD_GRAD = 16, 32
 SCORES = {"softmax": 0, "sigmoid": 1}         # moe_score
 GATE_NONE, GATE_TOKEN, GATE_FEATURE = 0, 1, 2  # moe_gate_kind
 ADAMW_BLOCK = 128                             # MOE_ADAMW_BLOCK
@@ -52,6 +52,7 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_max_slots", "moe_max_blocks
            "moe_norm_workspace_size", "moe_norm_in", "moe_norm_in_backward", "moe_norm_out",
            "moe_norm_out_backward",
            "moe_adamw_workspace_size", "moe_adamw_prepare", "moe_adamw",
+           "moe_grad_workspace_size", "moe_grad_prepare", "moe_grad_norm", "moe_grad_scale",
            "moe_event_create", "moe_event_destroy", "moe_event_record", "moe_event_elapsed_ms",
            "moe_device_info"]
 
@@ -96,6 +97,19 @@ class AdamwHyper(ctypes.Structure):
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
                 ("step", ctypes.c_int), ("seed", ctypes.c_uint32), ("step_dev", ctypes.c_void_p),
                 ("lr_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p)]
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class GradList(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("tensors", ctypes.c_int), ("items", ctypes.c_uint32),
+                ("apart", ctypes.c_int)]
+
+
+class Clip(ctypes.Structure):
+    _fields_ = [("max_norm", ctypes.c_double), ("mult", ctypes.c_double), ("mult_dev", ctypes.c_void_p)]
 
 
 _lib = None
@@ -172,6 +186,14 @@ def load():
                                       _P, _SZ, _P]
     lib.moe_adamw.restype = _I
     lib.moe_adamw.argtypes = [ctypes.POINTER(AdamwList), ctypes.POINTER(AdamwHyper), _P]
+    lib.moe_grad_workspace_size.restype = _SZ
+    lib.moe_grad_workspace_size.argtypes = [_I]
+    lib.moe_grad_prepare.restype = _I
+    lib.moe_grad_prepare.argtypes = [ctypes.POINTER(GradTensor), _I, ctypes.POINTER(GradList), _P, _SZ, _P]
+    lib.moe_grad_norm.restype = _I
+    lib.moe_grad_norm.argtypes = [ctypes.POINTER(GradList), ctypes.POINTER(Clip), _P, _P, _P, _P]
+    lib.moe_grad_scale.restype = _I
+    lib.moe_grad_scale.argtypes = [ctypes.POINTER(GradList), _P, _P]
     lib.moe_event_create.argtypes = [ctypes.POINTER(_P)]
     lib.moe_event_destroy.argtypes = [_P]
     lib.moe_event_record.argtypes = [_P, _P]
@@ -873,6 +895,60 @@ def adamw(prepared: PreparedAdamw, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_
         _vector(grad_scale, 1, torch.float32, "grad_scale")
         h.grad_scale = grad_scale.data_ptr()
     _check(load().moe_adamw(ctypes.byref(prepared.list), ctypes.byref(h), _here(prepared.ws)))
+
+
+class PreparedGrads:
+    """A prepared list of gradients (moe_grad_prepare), its workspace, and the gradients, which it keeps
+    alive."""
+
+    def __init__(self, c_list, ws, keep):
+        self.list, self.ws, self.keep = c_list, ws, keep
+
+
+def make_grads(grads) -> PreparedGrads:
+    """Prepares a list of contiguous gradients (float32 or bfloat16) for grad_norm and grad_scale.  A list
+    of its own: it may hold the gradients of several optimizers."""
+    grads = list(grads)
+    count = len(grads)
+    arr = (GradTensor * max(count, 1))()
+    for i, g in enumerate(grads):
+        _vector(g, g.numel(), g.dtype, f"grads[{i}]")
+        _here(g)
+        arr[i].g, arr[i].n, arr[i].dtype = g.data_ptr(), g.numel(), _dtype_code(g.dtype, f"grads[{i}]")
+    size = int(load().moe_grad_workspace_size(count))
+    if size == 0:
+        raise MoeError("moe_grad_workspace_size rejected the list")
+    ws = torch.empty(size + 256, dtype=torch.uint8, device="cuda")
+    wsp, wsn = _aligned(ws)
+    out = GradList()
+    _check(load().moe_grad_prepare(arr, count, ctypes.byref(out), wsp, wsn, _stream()))
+    return PreparedGrads(out, ws, grads)
+
+
+def grad_norm(prepared: PreparedGrads, max_norm, norm, scale, status, mult=1.0):
+    """The list's norm (times |mult|) into norm [1], and into scale [1] what brings mult times the gradients
+    to a norm of max_norm at most: adamw's grad_scale, or grad_scale's.  mult is a number or a float32
+    tensor, read when the call runs."""
+    st = _here(prepared.ws, norm, scale, status)
+    c = Clip(max_norm, 1.0, None)
+    if isinstance(mult, torch.Tensor):
+        _here(mult)
+        _vector(mult, 1, torch.float32, "mult")
+        c.mult_dev = mult.data_ptr()
+    else:
+        c.mult = mult
+    _vector(norm, 1, torch.float32, "norm")
+    _vector(scale, 1, torch.float32, "scale")
+    _vector(status, 1, torch.int32, "status")
+    _check(load().moe_grad_norm(ctypes.byref(prepared.list), ctypes.byref(c), _at(norm), _at(scale), _at(status), st))
+    return norm
+
+
+def grad_scale(prepared: PreparedGrads, scale):
+    """Every gradient of the list times scale [1], in place."""
+    st = _here(prepared.ws, scale)
+    _vector(scale, 1, torch.float32, "scale")
+    _check(load().moe_grad_scale(ctypes.byref(prepared.list), _at(scale), st))
 
 
 class Events:

@@ -228,16 +228,6 @@ MOE_DEV void root_under_m(const AdamArgs& a, const uint8_t* mc, float ms, uint8_
 // 1 - beta^t, from log(beta) in double: no cancellation at beta near 1
 static __host__ __device__ float bias(double log_beta, int t) { return (float)-expm1(log_beta * t); }
 
-// The tensor that holds an item: how many of first[1..tensors] are at or below
-// it.  64 lanes look at a sorted table of up to 64 * 64 entries in two steps.
-MOE_DEV int tensor_of(const uint32_t* first, int tensors, uint32_t item) {
-  const int lane = threadIdx.x & 63;
-  const int i1 = (lane + 1) * 64;
-  const int blk = __popcll(__ballot(i1 <= tensors && first[min(i1, tensors)] <= item));
-  const int i2 = blk * 64 + 1 + lane;
-  return blk * 64 + __popcll(__ballot(i2 <= tensors && first[min(i2, tensors)] <= item));
-}
-
 struct AdamRates { float rate, root, keep, gs; };
 
 // Eight consecutive elements at `at` of tensor t (n of them there).
@@ -351,7 +341,7 @@ __global__ __launch_bounds__(kAdamThreads, 4) void k_adamw(AdamArgs a) {
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   const AdamRates h{lr / b1, 1.f / sqrtf(b2), 1.f - lr * a.wd, a.grad_scale ? *a.grad_scale : 1.f};
   const uint32_t item = blockIdx.x;
-  const int j = __builtin_amdgcn_readfirstlane(tensor_of(a.first, a.tensors, item));
+  const int j = __builtin_amdgcn_readfirstlane(list_place(a.first, a.tensors, item));
   const AdamTensor t = a.t[j];
   const uint32_t key = mix(a.seed + (uint32_t)step * kGold + (uint32_t)j * kRoot3);
   // whole blocks of 128 (a row of 16 lanes) take the wide accesses

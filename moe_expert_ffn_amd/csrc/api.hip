@@ -568,6 +568,64 @@ int moe_adamw(const moe_adamw_list* list, const moe_adamw_hyper* h, void* stream
   return launch_adamw(*list, *h, (hipStream_t)stream);
 }
 
+size_t moe_grad_workspace_size(int tensors) {
+  return tensors < 0 || tensors > MOE_GRAD_MAX_TENSORS ? 0 : grads_ws_bytes(tensors);
+}
+
+// Whether no two tensors of the list share memory; as extents_apart, only their numbers are sorted.
+static bool grads_apart(const moe_grad_tensor* t, int count) {
+  uint16_t order[MOE_GRAD_MAX_TENSORS];
+  int m = 0;
+  for (int i = 0; i < count; ++i)
+    if (t[i].n > 0) order[m++] = (uint16_t)i;
+  std::sort(order, order + m, [&](uint16_t a, uint16_t b) { return (uintptr_t)t[a].g < (uintptr_t)t[b].g; });
+  uintptr_t end = 0;
+  for (int i = 0; i < m; ++i) {
+    const moe_grad_tensor& a = t[order[i]];
+    if ((uintptr_t)a.g < end) return false;
+    end = std::max(end, (uintptr_t)a.g + (uintptr_t)a.n * (a.dtype == MOE_F32 ? 4 : 2));
+  }
+  return true;
+}
+
+int moe_grad_prepare(const moe_grad_tensor* tensors, int count, moe_grad_list* out, void* ws,
+                     size_t ws_bytes, void* stream) {
+  if (count < 0 || count > MOE_GRAD_MAX_TENSORS || !out || (count > 0 && !tensors)) return MOE_ERR_ARG;
+  long long total = 0;
+  for (int i = 0; i < count; ++i) {
+    const moe_grad_tensor& t = tensors[i];
+    if (t.n < 0 || !dtype_ok(t.dtype)) return MOE_ERR_ARG;
+    if (t.n == 0) continue;
+    if (t.n > (1ll << 43) || (total += t.n) > (1ll << 43)) return MOE_ERR_UNSUPPORTED;
+    if (!t.g || ((uintptr_t)t.g & (t.dtype == MOE_F32 ? 3 : 1))) return MOE_ERR_ARG;
+  }
+  if (!ws_ok(ws, ws_bytes, grads_ws_bytes(count))) return MOE_ERR_WORKSPACE;
+  moe_grad_list list{};
+  list.table = ws;
+  list.tensors = count;
+  list.apart = grads_apart(tensors, count);
+  const int rc = launch_grads_table(tensors, count, &list, (hipStream_t)stream);
+  if (rc == MOE_OK) *out = list;
+  return rc;
+}
+
+static bool grad_list_ok(const moe_grad_list* l) {
+  return l && l->table && l->tensors >= 0 && l->tensors <= MOE_GRAD_MAX_TENSORS && l->items < (1u << 24);
+}
+
+int moe_grad_norm(const moe_grad_list* list, const moe_clip* clip, float* norm, float* scale,
+                  int32_t* status_dev, void* stream) {
+  if (!grad_list_ok(list) || !clip || !norm || !scale || !status_dev || !(clip->max_norm > 0) ||
+      (!clip->mult_dev && !std::isfinite(clip->mult)))
+    return MOE_ERR_ARG;
+  return launch_grad_norm(*list, *clip, norm, scale, status_dev, (hipStream_t)stream);
+}
+
+int moe_grad_scale(const moe_grad_list* list, const float* scale, void* stream) {
+  if (!grad_list_ok(list) || !scale || !list->apart) return MOE_ERR_ARG;
+  return launch_grad_scale(*list, scale, (hipStream_t)stream);
+}
+
 int moe_event_create(void** ev) {
   if (!ev) return MOE_ERR_ARG;
   return hipEventCreate((hipEvent_t*)ev) == hipSuccess ? MOE_OK : MOE_ERR_HIP;

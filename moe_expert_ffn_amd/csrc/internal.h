@@ -102,6 +102,12 @@ size_t adamw_ws_bytes(int tensors);
 int launch_adamw_table(const moe_adamw_tensor* t, int count, moe_adamw_list* out, hipStream_t st);
 int launch_adamw(const moe_adamw_list& l, const moe_adamw_hyper& h, hipStream_t st);
 
+size_t grads_ws_bytes(int tensors);
+int launch_grads_table(const moe_grad_tensor* t, int count, moe_grad_list* out, hipStream_t st);
+int launch_grad_norm(const moe_grad_list& l, const moe_clip& c, float* norm, float* scale, int32_t* status,
+                     hipStream_t st);
+int launch_grad_scale(const moe_grad_list& l, const float* scale, hipStream_t st);
+
 int launch_forward(const Sizes& z, const LayerPtrs& L, const void* x, const float* gates,
                    const int32_t* counts, const int32_t* boff, const int32_t* row_to_slot,
                    const int32_t* slot_to_row, const int32_t* block_worker, void* y,

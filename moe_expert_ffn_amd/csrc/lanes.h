@@ -48,6 +48,16 @@ MOE_DEV void wave_lds_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// The place in a list of tensors that holds an item: how many of first[1..tensors] are at or below
+// it.  64 lanes look at a sorted table of up to 64 * 64 entries in two steps.
+MOE_DEV int list_place(const uint32_t* first, int tensors, uint32_t item) {
+  const int lane = threadIdx.x & 63;
+  const int i1 = (lane + 1) * 64;
+  const int blk = __popcll(__ballot(i1 <= tensors && first[min(i1, tensors)] <= item));
+  const int i2 = blk * 64 + 1 + lane;
+  return blk * 64 + __popcll(__ballot(i2 <= tensors && first[min(i2, tensors)] <= item));
+}
+
 MOE_DEV float elem_f(uint16_t h) { return bf2f(h); }
 MOE_DEV float elem_f(float f) { return f; }
 // N (even) values to the rows' type; bf16 in pairs, one instruction each

@@ -232,10 +232,18 @@ class BlockRunner(LayerRunner):
             if state_bits == 8 else None
         self.state = {"m": states(), "v": states(), "m_scale": scales(), "v_scale": scales()}
         self.optimizer = B.make_adamw(p, g, **self.state)
+        self.grads = B.make_grads(g)
+        self.grad_norm, self.grad_scale = (torch.zeros(1, device=self.dev) for _ in range(2))
         return self.optimizer
 
-    def optimizer_step(self, lr, step, **hyper):
-        """One AdamW step (binding.adamw's arguments) on the block's weights, in place."""
+    def optimizer_step(self, lr, step, max_norm=None, grad_scale=None, **hyper):
+        """One AdamW step (binding.adamw's arguments) on the block's weights, in place.  max_norm: the
+        gradients, times grad_scale (a number or a tensor), are first scaled down to this norm where theirs,
+        which self.grad_norm receives, is above it."""
         if self.optimizer is None:
             raise B.MoeError("make_optimizer first")
-        B.adamw(self.optimizer, lr, step=step, **hyper)
+        if max_norm is not None:
+            B.grad_norm(self.grads, max_norm, self.grad_norm, self.grad_scale, self.status,
+                        1.0 if grad_scale is None else grad_scale)
+            grad_scale = self.grad_scale
+        B.adamw(self.optimizer, lr, step=step, grad_scale=grad_scale, **hyper)
