@@ -474,6 +474,36 @@ int moe_router_forward(const moe_router* R, const void* logits, int ld,
                        int32_t* counts, float* prob_sum, int32_t* live, float* losses,
                        int32_t* status_dev, void* ws, size_t ws_bytes, void* stream);
 
+/* A choice by values instead of logits.  With s_te the score of the gates, softmax(l_t)_e or
+ * sigmoid(l_te), the value is v_te = s_te + bias_e: the bias steers the choice (moe_router_bias_update
+ * balances the experts with it) and enters no gate.  The E experts form `groups` groups of E / groups
+ * consecutive ones; a group's value is its best member's, or the sum of its two best (of one where only
+ * one can be chosen).  The top_groups best groups are open, and the chosen experts are the k largest
+ * values in them, in descending order; the lower index among equals, groups and experts alike.  Values are
+ * compared as 64-bit numbers.  An expert whose bias is NaN or -infinity is never chosen. */
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+typedef struct {
+  const float* bias;     /* [E] device, nullable */
+  int groups, top_groups;
+  int group_score;
+} moe_choice;
+
+/* moe_router_forward with a choice by values; gates, sums, losses and workspace are the same, and
+ * moe_router_backward is the gradient of both (the choice has none).  Without a bias and with all groups
+ * open it is moe_router_forward.
+ * Errors: as moe_router_forward; MOE_ERR_ARG for groups < 1 or that do not divide E, top_groups < 1 or >
+ *   groups, k > top_groups * E / groups or an unknown group_score; MOE_ERR_UNSUPPORTED for groups > 64. */
+int moe_router_forward_choice(const moe_router* R, const moe_choice* choice, const void* logits, int ld,
+                              const uint8_t* token_mask, int T, int32_t* topk_ids, float* gates,
+                              int32_t* counts, float* prob_sum, int32_t* live, float* losses,
+                              int32_t* status_dev, void* ws, size_t ws_bytes, void* stream);
+
+/* The balancing step of a bias: bias_e += rate * sign(mean(counts) - counts_e), in place, compared as
+ * whole numbers.  counts [E]: a batch's, or the sum of several.
+ * Errors: MOE_ERR_ARG for E < 1, a rate that is not finite or a null pointer; MOE_ERR_UNSUPPORTED for
+ *   E > 1024. */
+int moe_router_bias_update(const int32_t* counts, int E, float rate, float* bias, void* stream);
+
 /* Gradient of the logits.
  *   topk_ids, counts, live: moe_router_forward's, on the same logits and mask.
  *   dlogp [T][k] fp32 (nullable): p * dL/dp of each gate p, its gradient in log

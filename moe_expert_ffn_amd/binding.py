@@ -22,6 +22,7 @@ PLAN_FWD, PLAN_BWD, PLAN_QUOTA = 0, 1, 2
 DEV_BAD_EXPERT, DEV_BAD_PLAN, DEV_BAD_OWNER, DEV_WAIT_TIMEOUT = 1, 2, 4, 8
 DEV_BAD_LOGIT, DEV_BAD_GRAD = 16, 32
 SCORES = {"softmax": 0, "sigmoid": 1}         # moe_score
+GROUP_SCORES = {"max": 0, "top2": 1}          # moe_group_score
 GATE_NONE, GATE_TOKEN, GATE_FEATURE = 0, 1, 2  # moe_gate_kind
 ADAMW_BLOCK = 128                             # MOE_ADAMW_BLOCK
 EXEC_TWO_PHASE = 1              # MOE_EXEC_TWO_PHASE
@@ -49,6 +50,7 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_max_slots", "moe_max_blocks
            "moe_quantize_act_rows", "moe_forward",
            "moe_backward", "moe_backward_gates", "moe_gate_grad",
            "moe_router_workspace_size", "moe_router_forward", "moe_router_backward",
+           "moe_router_forward_choice", "moe_router_bias_update",
            "moe_norm_workspace_size", "moe_norm_in", "moe_norm_in_backward", "moe_norm_out",
            "moe_norm_out_backward",
            "moe_adamw_workspace_size", "moe_adamw_prepare", "moe_adamw",
@@ -71,6 +73,12 @@ class Layer(ctypes.Structure):
 class Router(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int), ("k", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("score", ctypes.c_int), ("renorm", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class Choice(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_score", ctypes.c_int)]
+    tensor = None                             # the bias, which the choice keeps alive
 
 
 class Norm(ctypes.Structure):
@@ -169,6 +177,10 @@ def load():
     lib.moe_router_forward.argtypes = [R, _P, _I, _P, _I] + [_P] * 7 + [_P, _SZ, _P]
     lib.moe_router_backward.restype = _I
     lib.moe_router_backward.argtypes = [R, _P, _I, _P, _I] + [_P] * 6 + [_I, _P]
+    lib.moe_router_forward_choice.restype = _I
+    lib.moe_router_forward_choice.argtypes = [R, ctypes.POINTER(Choice), _P, _I, _P, _I] + [_P] * 7 + [_P, _SZ, _P]
+    lib.moe_router_bias_update.restype = _I
+    lib.moe_router_bias_update.argtypes = [_P, _I, ctypes.c_float, _P, _P]
     lib.moe_norm_workspace_size.restype = _SZ
     lib.moe_norm_workspace_size.argtypes = [_I, _I]
     lib.moe_norm_in.restype = _I
@@ -652,6 +664,33 @@ def router_workspace(router: Router, T, device) -> torch.Tensor:
     return torch.empty(n + 256, dtype=torch.uint8, device=device)
 
 
+def make_choice(router: Router, bias=None, groups=1, top_groups=None, group_score="top2") -> Choice:
+    """A choice by values, score + bias [E] (float32, read when a forward pass runs; None: 0), in the
+    top_groups (None: all) best of so many groups of consecutive experts, by their best ("max") or the
+    sum of their two best ("top2")."""
+    if group_score not in GROUP_SCORES:
+        raise MoeError(f"group_score {group_score!r}: one of {sorted(GROUP_SCORES)}")
+    top_groups = groups if top_groups is None else top_groups
+    if not (1 <= top_groups <= groups <= 64 and router.E % groups == 0 and
+            router.k <= top_groups * (router.E // groups)):
+        raise MoeError(f"{top_groups} of {groups} groups are not supported for E={router.E}, k={router.k}")
+    if bias is not None:
+        _vector(bias, router.E, torch.float32, "bias")
+    c = Choice(_at(bias), groups, top_groups, GROUP_SCORES[group_score])
+    c.tensor = bias
+    return c
+
+
+def router_bias_update(bias, counts, rate):
+    """The balancing step of a choice's bias, in place: bias += rate * sign(mean(counts) - counts)."""
+    st = _here(bias, counts)
+    E = _int(bias.numel(), "bias")
+    _vector(bias, E, torch.float32, "bias")
+    _vector(counts, E, torch.int32, "counts")
+    _check(load().moe_router_bias_update(_at(counts), E, rate, _at(bias), st))
+    return bias
+
+
 def _router_args(router, logits, mask):
     if logits.dim() != 2:
         raise MoeError(f"logits: expected [T][E], got {tuple(logits.shape)}")
@@ -662,9 +701,12 @@ def _router_args(router, logits, mask):
     return T, ld, dt
 
 
-def router_forward(router: Router, logits, out: dict, ws, status, mask=None):
-    """Routes logits [T][E] into out (alloc_router): ids, gates, counts, prob_sum, live, losses."""
+def router_forward(router: Router, logits, out: dict, ws, status, mask=None, choice=None):
+    """Routes logits [T][E] into out (alloc_router): ids, gates, counts, prob_sum, live, losses.  choice
+    (make_choice): by values instead of logits."""
     st = _here(logits, mask, ws, status, *out.values())
+    if choice is not None and choice.tensor is not None:
+        _here(choice.tensor)
     T, ld, _ = _router_args(router, logits, mask)
     _vector(out["topk_ids"], T * router.k, torch.int32, "topk_ids")
     _vector(out["gates"], T * router.k, torch.float32, "gates")
@@ -674,10 +716,12 @@ def router_forward(router: Router, logits, out: dict, ws, status, mask=None):
     _vector(out["losses"], 2, torch.float32, "losses")
     _vector(status, 1, torch.int32, "status")
     wsp, wsn = _ws_at(ws)
-    _check(load().moe_router_forward(
-        ctypes.byref(router), _at(logits), ld, _at(mask), T, _at(out["topk_ids"]),
-        _at(out["gates"]), _at(out["counts"]), _at(out["prob_sum"]), _at(out["live"]),
-        _at(out["losses"]), _at(status), wsp, wsn, st))
+    args = (_at(logits), ld, _at(mask), T, _at(out["topk_ids"]), _at(out["gates"]), _at(out["counts"]),
+            _at(out["prob_sum"]), _at(out["live"]), _at(out["losses"]), _at(status), wsp, wsn, st)
+    if choice is None:
+        _check(load().moe_router_forward(ctypes.byref(router), *args))
+    else:
+        _check(load().moe_router_forward_choice(ctypes.byref(router), ctypes.byref(choice), *args))
     return out
 
 

@@ -363,18 +363,48 @@ size_t moe_router_workspace_size(const moe_router* R, int T) {
   return router_ws_bytes(T, R->E);
 }
 
-int moe_router_forward(const moe_router* R, const void* logits, int ld,
-                       const uint8_t* token_mask, int T, int32_t* topk_ids, float* gates,
-                       int32_t* counts, float* prob_sum, int32_t* live, float* losses,
-                       int32_t* status_dev, void* ws, size_t ws_bytes, void* stream) {
+static int router_forward(const moe_router* R, const moe_choice* C, const void* logits, int ld,
+                          const uint8_t* token_mask, int T, int32_t* topk_ids, float* gates,
+                          int32_t* counts, float* prob_sum, int32_t* live, float* losses,
+                          int32_t* status_dev, void* ws, size_t ws_bytes, void* stream) {
   const int rc = check_router(R, ld, T);
   if (rc != MOE_OK) return rc;
+  if (C) {
+    if (C->groups < 1 || R->E % C->groups || C->top_groups < 1 || C->top_groups > C->groups ||
+        R->k > C->top_groups * (R->E / C->groups) ||
+        (C->group_score != MOE_GROUP_MAX && C->group_score != MOE_GROUP_TOP2))
+      return MOE_ERR_ARG;
+    if (C->groups > kRouterMaxGroups) return MOE_ERR_UNSUPPORTED;
+  }
   if ((T > 0 && (!logits || !topk_ids || !gates)) || !counts || !prob_sum || !live || !losses ||
       !status_dev)
     return MOE_ERR_ARG;
   if (!ws_ok(ws, ws_bytes, router_ws_bytes(T, R->E))) return MOE_ERR_WORKSPACE;
-  return launch_router(*R, logits, ld, token_mask, T, topk_ids, gates, counts, prob_sum, live,
+  return launch_router(*R, C, logits, ld, token_mask, T, topk_ids, gates, counts, prob_sum, live,
                        losses, status_dev, ws, (hipStream_t)stream);
+}
+
+int moe_router_forward(const moe_router* R, const void* logits, int ld,
+                       const uint8_t* token_mask, int T, int32_t* topk_ids, float* gates,
+                       int32_t* counts, float* prob_sum, int32_t* live, float* losses,
+                       int32_t* status_dev, void* ws, size_t ws_bytes, void* stream) {
+  return router_forward(R, nullptr, logits, ld, token_mask, T, topk_ids, gates, counts, prob_sum, live, losses,
+                        status_dev, ws, ws_bytes, stream);
+}
+
+int moe_router_forward_choice(const moe_router* R, const moe_choice* choice, const void* logits, int ld,
+                              const uint8_t* token_mask, int T, int32_t* topk_ids, float* gates,
+                              int32_t* counts, float* prob_sum, int32_t* live, float* losses,
+                              int32_t* status_dev, void* ws, size_t ws_bytes, void* stream) {
+  if (!choice) return MOE_ERR_ARG;
+  return router_forward(R, choice, logits, ld, token_mask, T, topk_ids, gates, counts, prob_sum, live, losses,
+                        status_dev, ws, ws_bytes, stream);
+}
+
+int moe_router_bias_update(const int32_t* counts, int E, float rate, float* bias, void* stream) {
+  if (E < 1 || !std::isfinite(rate) || !counts || !bias) return MOE_ERR_ARG;
+  if (E > kMaxExperts) return MOE_ERR_UNSUPPORTED;
+  return launch_bias_update(counts, E, rate, bias, (hipStream_t)stream);
 }
 
 int moe_router_backward(const moe_router* R, const void* logits, int ld,

@@ -77,15 +77,16 @@ struct LayerPtrs {
   int act_dtype, w_dtype;
 };
 
-constexpr int kRouterMaxK = 32;
+constexpr int kRouterMaxK = 32, kRouterMaxGroups = 64;
 size_t router_ws_bytes(int T, int E);
-int launch_router(const moe_router& R, const void* logits, int ld, const uint8_t* mask, int T,
+int launch_router(const moe_router& R, const moe_choice* C, const void* logits, int ld, const uint8_t* mask, int T,
                   int32_t* ids, float* gates, int32_t* counts, float* psum, int32_t* live,
                   float* losses, int32_t* status, void* ws, hipStream_t st);
 int launch_router_bwd(const moe_router& R, const void* logits, int ld, const uint8_t* mask, int T,
                       const int32_t* ids, const float* dlogp, const int32_t* counts,
                       const int32_t* live, const float* dlosses, void* dlogits, int ld_out,
                       hipStream_t st);
+int launch_bias_update(const int32_t* counts, int E, float rate, float* bias, hipStream_t st);
 void launch_gate_grad(const void* z, const void* dz, int dtype, const int32_t* row_to_slot,
                       int rows, int slots, int dff, float* dlogp, hipStream_t st);
 

@@ -9,6 +9,7 @@ namespace moe {
 struct OpAdd { template <typename V> MOE_DEV V operator()(V a, V b) const { return a + b; } };
 struct OpMax { template <typename V> MOE_DEV V operator()(V a, V b) const { return a > b ? a : b; } };
 struct OpMaxF { MOE_DEV float operator()(float a, float b) const { return fmaxf(a, b); } };
+struct OpOr { template <typename V> MOE_DEV V operator()(V a, V b) const { return a | b; } };
 struct OpMin { template <typename V> MOE_DEV V operator()(V a, V b) const { return a < b ? a : b; } };
 
 // Value of another lane by a DPP control (a register move inside the VALU;

@@ -14,6 +14,9 @@ namespace moe {
 // pieces); a workgroup of four waves holds 256 / L rows at a time.
 constexpr int kRouterThreads = 256;
 constexpr int kRouterMaxWG = 1024;       // workgroups, and so partial sums, of the forward
+// The sum of a row's chosen shares below which they are formed anew from their logarithms: single ones next
+// to 2^-126 have lost bits, a part of 2^-26 of the sum at most here.
+constexpr float kFewShares = 0x1p-100f;
 constexpr int kTotalThreads = 1024, kTotalCols = 16;
 static_assert(kRouterMaxWG <= kTotalThreads, "a thread for every partial of the totals' small sums");
 static_assert(kMaxExperts <= 64 * kTotalCols, "a lane for every workgroup of the totals");
@@ -43,6 +46,8 @@ struct RouterArgs {
   size_t ld, ld_out;
   int T, E, k, renorm, parts;
   float scale;
+  const float* bias;   // a choice by values: added to the scores (nullable)
+  int groups, top_groups, two, gsize;    // the groups, how many are open, value of the two best members, E / groups
 };
 
 // Order of 32-bit floats as unsigned integers, 0 for what is never chosen
@@ -134,6 +139,11 @@ template <int SCORE> struct Score {
   }
 };
 
+// The logarithm of a score, up to the softmax's sum.
+template <int SCORE> MOE_DEV float log_score(float l) {
+  return SCORE == MOE_SCORE_SOFTMAX ? l : fminf(l, 0.f) - log1pf(exp_of(-fabsf(l)));
+}
+
 template <int L, int V> MOE_DEV float row_top(const float* v) {
   float m = v[0];
 #pragma unroll
@@ -198,6 +208,58 @@ MOE_DEV float block_sum(float s, float* red, int waves) {
   s = 0.f;
   for (int i = 0; i < waves; ++i) s += red[i];
   return s;
+}
+
+// The end of a forward kernel: a workgroup's sums, over its groups of lanes and then its four waves, each
+// in a fixed order, as totals (one workgroup) or as partial sums for k_router_totals.  psum, z, n: a lane's;
+// sc: the workgroup's counts.
+template <int L, int V>
+MOE_DEV void router_sums(const RouterArgs& a, const float* psum, float z, int n, float (*sp)[L * V],
+                         const int* sc, float (*red)[4], int* redn) {
+  const int tid = threadIdx.x, li = tid % L, c0 = li * V;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float s = psum[i];
+#pragma unroll
+    for (int o = L; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+    if ((tid & 63) < L) sp[tid >> 6][c0 + i] = s;
+  }
+  z = li == 0 ? z : 0.f;
+  n = li == 0 ? n : 0;
+  z = group_all<64>(z, OpAdd());
+  n = group_all<64>(n, OpAdd());
+  if ((tid & 63) == 0) {
+    red[0][tid >> 6] = z;
+    redn[tid >> 6] = n;
+  }
+  __syncthreads();
+  const bool alone = gridDim.x == 1;
+  float dot = 0.f;
+  for (int e = tid; e < a.E; e += kRouterThreads) {
+    const float s = sp[0][e] + sp[1][e] + sp[2][e] + sp[3][e];
+    const int c = sc[e];
+    if (alone) {
+      a.psum[e] = s;
+      a.counts[e] = c;
+      dot += (float)c * s;
+    } else {
+      a.part_p[(size_t)blockIdx.x * a.E + e] = s;
+      a.part_c[(size_t)blockIdx.x * a.E + e] = c;
+    }
+  }
+  if (alone) dot = block_sum(dot, red[1], 4);
+  if (tid == 0) {
+    const float zs = red[0][0] + red[0][1] + red[0][2] + red[0][3];
+    const int ns = redn[0] + redn[1] + redn[2] + redn[3];
+    if (alone) {
+      a.live[0] = ns;
+      a.losses[0] = balance_of(dot, a.E, a.k, ns);
+      a.losses[1] = ns > 0 ? zs / (float)ns : 0.f;
+    } else {
+      a.part_z[blockIdx.x] = zs;
+      a.part_n[blockIdx.x] = ns;
+    }
+  }
 }
 
 // Forward.  Each group takes rows in turn; its lanes keep the sums of P of
@@ -322,50 +384,210 @@ __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
       if (where[q] >= 0) atomicAdd(&sc[where[q]], 1);
     }
   }
-  // the wave's groups, then the four waves, each in a fixed order
+  router_sums<L, V>(a, psum, z, n, sp, sc, red, redn);
+}
+
+// ---- a choice by values --------------------------------------------------------
+// Values v = score + bias, groups of experts ranked by their best or their two best, and the k largest
+// values of the open groups.  Values are compared as 64-bit numbers: next to each other in 32 bits, they
+// would be chosen by their rounding.
+struct Chosen { double v; int e; };
+template <int L> MOE_DEV Chosen group_best(Chosen c) {
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) {
+    const double v = __shfl_xor(c.v, o, 64);
+    const int e = __shfl_xor(c.e, o, 64);
+    if (v > c.v || (v == c.v && e < c.e)) c = {v, e};
+  }
+  return c;
+}
+// The lane's choices, where[q] of place q * L + li (-1: none left), from its logits l (barred ones
+// -infinity).  row: the row's places in LDS, of which lane li's are those from c0 on.
+template <int L, int V, int SCORE>
+MOE_DEV void choose64(const RouterArgs& a, const float* l, float top, const float* bias, double* row, int li, int* where) {
+  constexpr int KQ = (kRouterMaxK + L - 1) / L, GQ = (kRouterMaxGroups + L - 1) / L;
+  const int c0 = li * V;
+  double v[V];
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v[i] = exp((double)l[i] - (double)top);
+      sum += v[i];
+    }
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) sum += __shfl_xor(sum, o, 64);
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] /= sum;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    float s = psum[i];
+    v[i] += (double)bias[i];
+    if (!(l[i] > -INFINITY && bias[i] > -INFINITY)) v[i] = -HUGE_VAL;
+  }
+  if (a.top_groups < a.groups) {
 #pragma unroll
-    for (int o = L; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
-    if ((tid & 63) < L) sp[tid >> 6][c0 + i] = s;
+    for (int i = 0; i < V; ++i) row[c0 + i] = v[i];
+    wave_lds_order();
+    double worth[GQ];
+#pragma unroll
+    for (int q = 0; q < GQ; ++q) {
+      const int first = (q * L + li) * a.gsize;
+      double best = -HUGE_VAL, second = -HUGE_VAL;
+      if (q * L + li < a.groups)
+        for (int i = 0; i < a.gsize; ++i) {
+          const double x = row[first + i];
+          second = fmax(second, fmin(best, x));
+          best = fmax(best, x);
+        }
+      worth[q] = best + (a.two && second > -HUGE_VAL ? second : 0.0);
+    }
+    wave_lds_order();                                    // all have read their members
+#pragma unroll
+    for (int q = 0; q < GQ; ++q)
+      if (q * L + li < a.groups) row[q * L + li] = worth[q];
+    wave_lds_order();
+    uint32_t open[2] = {0u, 0u};
+#pragma unroll
+    for (int q = 0; q < GQ; ++q) {
+      const int m = q * L + li;
+      int above = 0;
+      for (int j = 0; j < a.groups; ++j) above += row[j] > worth[q] || (row[j] == worth[q] && j < m);
+      if (m < a.groups && above < a.top_groups) open[m >> 5] |= 1u << (m & 31);
+    }
+    wave_lds_order();                                    // the places are used again
+    open[0] = group_all<L>(open[0], OpOr());
+    open[1] = group_all<L>(open[1], OpOr());
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int m = min((c0 + i) / a.gsize, kRouterMaxGroups - 1);
+      if (!((m & 32 ? open[1] : open[0]) >> (m & 31) & 1u)) v[i] = -HUGE_VAL;
+    }
   }
-  z = li == 0 ? z : 0.f;
-  n = li == 0 ? n : 0;
-  z = group_all<64>(z, OpAdd());
-  n = group_all<64>(n, OpAdd());
-  if ((tid & 63) == 0) {
-    red[0][tid >> 6] = z;
-    redn[tid >> 6] = n;
+#pragma unroll
+  for (int q = 0; q < KQ; ++q) where[q] = -1;
+  for (int j = 0; j < a.k; ++j) {
+    Chosen c{v[0], c0};
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+      if (v[i] > c.v) c = {v[i], c0 + i};
+    c = group_best<L>(c);
+    if (!(c.v > -HUGE_VAL)) break;                       // the whole group
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = c0 + i == c.e ? -HUGE_VAL : v[i];
+#pragma unroll
+    for (int q = 0; q < KQ; ++q)
+      if (j == q * L + li) where[q] = c.e;
   }
+}
+
+// Forward with a choice by values; rows, sums and outputs as in k_router.
+template <typename T, int L, int V, int SCORE>
+__global__ __launch_bounds__(kRouterThreads) void k_choice(RouterArgs a) {
+  constexpr int G = kRouterThreads / L, C = L * V, KQ = (kRouterMaxK + L - 1) / L;
+  __shared__ float sp[4][C];
+  __shared__ int sc[C];
+  __shared__ float red[2][4];
+  __shared__ int redn[4];
+  __shared__ double rows[G][C];
+  const int tid = threadIdx.x, li = tid % L, g = tid / L, c0 = li * V;
+  for (int i = tid; i < C; i += kRouterThreads) sc[i] = 0;
+  if (blockIdx.x == 0 && tid == 0 && gridDim.x > 1) *a.done = 0;
   __syncthreads();
-  const bool alone = gridDim.x == 1;
-  float dot = 0.f;
-  for (int e = tid; e < a.E; e += kRouterThreads) {
-    const float s = sp[0][e] + sp[1][e] + sp[2][e] + sp[3][e];
-    const int c = sc[e];
-    if (alone) {
-      a.psum[e] = s;
-      a.counts[e] = c;
-      dot += (float)c * s;
-    } else {
-      a.part_p[(size_t)blockIdx.x * a.E + e] = s;
-      a.part_c[(size_t)blockIdx.x * a.E + e] = c;
+  float psum[V], bias[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    psum[i] = 0.f;
+    bias[i] = a.bias && c0 + i < a.E ? a.bias[c0 + i] : 0.f;
+  }
+  float z = 0.f;
+  int n = 0;
+  const size_t step = (size_t)gridDim.x * G;
+  NextRow<T, V> next;
+  next.fetch(a, (size_t)blockIdx.x * G + g, c0);
+  for (size_t t = (size_t)blockIdx.x * G + g; t < (size_t)a.T; t += step) {
+    float v[V], w[V], e[V];
+    logits_of<T, V>(next, c0, a.E, v);
+    next.fetch(a, t + step, c0);
+    int32_t* ids = a.ids + t * a.k;
+    float* gates = a.gates + t * a.k;
+    Score<SCORE> sc_;
+    sc_.at_top(row_top<L, V>(v));
+    const float sum = row_scores<L, V, SCORE, false>(sc_, v, w, e, nullptr);
+    const float lsum = SCORE == MOE_SCORE_SOFTMAX ? sum : lane_sum<L, V>(e);
+    if (!row_live(sc_.top, sum)) {                       // the whole group
+      for (int j = li; j < a.k; j += L) {
+        ids[j] = -1;
+        gates[j] = 0.f;
+      }
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < V; ++i) bad |= !(v[i] < INFINITY);       // NaN or +infinity
+      if (bad) atomicOr(a.status, MOE_DEV_BAD_LOGIT);
+      continue;
+    }
+    const float inv = inverse(sum);
+#pragma unroll
+    for (int i = 0; i < V; ++i) psum[i] += w[i] * inv;
+    const float lse = sc_.top + logf(lsum);
+    z += lse * lse;
+    ++n;
+    int where[KQ];
+    choose64<L, V, SCORE>(a, v, sc_.top, bias, rows[g], li, where);
+    // lane j's choice: its weight again, from the logit of the lane that has it
+    float* logits = (float*)rows[g];
+    wave_lds_order();
+#pragma unroll
+    for (int i = 0; i < V; ++i) logits[c0 + i] = v[i];
+    wave_lds_order();
+    float l[KQ], mine[KQ], most = -INFINITY, chosen = 0.f;
+#pragma unroll
+    for (int q = 0; q < KQ; ++q) {
+      l[q] = where[q] >= 0 ? logits[where[q]] : -INFINITY;
+      most = fmaxf(most, l[q]);
+    }
+    wave_lds_order();                                    // read before the next row's
+    // shares of the chosen, whose best may be next to nothing beside the row's
+    Score<SCORE> part = sc_;
+    if (a.renorm) part.at_top(group_all<L>(most, OpMaxF()));
+#pragma unroll
+    for (int q = 0; q < KQ; ++q) {
+      mine[q] = where[q] >= 0 ? part.weight(l[q]) : 0.f;
+      chosen += mine[q];
+    }
+    chosen = group_all<L>(chosen, OpAdd());
+    const float mul = a.renorm ? (chosen > 0.f ? a.scale / chosen : 0.f)
+                      : SCORE == MOE_SCORE_SOFTMAX ? a.scale / sum : a.scale * sc_.elow;
+#pragma unroll
+    for (int q = 0; q < KQ; ++q) {
+      const int j = q * L + li;
+      if (j >= a.k) continue;
+      ids[j] = where[q];
+      gates[j] = mine[q] * mul;
+      if (where[q] >= 0) atomicAdd(&sc[where[q]], 1);
     }
   }
-  if (alone) dot = block_sum(dot, red[1], 4);
-  if (tid == 0) {
-    const float zs = red[0][0] + red[0][1] + red[0][2] + red[0][3];
-    const int ns = redn[0] + redn[1] + redn[2] + redn[3];
-    if (alone) {
-      a.live[0] = ns;
-      a.losses[0] = balance_of(dot, a.E, a.k, ns);
-      a.losses[1] = ns > 0 ? zs / (float)ns : 0.f;
-    } else {
-      a.part_z[blockIdx.x] = zs;
-      a.part_n[blockIdx.x] = ns;
-    }
-  }
+  router_sums<L, V>(a, psum, z, n, sp, sc, red, redn);
+}
+
+// b += rate * sign(mean count - count), compared as whole numbers.
+__global__ __launch_bounds__(1024) void k_bias_update(const int32_t* __restrict__ counts, int E, float rate,
+                                                      float* __restrict__ bias) {
+  __shared__ long long red[16];
+  const int e = threadIdx.x;
+  const long long c = e < E ? counts[e] : 0;
+  const long long w = wave_sum64(c);
+  if ((e & 63) == 0) red[e >> 6] = w;
+  __syncthreads();
+  long long sum = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sum += red[i];
+  if (e >= E) return;
+  const long long more = sum - c * E;
+  if (more != 0) bias[e] += more > 0 ? rate : -rate;
 }
 
 // Totals of the workgroups' partial sums.  A workgroup takes 16 experts, 64
@@ -553,8 +775,19 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
       }
       Q = group_all<L>(Q, OpAdd());
       pg = group_all<L>(pg, OpAdd());
-      const float hq = a.renorm ? (Q > 0.f ? H / Q : 0.f)
-                                : (SCORE == MOE_SCORE_SOFTMAX ? H : 0.f);
+      float hq = a.renorm ? (Q > 0.f ? H / Q : 0.f) : (SCORE == MOE_SCORE_SOFTMAX ? H : 0.f);
+      if (a.renorm && Q < kFewShares && H != 0.f) {      // the whole group: shares of next to nothing
+        float most = -INFINITY, all = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) most = fmaxf(most, flag[i] ? log_score<SCORE>(v[i]) : -INFINITY);
+        most = group_all<L>(most, OpMaxF());
+#pragma unroll
+        for (int i = 0; i < V; ++i) all += flag[i] ? exp_of(log_score<SCORE>(v[i]) - most) : 0.f;
+        all = group_all<L>(all, OpAdd());
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] -= flag[i] && all > 0.f ? H / all * exp_of(log_score<SCORE>(v[i]) - most) : 0.f;
+        hq = 0.f;
+      }
       const float rest = a.renorm ? 0.f : hq;            // of the experts not chosen
       float zs = 0.f;
       if (zmul != 0.f) {
@@ -673,15 +906,28 @@ template <typename T, int L, int V, int SCORE> struct BwdK {
   }
 };
 
-int launch_router(const moe_router& R, const void* logits, int ld, const uint8_t* mask, int T,
+template <typename T, int L, int V, int SCORE> struct ChoiceK {
+  static constexpr bool kForward = false;
+  static void go(const RouterArgs& a, int grid, hipStream_t st) {
+    hipLaunchKernelGGL((k_choice<T, L, V, SCORE>), dim3(grid), dim3(kRouterThreads), 0, st, a);
+  }
+};
+
+int launch_router(const moe_router& R, const moe_choice* C, const void* logits, int ld, const uint8_t* mask, int T,
                   int32_t* ids, float* gates, int32_t* counts, float* psum, int32_t* live,
                   float* losses, int32_t* status, void* ws, hipStream_t st) {
+  // one group of all or every group open, and no bias: the k largest logits
+  const bool values = C && (C->bias || C->top_groups < C->groups);
   RouterArgs a{};
+  if (values) {
+    a.bias = C->bias; a.groups = C->groups; a.top_groups = C->top_groups;
+    a.two = C->group_score == MOE_GROUP_TOP2; a.gsize = R.E / C->groups;
+  }
   a.logits = logits; a.ld = (size_t)ld; a.mask = mask; a.T = T; a.E = R.E; a.k = R.k;
   a.renorm = R.renorm; a.scale = R.scale;
   a.ids = ids; a.gates = gates; a.counts = counts; a.psum = psum; a.live = live;
   a.losses = losses; a.status = status;
-  const int grid = router_grid(T, router_lanes_fwd(T, R.E));
+  const int grid = router_grid(T, values ? router_lanes(R.E) : router_lanes_fwd(T, R.E));
   char* w = (char*)ws;
   a.part_p = (float*)w;
   a.part_c = (int32_t*)(w += align_up((size_t)grid * R.E * 4));
@@ -690,9 +936,15 @@ int launch_router(const moe_router& R, const void* logits, int ld, const uint8_t
   a.dots = (float*)(w += align_up((size_t)grid * 4));
   a.done = (int32_t*)(w += align_up(64 * 4));
   a.parts = grid;
-  router_kind<FwdK>(R, a, grid, st);
+  if (values) router_kind<ChoiceK>(R, a, grid, st);
+  else router_kind<FwdK>(R, a, grid, st);
   if (grid > 1)
     hipLaunchKernelGGL(k_router_totals, dim3((R.E + kTotalCols - 1) / kTotalCols), dim3(kTotalThreads), 0, st, a);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+int launch_bias_update(const int32_t* counts, int E, float rate, float* bias, hipStream_t st) {
+  hipLaunchKernelGGL(k_bias_update, dim3(1), dim3(kMaxExperts), 0, st, counts, E, rate, bias);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

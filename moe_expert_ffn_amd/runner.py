@@ -139,10 +139,12 @@ class BlockRunner(LayerRunner):
 
     w_router [E][d] and the norms' weights w_in, w_out [d] are of the activation dtype, gate [d] is
     fp32 (None: 1).  The two products with w_router are plain library products; every other step
-    is a library call of its own over buffers made here, on the current stream."""
+    is a library call of its own over buffers made here, on the current stream.  With a bias [E] (fp32)
+    or groups the router chooses by values (binding.make_choice); update_bias balances the experts."""
 
     def __init__(self, w1, w2, w_router, w_in, w_out, gate=None, w1_scale=None, w2_scale=None, *,
-                 score="softmax", renorm=True, scale=1.0, alpha=1.0, eps=1e-6, **layer):
+                 score="softmax", renorm=True, scale=1.0, bias=None, groups=1, top_groups=None, group_score="top2",
+                 alpha=1.0, eps=1e-6, **layer):
         super().__init__(w1, w2, w1_scale, w2_scale, **layer)
         T, d, dev, dt = self.T, self.d, self.dev, self.act_dtype
         if tuple(w_router.shape) != (self.E, d) or w_router.dtype != dt:
@@ -153,6 +155,9 @@ class BlockRunner(LayerRunner):
         self.w_router, self.w_in, self.w_out, self.gate = w_router, w_in, w_out, gate
         self.alpha, self.eps = alpha, eps
         self.router = B.make_router(self.E, self.k, dt, score, renorm, scale)
+        self.choice = None
+        if bias is not None or groups != 1 or top_groups is not None:
+            self.choice = B.make_choice(self.router, bias, groups, top_groups, group_score)
         self.routed = B.alloc_router(self.router, T, dev)
         self.router_ws = B.router_workspace(self.router, T, dev)
         rows = dict(dtype=dt, device=dev)
@@ -182,7 +187,7 @@ class BlockRunner(LayerRunner):
         self.x, self.mask = None if _share(x, [self.out]) else x, mask
         B.norm_in(x, self.w_in, self.eps, self.n, self.rstd_in, mask=mask)
         torch.mm(self.n, self.w_router.t(), out=self.logits)
-        r = B.router_forward(self.router, self.logits, self.routed, self.router_ws, self.status, mask)
+        r = B.router_forward(self.router, self.logits, self.routed, self.router_ws, self.status, mask, self.choice)
         self.route(r["topk_ids"])
         if self.with_backward:
             self.plan_bwd_async()
@@ -247,3 +252,9 @@ class BlockRunner(LayerRunner):
                         1.0 if grad_scale is None else grad_scale)
             grad_scale = self.grad_scale
         B.adamw(self.optimizer, lr, step=step, grad_scale=grad_scale, **hyper)
+
+    def update_bias(self, rate):
+        """The balancing step of the router's bias by the last routing's counts, in place."""
+        if self.choice is None or self.choice.tensor is None:
+            raise B.MoeError("the runner's router has no bias")
+        B.router_bias_update(self.choice.tensor, self.routed["counts"], rate)
