@@ -48,6 +48,7 @@ struct RouterArgs {
   float scale;
   const float* bias;   // a choice by values: added to the scores (nullable)
   int groups, top_groups, two, gsize;    // the groups, how many are open, value of the two best members, E / groups
+  int glog;            // a group is 2^glog whole lanes; -1: it is not
 };
 
 // Order of 32-bit floats as unsigned integers, 0 for what is never chosen
@@ -71,7 +72,7 @@ MOE_DEV int pick_expert(uint32_t w) { return 0xFFFF - (int)(w & 0xFFFFu); }
 MOE_DEV uint32_t pick_key(uint32_t w) { return w & 0x80000000u ? w & 0xFFFF0000u : w | 0xFFFFu; }
 
 // N words in descending order: Batcher's odd-even merge sort.
-template <int N> MOE_DEV void sort_down(uint32_t* k) {
+template <int N, typename K> MOE_DEV void sort_down(K* k) {
 #pragma unroll
   for (int p = 1; p < N; p <<= 1)
 #pragma unroll
@@ -81,7 +82,7 @@ template <int N> MOE_DEV void sort_down(uint32_t* k) {
 #pragma unroll
         for (int i = 0; i < d; ++i)
           if (i + j + d < N && (i + j) / (2 * p) == (i + j + d) / (2 * p)) {
-            const uint32_t a = k[i + j], b = k[i + j + d];
+            const K a = k[i + j], b = k[i + j + d];
             k[i + j] = max(a, b);
             k[i + j + d] = min(a, b);
           }
@@ -391,109 +392,428 @@ __global__ __launch_bounds__(kRouterThreads) void k_router(RouterArgs a) {
 // Values v = score + bias, groups of experts ranked by their best or their two best, and the k largest
 // values of the open groups.  Values are compared as 64-bit numbers: next to each other in 32 bits, they
 // would be chosen by their rounding.
+// A wave-uniform number that the compiler forgets: its comparisons are made where they are used.  (Kept over
+// the loop of rows as masks, they took 160 scalar registers to VGPRs and back: 65521 x 256 87 us.)
+MOE_DEV int fresh(int v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
+// The same of a lane's number, and so of the addresses and comparisons made of it.
+MOE_DEV int fresh_lane(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 struct Chosen { double v; int e; };
+MOE_DEV Chosen better(Chosen a, Chosen b) { return b.v > a.v || (b.v == a.v && b.e < a.e) ? b : a; }
+template <int CTRL> MOE_DEV Chosen dpp_chosen(Chosen c) {
+  const uint64_t w = __builtin_bit_cast(uint64_t, c.v);
+  const uint32_t lo = dpp_of<CTRL>((uint32_t)w), hi = dpp_of<CTRL>((uint32_t)(w >> 32));
+  return {__builtin_bit_cast(double, (uint64_t)hi << 32 | lo), dpp_of<CTRL>(c.e)};
+}
 template <int L> MOE_DEV Chosen group_best(Chosen c) {
+  c = better(c, dpp_chosen<0xB1>(c));
+  c = better(c, dpp_chosen<0x4E>(c));
+  c = better(c, dpp_chosen<0x141>(c));
+  if constexpr (L >= 16) c = better(c, dpp_chosen<0x140>(c));
 #pragma unroll
-  for (int o = 1; o < L; o <<= 1) {
-    const double v = __shfl_xor(c.v, o, 64);
-    const int e = __shfl_xor(c.e, o, 64);
-    if (v > c.v || (v == c.v && e < c.e)) c = {v, e};
-  }
+  for (int o = 16; o < L; o <<= 1) c = better(c, {__shfl_xor(c.v, o, 64), __shfl_xor(c.e, o, 64)});
   return c;
 }
-// The lane's choices, where[q] of place q * L + li (-1: none left), from its logits l (barred ones
-// -infinity).  row: the row's places in LDS, of which lane li's are those from c0 on.
-template <int L, int V, int SCORE>
-MOE_DEV void choose64(const RouterArgs& a, const float* l, float top, const float* bias, double* row, int li, int* where) {
-  constexpr int KQ = (kRouterMaxK + L - 1) / L, GQ = (kRouterMaxGroups + L - 1) / L;
-  const int c0 = li * V;
-  double v[V];
-  if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
-    double sum = 0.0;
+// e^x in 64 bits: x = n log 2 + r, and the series of e^r to r^13 / 13! (|r| <= 0.35: the next term is below
+// 2^-57).  Its coefficients are read here, by an address that the compiler forgets: kept in registers over the
+// loop of rows, they took a third of them.
+__constant__ const double kInverseFactorials[14] = {
+    1.0, 1.0, 1.0 / 2, 1.0 / 6, 1.0 / 24, 1.0 / 120, 1.0 / 720, 1.0 / 5040, 1.0 / 40320, 1.0 / 362880, 1.0 / 3628800,
+    1.0 / 39916800, 1.0 / 479001600, 1.0 / 6227020800.0};
+MOE_DEV double exp64(double x) {
+  const MOE_CONST double* c = (const MOE_CONST double*)kInverseFactorials;
+  asm volatile("" : "+s"(c));
+  x = fmin(fmax(x, -800.0), 800.0);
+  const double n = rint(x * 1.4426950408889634);
+  // log 2 in two parts, the first of 32 bits, so that its product with n is exact
+  const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.69314718036912382, x));
+  double p = c[13];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      v[i] = exp((double)l[i] - (double)top);
-      sum += v[i];
-    }
+  for (int i = 12; i >= 0; --i) p = fma(p, r, c[i]);
+  return ldexp(p, (int)n);
+}
+template <int SCORE> MOE_DEV double score64(float l, float top) {
+  return SCORE == MOE_SCORE_SOFTMAX ? exp64((double)l - (double)top) : 1.0 / (1.0 + exp64(-(double)l));
+}
+
+// The lane's choices, where[q] of place q * L + li (-1: none left), from its logits l.  bias: -infinity where
+// barred.  row: the row's C places in LDS, which hold the values: rows come here rarely, and registers for
+// them would be the loop of rows'.
+template <int L, int V, int SCORE>
+MOE_DEV void choose64(const RouterArgs& a, const float* l, float top, const float* bias, MOE_LDS double* row, int li,
+                      int* where) {
+  constexpr int KQ = (kRouterMaxK + L - 1) / L, GQ = (kRouterMaxGroups + L - 1) / L;
+  const int c0 = li * V, groups = fresh(a.groups), top_groups = fresh(a.top_groups), k = fresh(a.k);
+  MOE_LDS double* mine = row + c0;
+  wave_lds_order();
+  uint32_t barred = 0u;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    mine[i] = (double)l[i];
+    barred |= l[i] > -INFINITY && bias[i] > -INFINITY ? 0u : 1u << i;
+  }
+  double sum = SCORE == MOE_SCORE_SOFTMAX ? 0.0 : 1.0;
+#pragma unroll 4
+  for (int i = 0; i < V; ++i) {
+    const double w = score64<SCORE>((float)mine[i], top);
+    mine[i] = w;
+    if constexpr (SCORE == MOE_SCORE_SOFTMAX) sum += w;
+  }
+  if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) sum += __shfl_xor(sum, o, 64);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] /= sum;
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = 1.0 / (1.0 + exp(-(double)l[i]));
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    v[i] += (double)bias[i];
-    if (!(l[i] > -INFINITY && bias[i] > -INFINITY)) v[i] = -HUGE_VAL;
+    const double v = mine[i] / sum + (double)bias[i];
+    mine[i] = barred >> i & 1u ? -HUGE_VAL : v;
   }
-  if (a.top_groups < a.groups) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) row[c0 + i] = v[i];
-    wave_lds_order();
+  wave_lds_order();
+  if (top_groups < groups) {
+    const int gsize = fresh(a.gsize), two = fresh(a.two);
     double worth[GQ];
 #pragma unroll
     for (int q = 0; q < GQ; ++q) {
-      const int first = (q * L + li) * a.gsize;
+      const int m = q * L + li;
       double best = -HUGE_VAL, second = -HUGE_VAL;
-      if (q * L + li < a.groups)
-        for (int i = 0; i < a.gsize; ++i) {
-          const double x = row[first + i];
+      if (m < groups)
+#pragma unroll 8
+        for (int i = 0; i < gsize; ++i) {
+          const double x = row[m * gsize + i];
           second = fmax(second, fmin(best, x));
           best = fmax(best, x);
         }
-      worth[q] = best + (a.two && second > -HUGE_VAL ? second : 0.0);
+      worth[q] = best + (two && second > -HUGE_VAL ? second : 0.0);
     }
-    wave_lds_order();                                    // all have read their members
-#pragma unroll
-    for (int q = 0; q < GQ; ++q)
-      if (q * L + li < a.groups) row[q * L + li] = worth[q];
-    wave_lds_order();
     uint32_t open[2] = {0u, 0u};
 #pragma unroll
     for (int q = 0; q < GQ; ++q) {
       const int m = q * L + li;
       int above = 0;
-      for (int j = 0; j < a.groups; ++j) above += row[j] > worth[q] || (row[j] == worth[q] && j < m);
-      if (m < a.groups && above < a.top_groups) open[m >> 5] |= 1u << (m & 31);
+#pragma unroll
+      for (int p = 0; p < GQ; ++p)
+#pragma unroll 4
+        for (int j = 0; j < min(L, groups - p * L); ++j) {               // the lanes' groups in turn
+          const double o = __shfl(worth[p], j, L);
+          above += o > worth[q] || (o == worth[q] && p * L + j < m);
+        }
+      const bool in = m < groups && above < top_groups;
+      open[0] |= in && m < 32 ? 1u << m : 0u;
+      open[1] |= in && m >= 32 ? 1u << (m & 31) : 0u;
     }
-    wave_lds_order();                                    // the places are used again
     open[0] = group_all<L>(open[0], OpOr());
     open[1] = group_all<L>(open[1], OpOr());
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < V; ++i) {
-      const int m = min((c0 + i) / a.gsize, kRouterMaxGroups - 1);
-      if (!((m & 32 ? open[1] : open[0]) >> (m & 31) & 1u)) v[i] = -HUGE_VAL;
+      const int m = min((c0 + i) / gsize, kRouterMaxGroups - 1);
+      if (!((m & 32 ? open[1] : open[0]) >> (m & 31) & 1u)) mine[i] = -HUGE_VAL;
     }
   }
 #pragma unroll
   for (int q = 0; q < KQ; ++q) where[q] = -1;
-  for (int j = 0; j < a.k; ++j) {
-    Chosen c{v[0], c0};
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    Chosen c{mine[0], c0};
 #pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (v[i] > c.v) c = {v[i], c0 + i};
+    for (int i = 1; i < V; ++i) {
+      const double v = mine[i];
+      if (v > c.v) c = {v, c0 + i};
+    }
     c = group_best<L>(c);
     if (!(c.v > -HUGE_VAL)) break;                       // the whole group
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = c0 + i == c.e ? -HUGE_VAL : v[i];
+    if (c.e >= c0 && c.e < c0 + V) row[c.e] = -HUGE_VAL;
 #pragma unroll
     for (int q = 0; q < KQ; ++q)
       if (j == q * L + li) where[q] = c.e;
   }
 }
 
-// Forward with a choice by values; rows, sums and outputs as in k_router.
+// The same in 32 bits, with a bound of its own error.  An expert's key is its value as a whole number of
+// units above its index, so that all keys of a row are different, and below C where it is not chosen; a
+// difference of keys of more than `close` is the values' own.
+struct TwoBest {
+  uint32_t a, b;
+  MOE_DEV void join(uint32_t oa, uint32_t ob) {
+    b = max(max(b, ob), min(a, oa));
+    a = max(a, oa);
+  }
+};
+// over groups of 2^log aligned lanes (log the same in every lane)
+MOE_DEV TwoBest lanes_two_best(TwoBest t, int log) {
+  if (log >= 1) t.join(dpp_of<0xB1>(t.a), dpp_of<0xB1>(t.b));
+  if (log >= 2) t.join(dpp_of<0x4E>(t.a), dpp_of<0x4E>(t.b));
+  if (log >= 3) t.join(dpp_of<0x141>(t.a), dpp_of<0x141>(t.b));
+  if (log >= 4) t.join(dpp_of<0x140>(t.a), dpp_of<0x140>(t.b));
+  if (log >= 5) {
+    const auto a = __builtin_amdgcn_permlane16_swap(t.a, t.a, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(t.b, t.b, false, false);
+    t = {a[0], b[0]};
+    t.join(a[1], b[1]);
+  }
+  return t;
+}
+// Eight words that fall and then rise (or the other way), in descending order.
+MOE_DEV void sort_bitonic8(uint32_t* k) {
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & d)) {
+        const uint32_t a = k[i], b = k[i + d];
+        k[i] = max(a, b);
+        k[i + d] = min(a, b);
+      }
+}
+// The eight largest of two descending lists: of each list's i-th and the other's i-th from the end one is.
+template <class F> MOE_DEV void merge8(uint32_t* k, F other) {
+  uint32_t m[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m[i] = max(k[i], other(7 - i));
+  sort_bitonic8(m);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) k[i] = m[i];
+}
+template <int L> MOE_DEV void lanes_merge8(uint32_t* k) {
+  merge8(k, [&](int i) { return dpp_of<0xB1>(k[i]); });
+  merge8(k, [&](int i) { return dpp_of<0x4E>(k[i]); });
+  merge8(k, [&](int i) { return dpp_of<0x141>(k[i]); });
+  if constexpr (L >= 16) merge8(k, [&](int i) { return dpp_of<0x140>(k[i]); });
+  auto across = [&](auto swap) {
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const auto s = swap(k[i]);
+      k[i] = s[0];
+      o[i] = s[1];
+    }
+    merge8(k, [&](int i) { return o[i]; });
+  };
+  if constexpr (L >= 32) across([](uint32_t v) { return __builtin_amdgcn_permlane16_swap(v, v, false, false); });
+  if constexpr (L >= 64) across([](uint32_t v) { return __builtin_amdgcn_permlane32_swap(v, v, false, false); });
+}
+// Whether `on` holds in any lane of the group.
+template <int L> MOE_DEV bool group_any(bool on) {
+  const uint64_t m = __ballot(on);
+  if constexpr (L == 64) return m != 0;
+  const int lane = threadIdx.x & 63;
+  const uint32_t h = lane & 32 ? (uint32_t)(m >> 32) : (uint32_t)m;
+  return (h >> (lane & 31 & ~(L - 1)) & (uint32_t)((1ull << L) - 1)) != 0;
+}
+constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
+
+// The lane's choices from its scores, each off by `err` at most, the largest smost.  bias: -infinity where
+// barred; bmost the largest |bias| of the others.  In LDS: the row's logits and the biases, C places for keys,
+// and a place for every group; gid: the groups of the lane's experts.  Returns whether the choice stays open.
+template <int L, int V>
+MOE_DEV bool choose32(const RouterArgs& a, const float* l, const float* score, float err, float smost, const float* bias,
+                      float bmost, const MOE_LDS float* logits, const MOE_LDS float* sbias, MOE_LDS uint32_t* keys,
+                      MOE_LDS uint32_t* worth, const uint32_t* gid, int li, int* where) {
+  constexpr int KQ = (kRouterMaxK + L - 1) / L, C = L * V, IB = log2_of(C), UB = 32 - IB < 24 ? 32 - IB : 24;
+  const int c0 = li * V, groups = fresh(a.groups), top_groups = fresh(a.top_groups), k = fresh(a.k);
+  // values from -bmost to smost + bmost are units from 1 to 2^UB - 3
+  const float range = fmaxf(smost + 2.f * bmost, 0x1p-100f), per = (float)((1 << UB) - 8) / range, zero = bmost * per + 2.f;
+  // two values' errors in units: their scores', and their sums' roundings, the units' and the cuts to whole ones
+  const float far = 2.f * err * per + 5.f;
+  uint32_t key[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float v = l[i] > -INFINITY ? score[i] + bias[i] : -INFINITY;
+    key[i] = ((uint32_t)fmaxf(__builtin_fmaf(v, per, zero), 0.f) << IB | (uint32_t)(C - V - c0)) | (uint32_t)(V - 1 - i);
+  }
+  bool unsure = !(bmost < 0x1p64f);                      // out of the bounds' range
+  if (top_groups < groups) {
+    const int glog = fresh(a.glog), two = fresh(a.two);
+    // in units; a second that is not there has the value 0
+    auto worth_of = [&](TwoBest t) {
+      return t.a >= C ? (t.a >> IB) + (two ? (t.b >= C ? t.b >> IB : (uint32_t)zero) : 0u) : 0u;
+    };
+    wave_lds_order();
+    if (glog >= 0) {                                     // a group is 2^glog whole lanes
+      TwoBest t{key[0], 0u};
+#pragma unroll
+      for (int i = 1; i < V; ++i) t.join(key[i], 0u);
+      t = lanes_two_best(t, glog);
+      if (li >> glog < groups) worth[li >> glog] = worth_of(t);          // the group's lanes write the same
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) keys[c0 + i] = key[i];
+      wave_lds_order();
+      const int gsize = fresh(a.gsize);
+#pragma unroll 1
+      for (int m = li; m < groups; m += L) {
+        TwoBest t{0u, 0u};
+#pragma unroll 1
+        for (int i = 0; i < gsize; ++i) t.join(keys[m * gsize + i], 0u);
+        worth[m] = worth_of(t);
+      }
+    }
+    if (li < 3) worth[groups + li] = 0u;                 // whole fours are read
+    wave_lds_order();
+    uint32_t open[2] = {0u, 0u}, least = ~0u, most = 0u; // worths of the open groups, of the closed ones
+#pragma unroll 1
+    for (int m = li; m < groups; m += L) {
+      const uint32_t w = worth[m];
+      int above = 0;
+#pragma unroll 1
+      for (int j = 0; j < groups; j += 4) {
+        const u32x4_t o = *(const MOE_LDS u32x4_t*)(worth + j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) above += o[i] > w;
+      }
+      const bool in = above < top_groups;
+      open[0] |= in && m < 32 ? 1u << m : 0u;
+      open[1] |= in && m >= 32 ? 1u << (m & 31) : 0u;
+      least = in ? min(least, w) : least;
+      most = in ? most : max(most, w);
+    }
+    open[0] = group_all<L>(open[0], OpOr());
+    if (groups > 32) open[1] = group_all<L>(open[1], OpOr());
+    least = group_all<L>(least, OpMin());
+    most = group_all<L>(most, OpMax());
+    // a group's value has two values' errors; equals are all open
+    unsure |= __popc(open[0]) + __popc(open[1]) != top_groups;
+    unsure |= most > 0u && (float)(least - most) <= 2.f * far + 1.f;
+    if (glog >= 0) {
+      const int m = li >> glog;
+      const bool in = (m & 32 ? open[1] : open[0]) >> (m & 31) & 1u;
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = in ? key[i] : 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t m = gid[i / 4] >> 8 * (i % 4);
+        key[i] = (m & 32 ? open[1] : open[0]) >> (m & 31) & 1u ? key[i] : 0u;
+      }
+    }
+  }
+  const uint32_t close = far < 0x1p20f ? ((uint32_t)far + 1u) << IB : ~0u - C;
+#pragma unroll
+  for (int q = 0; q < KQ; ++q) where[q] = -1;
+  bool near = false;
+  auto expert = [&](uint32_t key) { return C - 1 - (int)(key & (C - 1)); };
+  if (k <= 8) {
+    // Lists of the lanes' eight largest, merged over the lanes: 32 instructions a step.  (A maximum over the
+    // lanes for each place: 40.)
+    uint32_t list[8], ninth = 0u;
+    if constexpr (V == 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) list[i] = key[i];
+      sort_down<8>(list);
+    } else {
+      uint32_t more[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        list[i] = key[i];
+        more[i] = key[V - 8 + i];
+      }
+      sort_down<8>(list);
+      sort_down<8>(more);
+      merge8(list, [&](int i) { return more[i]; });
+    }
+    lanes_merge8<L>(list);
+    if (k == 8) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) ninth = max(ninth, key[i] < list[7] ? key[i] : 0u);
+      ninth = group_all<L>(ninth, OpMax());
+    }
+    auto either = [](bool second, uint32_t a, uint32_t b) { return second ? b : a; };      // values: elements would index
+    const bool b0 = li & 1, b1 = li & 2, b2 = li & 4;
+    const uint32_t p0 = either(b2, list[0], list[4]), p1 = either(b2, list[1], list[5]);
+    const uint32_t p2 = either(b2, list[2], list[6]), p3 = either(b2, list[3], list[7]);
+    const uint32_t mine = either(b0, either(b1, p0, p2), either(b1, p1, p3));
+    uint32_t next = dpp_of<0x101>(mine);                 // the next lane's
+    next = (li & 7) == 7 ? ninth : next;
+    const bool on = li < k && mine >= C;
+    where[0] = on ? expert(mine) : -1;
+    // (an equal logit with an equal bias has an equal value, and the keys' order is the indexes')
+    const int e = expert(mine), f = expert(next);
+    near = on && next >= C && mine - next <= close && !(logits[e] == logits[f] && sbias[e] == sbias[f]);
+  } else {
+    uint32_t lane[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) lane[i] = key[i];
+    sort_down<V>(lane);
+    uint32_t last = 0u;
+    for (int j = 0; j <= k; ++j) {                       // one more than is chosen, for its distance
+      const uint32_t best = group_all<L>(lane[0], OpMax());
+      if (best < C) break;                               // the whole group
+      near |= j > 0 && last - best <= close;
+      if (j == k) break;
+      last = best;
+      const bool mine = lane[0] == best;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t here = lane[i], next = i + 1 < V ? lane[i + 1 < V ? i + 1 : i] : 0u;
+        lane[i] = mine ? next : here;
+      }
+#pragma unroll
+      for (int q = 0; q < KQ; ++q)
+        if (j == q * L + li) where[q] = expert(best);
+    }
+  }
+  return group_any<L>(near) || unsure;
+}
+
+template <int V> MOE_DEV void row_to_lds(const float* v, MOE_LDS float* row, int li) {
+  wave_lds_order();
+#pragma unroll
+  for (int i = 0; i < V; i += 4)
+    *(MOE_LDS u32x4_t*)(row + li * V + i) = u32x4_t{__float_as_uint(v[i]), __float_as_uint(v[i + 1]),
+                                                    __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])};
+  wave_lds_order();
+}
+// Gates of the row's choices, lane j's choice of place q * L + j; row: the logits in LDS.
+template <int L, int SCORE>
+MOE_DEV void write_choice(const RouterArgs& a, size_t t, const Score<SCORE>& top, float sum, const int* where,
+                          const MOE_LDS float* row, int* sc, int li) {
+  constexpr int KQ = (kRouterMaxK + L - 1) / L;
+  float l[KQ], mine[KQ], most = -INFINITY, chosen = 0.f;
+#pragma unroll
+  for (int q = 0; q < KQ; ++q) {
+    l[q] = where[q] >= 0 ? row[where[q]] : -INFINITY;
+    most = fmaxf(most, l[q]);
+  }
+  // shares of the chosen, whose best may be next to nothing beside the row's
+  Score<SCORE> part = top;
+  if (a.renorm) part.at_top(group_all<L>(most, OpMaxF()));
+#pragma unroll
+  for (int q = 0; q < KQ; ++q) {
+    mine[q] = where[q] >= 0 ? part.weight(l[q]) : 0.f;
+    chosen += mine[q];
+  }
+  chosen = group_all<L>(chosen, OpAdd());
+  const float mul = a.renorm ? (chosen > 0.f ? a.scale / chosen : 0.f)
+                    : SCORE == MOE_SCORE_SOFTMAX ? a.scale / sum : a.scale * part.elow;
+#pragma unroll
+  for (int q = 0; q < KQ; ++q) {
+    const int j = q * L + li;
+    if (j >= a.k) continue;
+    a.ids[t * a.k + j] = where[q];
+    a.gates[t * a.k + j] = mine[q] * mul;
+    if (where[q] >= 0) atomicAdd(&sc[where[q]], 1);
+  }
+}
+
+// Forward with a choice by values; rows, sums and outputs as in k_router.  Rows whose choice 32 bits leave
+// open are remembered, a bit each, and chosen in 64 after every 32 rows: in the loop of the rows themselves
+// the 64-bit values' registers would halve its waves.
+constexpr int kChoiceWaves = 4;
 template <typename T, int L, int V, int SCORE>
-__global__ __launch_bounds__(kRouterThreads) void k_choice(RouterArgs a) {
+__global__ __launch_bounds__(kRouterThreads, kChoiceWaves) void k_choice(RouterArgs a) {
   constexpr int G = kRouterThreads / L, C = L * V, KQ = (kRouterMaxK + L - 1) / L;
   __shared__ float sp[4][C];
   __shared__ int sc[C];
   __shared__ float red[2][4];
   __shared__ int redn[4];
-  __shared__ double rows[G][C];
-  const int tid = threadIdx.x, li = tid % L, g = tid / L, c0 = li * V;
+  __shared__ __attribute__((aligned(16))) double rows[G][C];        // a row's logits and keys, or its 64-bit values
+  __shared__ __attribute__((aligned(16))) uint32_t worths[G][kRouterMaxGroups + 4];
+  __shared__ float sbias[C];
+  const int tid = threadIdx.x, lane = tid % L, group = tid / L;
   for (int i = tid; i < C; i += kRouterThreads) sc[i] = 0;
   if (blockIdx.x == 0 && tid == 0 && gridDim.x > 1) *a.done = 0;
   __syncthreads();
@@ -501,73 +821,91 @@ __global__ __launch_bounds__(kRouterThreads) void k_choice(RouterArgs a) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     psum[i] = 0.f;
-    bias[i] = a.bias && c0 + i < a.E ? a.bias[c0 + i] : 0.f;
+    const float b = a.bias && lane * V + i < a.E ? a.bias[lane * V + i] : 0.f;
+    bias[i] = b > -INFINITY ? b : -INFINITY;             // NaN
+    if (group == 0) sbias[lane * V + i] = bias[i];
   }
+  __syncthreads();
+  float bmost = 0.f;                                     // of the biases that can be chosen
+#pragma unroll
+  for (int i = 0; i < V; ++i) bmost = fmaxf(bmost, bias[i] > -INFINITY ? fabsf(bias[i]) : 0.f);
+  bmost = group_all<L>(bmost, OpMaxF());
+  uint32_t gid[V / 4];                                   // the experts' groups, a byte each
+#pragma unroll
+  for (int i = 0; i < V; ++i) gid[i / 4] = (i % 4 ? gid[i / 4] : 0u) | (uint32_t)min((lane * V + i) / a.gsize, 255) << 8 * (i % 4);
   float z = 0.f;
   int n = 0;
   const size_t step = (size_t)gridDim.x * G;
+  size_t t = (size_t)blockIdx.x * G + group;
   NextRow<T, V> next;
-  next.fetch(a, (size_t)blockIdx.x * G + g, c0);
-  for (size_t t = (size_t)blockIdx.x * G + g; t < (size_t)a.T; t += step) {
-    float v[V], w[V], e[V];
-    logits_of<T, V>(next, c0, a.E, v);
-    next.fetch(a, t + step, c0);
-    int32_t* ids = a.ids + t * a.k;
-    float* gates = a.gates + t * a.k;
-    Score<SCORE> sc_;
-    sc_.at_top(row_top<L, V>(v));
-    const float sum = row_scores<L, V, SCORE, false>(sc_, v, w, e, nullptr);
-    const float lsum = SCORE == MOE_SCORE_SOFTMAX ? sum : lane_sum<L, V>(e);
-    if (!row_live(sc_.top, sum)) {                       // the whole group
-      for (int j = li; j < a.k; j += L) {
-        ids[j] = -1;
-        gates[j] = 0.f;
+  next.fetch(a, t, lane * V);
+  while (t < (size_t)a.T) {
+    const size_t first = t;
+    uint32_t open = 0u;                                  // of the rows from `first` on
+    for (int r = 0; r < 32 && t < (size_t)a.T; ++r, t += step) {
+      const int li = fresh_lane(lane), g = fresh_lane(group), c0 = li * V;
+      float v[V], w[V], e[V];
+      logits_of<T, V>(next, c0, a.E, v);
+      next.fetch(a, t + step, c0);
+      Score<SCORE> sc_;
+      sc_.at_top(row_top<L, V>(v));
+      const float sum = row_scores<L, V, SCORE, false>(sc_, v, w, e, nullptr);
+      const float lsum = SCORE == MOE_SCORE_SOFTMAX ? sum : lane_sum<L, V>(e);
+      if (!row_live(sc_.top, sum)) {                     // the whole group
+        for (int j = li; j < a.k; j += L) {
+          a.ids[t * a.k + j] = -1;
+          a.gates[t * a.k + j] = 0.f;
+        }
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i) bad |= !(v[i] < INFINITY);       // NaN or +infinity
+        if (bad) atomicOr(a.status, MOE_DEV_BAD_LOGIT);
+        continue;
       }
-      bool bad = false;
+      const float inv = inverse(sum);
 #pragma unroll
-      for (int i = 0; i < V; ++i) bad |= !(v[i] < INFINITY);       // NaN or +infinity
-      if (bad) atomicOr(a.status, MOE_DEV_BAD_LOGIT);
-      continue;
+      for (int i = 0; i < V; ++i) psum[i] += w[i] * inv;
+      const float lse = sc_.top + logf(lsum);
+      z += lse * lse;
+      ++n;
+      // The bound of the scores' errors, in units of 2^-24 of the largest score, half as much again to spare.
+      // Softmax: the exponentials 3, their sum 14, its inverse and the product 3.  Sigmoid, with x = l - top:
+      // 2 |x| + |top| + 4 of the exponentials, of a slope s (1 - s), where s (1 - s) |l| is below 0.23, and 3
+      // of the sum, its inverse and the product: 5 + 0.75 |top|; where all are small, of parts that decay with
+      // x, 8 + |top|.  (Far from 0, by their own exponentials, 4, or 10 + 2 |top|.)
+      const float unit = SCORE == MOE_SCORE_SOFTMAX ? inv : fabsf(sc_.top) <= kNearTop ? 1.f : sc_.elow;
+      const float smost = SCORE == MOE_SCORE_SOFTMAX ? inv : sc_.elow;
+      const float err = smost * (SCORE == MOE_SCORE_SOFTMAX ? 30.f
+                                 : sc_.top > kNearTop       ? 8.f
+                                 : sc_.top < -kNearTop      ? 16.f - 3.f * sc_.top
+                                                            : (sc_.top > 0.f ? 8.f : 12.f) + 1.5f * fabsf(sc_.top)) * 0x1p-24f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) w[i] *= unit;
+      MOE_LDS float* row = (MOE_LDS float*)rows[g];
+      row_to_lds<V>(v, row, li);
+      int where[KQ];
+      if (choose32<L, V>(a, v, w, err, smost, bias, bmost, row, (MOE_LDS float*)sbias, (MOE_LDS uint32_t*)row + C,
+                         (MOE_LDS uint32_t*)worths[g], gid, li, where))
+        open |= 1u << r;
+      else
+        write_choice<L, SCORE>(a, t, sc_, sum, where, row, sc, li);
     }
-    const float inv = inverse(sum);
-#pragma unroll
-    for (int i = 0; i < V; ++i) psum[i] += w[i] * inv;
-    const float lse = sc_.top + logf(lsum);
-    z += lse * lse;
-    ++n;
-    int where[KQ];
-    choose64<L, V, SCORE>(a, v, sc_.top, bias, rows[g], li, where);
-    // lane j's choice: its weight again, from the logit of the lane that has it
-    float* logits = (float*)rows[g];
-    wave_lds_order();
-#pragma unroll
-    for (int i = 0; i < V; ++i) logits[c0 + i] = v[i];
-    wave_lds_order();
-    float l[KQ], mine[KQ], most = -INFINITY, chosen = 0.f;
-#pragma unroll
-    for (int q = 0; q < KQ; ++q) {
-      l[q] = where[q] >= 0 ? logits[where[q]] : -INFINITY;
-      most = fmaxf(most, l[q]);
-    }
-    wave_lds_order();                                    // read before the next row's
-    // shares of the chosen, whose best may be next to nothing beside the row's
-    Score<SCORE> part = sc_;
-    if (a.renorm) part.at_top(group_all<L>(most, OpMaxF()));
-#pragma unroll
-    for (int q = 0; q < KQ; ++q) {
-      mine[q] = where[q] >= 0 ? part.weight(l[q]) : 0.f;
-      chosen += mine[q];
-    }
-    chosen = group_all<L>(chosen, OpAdd());
-    const float mul = a.renorm ? (chosen > 0.f ? a.scale / chosen : 0.f)
-                      : SCORE == MOE_SCORE_SOFTMAX ? a.scale / sum : a.scale * sc_.elow;
-#pragma unroll
-    for (int q = 0; q < KQ; ++q) {
-      const int j = q * L + li;
-      if (j >= a.k) continue;
-      ids[j] = where[q];
-      gates[j] = mine[q] * mul;
-      if (where[q] >= 0) atomicAdd(&sc[where[q]], 1);
+    while (open) {                                       // the whole group
+      const int li = fresh_lane(lane), g = fresh_lane(group), c0 = li * V;
+      const size_t row = first + (size_t)__builtin_ctz(open) * step;
+      open &= open - 1;
+      NextRow<T, V> again;
+      again.fetch(a, row, c0);
+      float v[V];
+      logits_of<T, V>(again, c0, a.E, v);
+      Score<SCORE> sc_;
+      sc_.at_top(row_top<L, V>(v));
+      float w[V], e[V];
+      const float sum = row_scores<L, V, SCORE, false>(sc_, v, w, e, nullptr);
+      int where[KQ];
+      choose64<L, V, SCORE>(a, v, sc_.top, bias, (MOE_LDS double*)rows[g], li, where);
+      row_to_lds<V>(v, (MOE_LDS float*)rows[g], li);
+      write_choice<L, SCORE>(a, row, sc_, sum, where, (MOE_LDS float*)rows[g], sc, li);
     }
   }
   router_sums<L, V>(a, psum, z, n, sp, sc, red, redn);
@@ -922,6 +1260,8 @@ int launch_router(const moe_router& R, const moe_choice* C, const void* logits, 
   if (values) {
     a.bias = C->bias; a.groups = C->groups; a.top_groups = C->top_groups;
     a.two = C->group_score == MOE_GROUP_TOP2; a.gsize = R.E / C->groups;
+    const int each = R.E > 512 ? 16 : 8, wide = a.gsize / each;        // experts of a lane, lanes of a group
+    a.glog = a.gsize % each == 0 && (wide & (wide - 1)) == 0 ? __builtin_ctz(wide) : -1;
   }
   a.logits = logits; a.ld = (size_t)ld; a.mask = mask; a.T = T; a.E = R.E; a.k = R.k;
   a.renorm = R.renorm; a.scale = R.scale;
