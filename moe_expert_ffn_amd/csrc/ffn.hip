@@ -256,7 +256,7 @@ struct ExecArgs {
   void* bufP;             // backward: P = p * SiLU(G) * U per routed row
   size_t slots;           // padded slot capacity (rows of bufA, bufO, bufP, z_save)
   const float* sgate;     // per-slot gate (0 for padding slots)
-  uint32_t kmagic;        // ceil(2^32 / k): token = umulhi(row, kmagic)
+  uint32_t kmagic;        // ceil(2^32 / k), 0 for k = 1: token = umulhi(row, kmagic), or row
   uint8_t* dq;            // fp8 backward: D = p * dy per slot, e4m3 [slots][d]
   float* dqs;             //   its scales [slots / beta][d]
   uint8_t* zq;            //   dZ, e4m3 [slots][2 d_ff]
@@ -1210,8 +1210,8 @@ MOE_DEV void load_1k(BufRsrc rs, uint32_t off, MOE_LDS uint16_t* smem, size_t ld
   buf_load_lds16(rs, off + (uint32_t)(threadIdx.x & 63) * 16u,
                  (MOE_LDS void*)((MOE_LDS char*)smem + lds_off));
 }
-// token of routed row `row` = row / k, exact for the sizes the host admits
-MOE_DEV uint32_t token_of(uint32_t row, uint32_t kmagic) { return __umulhi(row, kmagic); }
+// token of routed row `row` = row / k, exact for the sizes the host admits (k = 1: 2^32 has no word, 0 stands for it)
+MOE_DEV uint32_t token_of(uint32_t row, uint32_t kmagic) { return kmagic ? __umulhi(row, kmagic) : row; }
 
 // M-tile item: tile idx / nnt of the worker's list, N tile idx % nnt.
 struct MItem { int e, slot0, nrows, nj; };
