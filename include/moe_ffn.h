@@ -99,7 +99,7 @@ typedef enum {
  * stream kernels. */
 #define MOE_EXEC_FP8_ACT 2
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_INT8 = 3 } moe_dtype;
 
 /* Optional per-workgroup timeline of the persistent GEMM phases (moe_forward
  * and moe_backward's `timeline` argument): uint64 [MOE_TL_PHASES]
@@ -124,7 +124,10 @@ typedef enum { MOE_PLAN_FWD = 0, MOE_PLAN_BWD = 1, MOE_PLAN_QUOTA = 2 } moe_plan
  * w_dtype is MOE_F32 (with act MOE_F32), MOE_BF16 (with act MOE_BF16) or
  * MOE_FP8_E4M3 (OCP e4m3fn codes, act MOE_BF16; forward and backward); fp8 weights
  * carry one fp32 scale per 128x128 block:
- *   w1_scale [E][2*d_ff/128][d/128], w2_scale [E][d/128][d_ff/128].
+ *   w1_scale [E][2*d_ff/128][d/128], w2_scale [E][d/128][d_ff/128];
+ * or MOE_INT8 (codes of -127..127, act MOE_BF16; forward only, to answer with), with one
+ * fp32 scale per weight row (moe_quantize_int8_rows makes both):
+ *   w1_scale [E][2*d_ff], w2_scale [E][d].
  * Requires d % 128 == 0 and d_ff % 64 == 0 (fp8: d_ff % 128 == 0). */
 typedef struct {
   int E, d, d_ff;
@@ -324,10 +327,16 @@ int moe_predict_split(const int32_t* counts, const int32_t* block_offsets,
  *     MOE_EXEC_TWO_PHASE the FC1 and FC2 events follow the one launch).
  *   timeline (nullable): phases MOE_TL_FC1 and MOE_TL_FC2 (see above; in
  *     the two-phase launch a workgroup's FC1 ends where its FC2 starts).
+ * int8 weights: the products are whole numbers of 8-bit codes, x and A = SiLU(G) U
+ *   quantized per row as moe_quantize_int8_rows does, A as it is in bf16:
+ *   Z = sx w1_scale (cx W1),  O = sa w2_scale (ca W2),  sums of 32 bits, scales in fp32.
+ *   z_save must be NULL and exec_flags 0 (MOE_ERR_ARG).  A token of NaN or infinities
+ *   has a row of NaN.  The plan moves no value, as above.
  * Errors: MOE_ERR_ARG for an invalid layer, size or null pointer;
  *   MOE_ERR_UNSUPPORTED for E > 512, P outside {1,2,4,8}, d not a multiple
  *   of 128, d_ff not a multiple of 64 (128 with e4m3 weights), a dtype pair
- *   other than fp32/fp32, bf16/bf16 or bf16 activations with e4m3 weights,
+ *   other than fp32/fp32, bf16/bf16 or bf16 activations with e4m3 or int8
+ *   weights (int8: d and d_ff up to 131072),
  *   or an operand of 2 GiB or more (T*d, moe_max_slots*2*d_ff or
  *   moe_max_slots*d elements of the activation dtype, or 2*d_ff*d of the
  *   weight dtype): the kernels address operands with 32-bit byte offsets and
@@ -728,6 +737,15 @@ int moe_grad_norm(const moe_grad_list* list, const moe_clip* clip, float* norm, 
 /* Every element of the list times *scale (device), rounded to nearest; untouched where it is 1.
  * Errors: MOE_ERR_ARG for a null pointer or a list whose tensors share memory. */
 int moe_grad_scale(const moe_grad_list* list, const float* scale, void* stream);
+
+/* Rows as 8-bit integers with a scale each, of a weight's channels or of activations' tokens:
+ *   scale = max|v| / 127 (fp32),  code = 127 v / max|v| rounded to nearest, half to even, as real numbers,
+ * in [-127, 127].  A row whose magnitudes are all below 2^-100 is stored as zeros with a scale of 0; one with
+ * NaN or an infinity gets a scale of NaN and codes of 0.
+ *   src [rows][cols], rows ld apart, MOE_F32 or MOE_BF16; codes [rows][cols]; scales [rows].
+ * Errors: MOE_ERR_ARG for rows < 0, cols < 1, ld < cols, an unknown dtype or a null pointer. */
+int moe_quantize_int8_rows(const void* src, int ld, int dtype, int rows, int cols, int8_t* codes, float* scales,
+                           void* stream);
 
 /* Timing helpers so a caller without a HIP binding can time the stages:
  * create / destroy a hipEvent_t, and the milliseconds between two recorded

@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(HERE, "libmoe_ffn.so")
 
 ABI_VERSION = 5                 # MOE_ABI_VERSION of the header these signatures follow
 MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0, -1, -2, -3, -4
-MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_INT8 = 0, 1, 2, 3
 PLAN_FWD, PLAN_BWD, PLAN_QUOTA = 0, 1, 2
 DEV_BAD_EXPERT, DEV_BAD_PLAN, DEV_BAD_OWNER, DEV_WAIT_TIMEOUT = 1, 2, 4, 8
 DEV_BAD_LOGIT, DEV_BAD_GRAD = 16, 32
@@ -47,7 +47,7 @@ EXPORTS = ["moe_abi_version", "moe_status_str", "moe_max_slots", "moe_max_blocks
            "moe_workspace_size", "moe_route_stats", "moe_route_stats_noalloc", "moe_plan",
            "moe_plan_gate",
            "moe_predict_cost", "moe_predict_split", "moe_quantize_token_blocks",
-           "moe_quantize_act_rows", "moe_forward",
+           "moe_quantize_act_rows", "moe_quantize_int8_rows", "moe_forward",
            "moe_backward", "moe_backward_gates", "moe_gate_grad",
            "moe_router_workspace_size", "moe_router_forward", "moe_router_backward",
            "moe_router_forward_choice", "moe_router_bias_update",
@@ -155,6 +155,8 @@ def load():
     lib.moe_predict_cost.argtypes = [_P] * 5 + [_I] * 6 + [_P, _P, _P]
     lib.moe_quantize_act_rows.restype = _I
     lib.moe_quantize_act_rows.argtypes = [_P, _I, _I, _P, _P, _P]
+    lib.moe_quantize_int8_rows.restype = _I
+    lib.moe_quantize_int8_rows.argtypes = [_P, _I, _I, _I, _I, _P, _P, _P]
     lib.moe_predict_split.restype = _I
     lib.moe_predict_split.argtypes = [_P] * 3 + [_I] * 7 + [_P, _P, _P, _P]
     lib.moe_plan_gate.restype = _I
@@ -292,6 +294,14 @@ def make_layer(w1, w2, w1_scale=None, w2_scale=None, act_dtype=torch.bfloat16) -
             raise MoeError("e4m3 weights need w1_scale and w2_scale")
         _expect(w1_scale, torch.float32, E * -(-two_dff // 128) * -(-d // 128), "w1_scale")
         _expect(w2_scale, torch.float32, E * -(-d // 128) * -(-(two_dff // 2) // 128), "w2_scale")
+    elif w1.dtype == torch.int8:
+        wcode = MOE_INT8
+        if w1_scale is None or w2_scale is None:
+            raise MoeError("int8 weights need w1_scale and w2_scale")
+        if act_dtype != torch.bfloat16:
+            raise MoeError(f"int8 weights take bfloat16 activations, not {act_dtype}")
+        _expect(w1_scale, torch.float32, E * two_dff, "w1_scale")
+        _expect(w2_scale, torch.float32, E * d, "w2_scale")
     elif w1.dtype == torch.float32:
         wcode = MOE_F32
     elif w1.dtype == torch.bfloat16:
@@ -761,6 +771,20 @@ def gate_grad(z, dz, row_to_slot, dlogp):
     _check(load().moe_gate_grad(_at(z), _at(dz), code, _at(row_to_slot), rows, slots, two // 2,
                                 _at(dlogp), st))
     return dlogp
+
+
+def quantize_int8_rows(src, codes, scales):
+    """Rows of src [rows][cols] (float32 or bfloat16) as int8 codes [rows][cols] with a scale each: a weight's
+    channels, or activations' tokens."""
+    st = _here(src, codes, scales)
+    if src.dim() != 2:
+        raise MoeError(f"src: expected [rows][cols], got {tuple(src.shape)}")
+    rows, cols = src.shape
+    ld = _rows(src, rows, cols, src.dtype, "src")
+    _vector(codes, rows * cols, torch.int8, "codes")
+    _vector(scales, rows, torch.float32, "scales")
+    _check(load().moe_quantize_int8_rows(_at(src), ld, _dtype_code(src.dtype, "src"), rows, cols, _at(codes), _at(scales), st))
+    return codes
 
 
 def norm_workspace(T, d, device) -> torch.Tensor:

@@ -25,6 +25,11 @@ bool ws_ok(const void* ws, size_t have, size_t need) {
   return have >= need;
 }
 
+bool dtype_ok(int d) { return d == MOE_F32 || d == MOE_BF16; }
+
+// 127 * 127 * K stays below 2^31
+constexpr int kI8MaxK = 131072;
+
 // Shared validation of the layer description; returns MOE_OK or an error.
 int check_layer(const moe_layer* L, bool backward) {
   if (!L) return MOE_ERR_ARG;
@@ -35,8 +40,13 @@ int check_layer(const moe_layer* L, bool backward) {
   const bool f32 = L->act_dtype == MOE_F32 && L->w_dtype == MOE_F32;
   const bool bf = L->act_dtype == MOE_BF16 && L->w_dtype == MOE_BF16;
   const bool f8 = L->act_dtype == MOE_BF16 && L->w_dtype == MOE_FP8_E4M3;
-  if (!f32 && !bf && !f8) return L->act_dtype > MOE_BF16 || L->w_dtype > MOE_FP8_E4M3
-                                     ? MOE_ERR_ARG : MOE_ERR_UNSUPPORTED;
+  const bool i8 = L->act_dtype == MOE_BF16 && L->w_dtype == MOE_INT8;
+  if (!f32 && !bf && !f8 && !i8)
+    return L->act_dtype > MOE_BF16 || L->w_dtype > MOE_INT8 ? MOE_ERR_ARG : MOE_ERR_UNSUPPORTED;
+  if (i8) {
+    if (!L->w1_scale || !L->w2_scale) return MOE_ERR_ARG;
+    if (backward || L->d > kI8MaxK || L->d_ff > kI8MaxK) return MOE_ERR_UNSUPPORTED;
+  }
   if (f8) {
     if (L->d_ff % 128 != 0) return MOE_ERR_UNSUPPORTED;
     if (!L->w1_scale || !L->w2_scale) return MOE_ERR_ARG;
@@ -49,6 +59,7 @@ Sizes make_sizes(const moe_layer* L, int T, int k, int beta, int P, int s) {
   z.T = T; z.k = k; z.E = L->E; z.d = L->d; z.dff = L->d_ff; z.beta = beta; z.P = P; z.s = s;
   z.act_bytes = L->act_dtype == MOE_F32 ? 4 : 2;
   z.fp8 = L->w_dtype == MOE_FP8_E4M3 ? 1 : 0;
+  z.i8 = L->w_dtype == MOE_INT8 ? 1 : 0;
   z.max_slots = moe_max_slots(T, k, L->E, beta);
   z.max_blocks = moe_max_blocks(T, k, L->E, beta);
   z.max_mt = max_tiles(z);
@@ -70,7 +81,7 @@ bool sizes_ok(int T, int k, int E, int beta) {
 bool extents_ok(const Sizes& z) {
   const unsigned long long lim = 1ull << 31, S = (unsigned long long)z.max_slots;
   const unsigned long long d = (unsigned long long)z.d, f = (unsigned long long)z.dff;
-  const unsigned long long ab = (unsigned long long)z.act_bytes, wb = z.fp8 ? 1ull : ab;
+  const unsigned long long ab = (unsigned long long)z.act_bytes, wb = z.fp8 || z.i8 ? 1ull : ab;
   return (unsigned long long)z.T * d * ab < lim && S * 2 * f * ab < lim && S * d * ab < lim &&
          2 * f * d * wb < lim;
 }
@@ -112,6 +123,7 @@ size_t moe_workspace_size(const moe_layer* L, int T, int k, int beta, int P, int
     if (!extents_ok(z)) return 0;
     const size_t f = exec_layout(z, false).total;
     if (f > need) need = f;
+    if (with_backward && z.i8) return 0;
     if (with_backward) {
       const size_t b = exec_layout(z, true).total;
       if (b > need) need = b;
@@ -209,6 +221,13 @@ int moe_quantize_act_rows(const void* src, int rows, int cols, uint8_t* codes, i
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
+int moe_quantize_int8_rows(const void* src, int ld, int dtype, int rows, int cols, int8_t* codes, float* scales,
+                           void* stream) {
+  if (rows < 0 || cols < 1 || ld < cols || !dtype_ok(dtype) || (rows > 0 && (!src || !codes || !scales)))
+    return MOE_ERR_ARG;
+  return launch_quant_int8_rows(src, ld, dtype, rows, cols, codes, scales, (hipStream_t)stream);
+}
+
 int moe_predict_cost(const int32_t* counts, const int32_t* block_offsets,
                      const int32_t* block_worker_fwd, const int32_t* block_worker_bwd,
                      const int32_t* owner, int E, int beta, int P, int d, int d_ff,
@@ -283,6 +302,7 @@ int moe_forward(const moe_layer* L, const void* x, const float* gates, const int
       (L->act_dtype != MOE_BF16 || L->w_dtype != MOE_FP8_E4M3 || !use_stream(z) ||
        (exec_flags & MOE_EXEC_TWO_PHASE)))
     return MOE_ERR_ARG;
+  if (z.i8 && (z_save || exec_flags)) return MOE_ERR_ARG;
   if (!ws_ok(ws, ws_bytes, exec_layout(z, false).total)) return MOE_ERR_WORKSPACE;
   LayerPtrs Lp{L->w1, L->w2, L->w1_scale, L->w2_scale, L->act_dtype, L->w_dtype};
   return launch_forward(z, Lp, x, gates, counts, block_offsets, row_to_slot, slot_to_row,
@@ -346,8 +366,6 @@ int moe_backward_gates(const moe_layer* L, const void* x, const float* gates, co
                   slot_to_row, owner, block_worker, dx, dw1, dw2, dlogp, status_dev, ws, ws_bytes,
                   exec_flags, stage_events, timeline, stream);
 }
-
-static bool dtype_ok(int d) { return d == MOE_F32 || d == MOE_BF16; }
 
 static int check_router(const moe_router* R, int ld, int T) {
   if (!R || R->E < 1 || R->k < 1 || R->k > R->E || T < 0 || ld < R->E || !dtype_ok(R->dtype) ||

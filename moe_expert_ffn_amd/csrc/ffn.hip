@@ -266,6 +266,7 @@ struct ExecArgs {
                           // [d_ff/128 (2 d_ff/128)][slots]
   void* hq;
   int32_t* he;
+  const float* sx;        // int8 layers: the scale of every slot's token
   void* dhat;             // fp8 backward on the stream kernels: D requantized and
                           //   widened back to bf16, [slots][d]
   const int32_t* boff;    // block offsets [E + 1]: boff[E] blocks of beta slots are in use
@@ -1489,6 +1490,102 @@ struct SrcFc2F8 : SrcFc2T<true> {
   MOE_DEV int steps(const Item&) const { return a.dff / 128; }
 };
 
+// FC1 and FC2 with int8 weights: codes of x (of A) and of the weights as stored, sums of 32 bits, scales of
+// tokens (slots, with the gate) and of weight rows applied in the epilogue.  The tile's 256 of each lie in the
+// item slot of LDS: rows' at 1024 (FC1 reads its slot map at 0), weight rows' in a slot of their own behind
+// the scratch.
+constexpr size_t kI8ScaleOff = kStreamLds;
+constexpr size_t kStreamLdsI8 = kStreamLds + kItemSlots * 1024;
+using RowI8 = RowKI8<256, kWNW>;
+MOE_DEV const MOE_LDS float* item_wscales(const MOE_LDS uint16_t* smem, int slot) {
+  return (const MOE_LDS float*)((const MOE_LDS char*)smem + kI8ScaleOff + slot * 1024);
+}
+// an accumulator's sum as a number
+MOE_DEV float i8_sum(float word) { return (float)__float_as_int(word); }
+struct SrcFc1I8 : SrcFc1T<false> {
+  using OB = RowI8;
+  // of the tile's weight row rho the row of W1
+  MOE_DEV int w1_row(const Item& it, int rho) const {
+    const int q = rho >> 5;
+    return (q & 1) * a.dff + it.nj * (WC::BN / 2) + (q >> 1) * 32 + (rho & 31);
+  }
+  MOE_DEV void fill(const Item& it, int slot) const {
+    fill_rows(it, slot);
+    if (wave_id() == 1)
+      load_1k(make_rsrc(a.sx, (uint32_t)(a.slots * 4)), (uint32_t)it.slot0 * 4u, smem,
+              kStageBytes + slot * kItemBytes + 1024);
+    if (wave_id() == 2)
+      buf_load_lds16(make_rsrc(a.w1s + (size_t)it.e * 2 * a.dff, (uint32_t)(2 * a.dff * 4)),
+                     (uint32_t)w1_row(it, (threadIdx.x & 63) * 4) * 4u,
+                     (MOE_LDS void*)((MOE_LDS char*)smem + kI8ScaleOff + slot * 1024));
+  }
+  MOE_DEV RowW opA(const Item& it, int slot) const { return gathered(it, slot, a.xq, a.d / 2); }
+  MOE_DEV RowI8 opB(const Item& it, int) const {
+    RowI8 w;
+    w.init((const uint16_t*)((const int8_t*)a.w1 + (size_t)it.e * 2 * a.dff * a.d), (uint32_t)((size_t)2 * a.dff * a.d),
+           [&](int rho) { return w1_row(it, rho) * (a.d / 2); });
+    return w;
+  }
+  MOE_DEV int steps(const Item&) const { return a.d / 128; }
+  template <int B> MOE_DEV void relaxed_wait() const { wait_vm_lgkm0<vm_clamp(B + kEpiVmA)>(); }
+  MOE_DEV void epilogue(const Item& it, int slot, const f32x16_t (&acc)[WC::MB][WC::NB]) const {
+    const int lane = threadIdx.x & 63, wm = wave_id() / WC::WAVES_N, wn = wave_id() % WC::WAVES_N;
+    const int dff = a.dff, colb = it.nj * (WC::BN / 2) + wn * 32;
+    const BufRsrc ra = make_rsrc(a.bufA, (uint32_t)(a.slots * dff * 2));
+    const MOE_LDS float* rs = item_gates(smem, slot);
+    const MOE_LDS float* ws = item_wscales(smem, slot) + wn * WC::WN + 4 * (lane >> 5);
+    MOE_LDS char* scr = epi_scratch(smem);
+#pragma unroll
+    for (int i = 0; i < WC::MB; ++i) {
+      const int rb = wm * WC::WM + i * 32;
+      const float s = rs[rb + (lane & 31)];
+      RowStore<uint16_t, 1>::run(scr, [&](int, int g, float* v) {
+        for (int q = 0; q < 4; ++q) {
+          const float gv = i8_sum(acc[i][0][4 * g + q]) * ws[8 * g + q] * s;
+          v[q] = gv * sigm(gv) * (i8_sum(acc[i][1][4 * g + q]) * ws[32 + 8 * g + q] * s);
+        }
+      }, [&](int row, int c, const u32x4_t& d) {
+        st_row16(ra, it.slot0 + rb + row, dff, colb + c * 8, rb + row < it.nrows, d);
+      });
+    }
+  }
+};
+struct SrcFc2I8 : SrcFc2T<false> {
+  using OB = RowI8;
+  MOE_DEV void fill(const Item& it, int slot) const {
+    fill_gates(it, slot);
+    if (wave_id() == 2)
+      load_1k(make_rsrc(a.w2s + (size_t)it.e * a.d, (uint32_t)(a.d * 4)), (uint32_t)(it.nj * WC::BN) * 4u, smem,
+              kI8ScaleOff + slot * 1024);
+  }
+  MOE_DEV RowW opA(const Item& it, int) const { return slotrows(it, a.hq, a.dff / 2); }
+  MOE_DEV RowI8 opB(const Item& it, int) const {
+    RowI8 w;
+    w.init((const uint16_t*)((const int8_t*)a.w2 + (size_t)it.e * a.d * a.dff), (uint32_t)((size_t)a.d * a.dff),
+           [&](int rho) { return (it.nj * WC::BN + rho) * (a.dff / 2); });
+    return w;
+  }
+  MOE_DEV int steps(const Item&) const { return a.dff / 128; }
+  MOE_DEV void epilogue(const Item& it, int slot, const f32x16_t (&acc)[WC::MB][WC::NB]) const {
+    const int lane = threadIdx.x & 63, wm = wave_id() / WC::WAVES_N, wn = wave_id() % WC::WAVES_N;
+    const BufRsrc ro = make_rsrc(a.bufO, (uint32_t)(a.slots * a.d * 2));
+    const int colb = it.nj * WC::BN + wn * WC::WN;
+    const MOE_LDS float* gt = item_gates(smem, slot);
+    const MOE_LDS float* ws = item_wscales(smem, slot) + wn * WC::WN + 4 * (lane >> 5);
+    MOE_LDS char* scr = epi_scratch(smem);
+#pragma unroll
+    for (int i = 0; i < WC::MB; ++i) {
+      const int rb = wm * WC::WM + i * 32;
+      const float s = gt[rb + (lane & 31)];
+      RowStore<uint16_t, 2>::run(scr, [&](int jj, int g, float* v) {
+        for (int q = 0; q < 4; ++q) v[q] = i8_sum(acc[i][jj][4 * g + q]) * ws[32 * jj + 8 * g + q] * s;
+      }, [&](int row, int c, const u32x4_t& d) {
+        st_row16(ro, it.slot0 + rb + row, a.d, colb + c * 8, rb + row < it.nrows, d);
+      });
+    }
+  }
+};
+
 // dA = p * dy W2 (W2 [d][d_ff] read K-major through transpose reads), then
 // dZ = [dA U s (1 + G (1 - s)), dA G s] with s = sigmoid(G), and the gated
 // activation P = p SiLU(G) U for the weight gradient of W2.  With e4m3
@@ -2190,7 +2287,12 @@ WsLayout exec_layout(const Sizes& z, bool backward) {
   L.rslots = backward ? take(sizeof(float) * (size_t)z.P * z.s * 3 * z.d * z.dff) : o;
   L.bufP = backward ? take((size_t)z.act_bytes * z.max_slots * z.dff) : o;
   L.sgate = take(sizeof(float) * z.max_slots);
-  L.dq = L.dqs = L.zq = L.zqs = L.dhat = L.xq = L.xe = L.hq = L.he = o;
+  L.dq = L.dqs = L.zq = L.zqs = L.dhat = L.xq = L.xe = L.hq = L.he = L.sx = o;
+  if (z.i8) {
+    L.xq = take((size_t)z.T * z.d);
+    L.hq = take(z.max_slots * (size_t)z.dff);
+    L.sx = take(sizeof(float) * z.max_slots);
+  }
   if (z.fp8 && use_stream(z)) {      // MOE_EXEC_FP8_ACT: x (dy) and A (dZ) as e4m3 rows
     const size_t hc = (size_t)(backward ? 2 : 1) * z.dff;
     L.xq = take((size_t)z.T * z.d);
@@ -2217,7 +2319,8 @@ bool use_big_tiles(const Sizes& z) {
 }
 
 size_t max_tiles(const Sizes& z) {
-  const int bm = use_big_tiles(z) ? BigCfg::BM : SmallCfg::BM;
+  // an int8 layer's tiles may be either kind, by the batch
+  const int bm = z.i8 ? kFewRows : use_big_tiles(z) ? BigCfg::BM : SmallCfg::BM;
   const size_t per_block = z.beta > bm ? (size_t)(z.beta + bm - 1) / bm : 1;
   return z.max_blocks * per_block;
 }
@@ -2276,7 +2379,7 @@ static void launch_sched(const Sizes& z, const int32_t* counts, const int32_t* b
   }
   s.counts = counts; s.boff = boff; s.bw = bw; s.owner = owner;
   s.E = z.E; s.P = z.P; s.s = z.s; s.beta = z.beta; s.backward = bwd ? 1 : 0;
-  s.bm = use_big_tiles(z) ? BigCfg::BM : SmallCfg::BM;
+  s.bm = z.i8 && i8_few(z) ? kFewRows : use_big_tiles(z) ? BigCfg::BM : SmallCfg::BM;
   s.ctr = (int32_t*)(ws + L.ctr);
   s.mt_cnt = (int32_t*)(ws + L.mt_cnt);
   s.mt = (int4*)(ws + L.mt);
@@ -2322,6 +2425,11 @@ static ExecArgs make_exec(const Sizes& z, const LayerPtrs& Lp, char* ws, const W
   a.slots = z.max_slots;
   a.sgate = (const float*)(ws + L.sgate);
   a.kmagic = (uint32_t)((((uint64_t)1 << 32) + (uint64_t)z.k - 1) / (uint64_t)z.k);
+  if (z.i8) {
+    a.xq = ws + L.xq;
+    a.hq = ws + L.hq;
+    a.sx = (const float*)(ws + L.sx);
+  }
   if (z.fp8) {
     a.xq = ws + L.xq;
     a.xe = (const int32_t*)(ws + L.xe);
@@ -2431,6 +2539,37 @@ static void run_forward_stream(const Sizes& z, ExecArgs& a, const int32_t* row_t
   rec(ev, 4, st);
 }
 
+// Where experts have few rows, a 256-row tile of the stream kernels is mostly empty and their items are too few
+// for the chip; sizes off the 256 grid have no others.
+bool i8_few(const Sizes& z) { return !use_stream(z) || (long long)z.T * z.k <= 16ll * z.E; }
+
+static void run_forward_int8(const Sizes& z, ExecArgs& a, const int32_t* row_to_slot, void* y, void* const* ev,
+                             hipStream_t st) {
+  const bool few = i8_few(z);
+  const size_t rows = (size_t)z.T * z.k;
+  launch_quant_int8_tokens(a.x, z.T, z.d, row_to_slot, z.k, (int8_t*)a.xq, (float*)a.sx, st);
+  a.tl_phase = MOE_TL_FC1;
+  if (few)
+    launch_i8_few(true, (const int8_t*)a.xq, (const int8_t*)a.w1, a.w1s, a.sx, a.slot_to_row, a.bufA, a.mt, a.mt_cnt,
+                  a.max_mt, z.P, z.k, z.d, z.dff, rows, st);
+  else
+    launch_stream<SrcFc1I8, WC, RowW, RowI8>(a, z.dff / (WC::BN / 2), kStreamLdsI8, st);
+  launch_quant_int8_slots(a.bufA, (int)z.max_slots, z.dff, a.slot_to_row, a.boff + z.E, z.beta, (int8_t*)a.hq,
+                          (float*)a.sgate, st);
+  rec(ev, 2, st);
+  a.tl_phase = MOE_TL_FC2;
+  if (few)
+    launch_i8_few(false, (const int8_t*)a.hq, (const int8_t*)a.w2, a.w2s, a.sgate, a.slot_to_row, a.bufO, a.mt, a.mt_cnt,
+                  a.max_mt, z.P, z.k, z.dff, z.d, rows, st);
+  else
+    launch_stream<SrcFc2I8, WC, RowW, RowI8>(a, z.d / WC::BN, kStreamLdsI8, st);
+  rec(ev, 3, st);
+  if (z.T > 0)
+    hipLaunchKernelGGL(k_combine<uint16_t>, combine_grid<uint16_t>(z.T, z.d), dim3(256), 0, st, (const uint16_t*)a.bufO,
+                       row_to_slot, z.T, z.k, z.d, (uint16_t*)y);
+  rec(ev, 4, st);
+}
+
 int launch_forward(const Sizes& z, const LayerPtrs& Lp, const void* x, const float* gates,
                    const int32_t* counts, const int32_t* boff, const int32_t* row_to_slot,
                    const int32_t* slot_to_row, const int32_t* block_worker, void* y,
@@ -2447,7 +2586,8 @@ int launch_forward(const Sizes& z, const LayerPtrs& Lp, const void* x, const flo
   rec(ev, 0, st);
   // the stream kernels read the per-slot gates, written beside the schedule
   const bool stream = Lp.act_dtype == MOE_BF16 &&
-                      (Lp.w_dtype == MOE_BF16 || Lp.w_dtype == MOE_FP8_E4M3) && use_stream(z);
+                      (((Lp.w_dtype == MOE_BF16 || Lp.w_dtype == MOE_FP8_E4M3) && use_stream(z)) ||
+                       Lp.w_dtype == MOE_INT8);
   launch_sched(z, counts, boff, block_worker, nullptr, false, ws, L, status,
                stream ? slot_to_row : nullptr, stream ? gates : nullptr, st);
   rec(ev, 1, st);
@@ -2459,7 +2599,8 @@ int launch_forward(const Sizes& z, const LayerPtrs& Lp, const void* x, const flo
   a.status = status;
   const bool big = use_big_tiles(z);
   const bool f8act = (exec_flags & MOE_EXEC_FP8_ACT) != 0;
-  if (Lp.act_dtype == MOE_BF16 && Lp.w_dtype == MOE_BF16 && use_stream(z))
+  if (Lp.w_dtype == MOE_INT8) run_forward_int8(z, a, row_to_slot, y, ev, st);
+  else if (Lp.act_dtype == MOE_BF16 && Lp.w_dtype == MOE_BF16 && use_stream(z))
     run_forward_stream<false>(z, a, row_to_slot, y, split, n1split, false, ev, st);
   else if (Lp.act_dtype == MOE_BF16 && Lp.w_dtype == MOE_FP8_E4M3 && use_stream(z))
     run_forward_stream<true>(z, a, row_to_slot, y, split, n1split, f8act, ev, st);

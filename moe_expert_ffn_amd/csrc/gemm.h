@@ -756,6 +756,19 @@ template <int ROWS, int NWAVES, size_t SC_OFF> struct RowK8A : RowK8<ROWS, NWAVE
 template <class T, class = void> struct op_f8mma { static constexpr bool value = false; };
 template <class T> struct op_f8mma<T, decltype((void)T::kF8Mma)> { static constexpr bool value = T::kF8Mma; };
 
+// K-contiguous rows of int8 codes, 128 (one K step) per row and stage, laid out like bf16 rows of 64: a
+// fragment's 16 bytes a lane are 16 consecutive codes, for A and B alike, of the 32 of v_mfma_i32_32x32x32_i8.
+// The accumulators hold the 32-bit sums' words.
+template <class T, class = void> struct op_i8 { static constexpr bool value = false; };
+template <class T> struct op_i8<T, decltype((void)T::kI8)> { static constexpr bool value = T::kI8; };
+template <int ROWS, int NWAVES> struct RowKI8 : RowK<ROWS, NWAVES, 64> { static constexpr bool kI8 = true; };
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+MOE_DEV f32x16_t mfma_i8(const bf16x8_t& w, const bf16x8_t& x, const f32x16_t& c) {
+  typedef int i32x4_t __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(f32x16_t, __builtin_amdgcn_mfma_i32_32x32x32_i8(
+      __builtin_bit_cast(i32x4_t, w), __builtin_bit_cast(i32x4_t, x), __builtin_bit_cast(i32x16_t, c), 0, 0, 0));
+}
+
 // 8 e4m3 codes (bytes of q, low first) times s, as bf16 rounded to nearest even.
 MOE_DEV bf16x8_t dequant8(const u32x2_t& q, float s) {
   bf16x8_t o;
@@ -1157,6 +1170,11 @@ template <class C, class OA, class OB, bool ROWS_IN_REGS = false> struct WideStr
         for (int i = 0; i < C::MB; ++i)
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bj, a[SB][i], acc[i][j], 0, 0, 0);
       }
+    } else if constexpr (op_i8<OB>::value) {
+#pragma unroll
+      for (int i = 0; i < C::MB; ++i)
+#pragma unroll
+        for (int j = 0; j < C::NB; ++j) acc[i][j] = mfma_i8(b[SB][j], a[SB][i], acc[i][j]);
     } else if constexpr (ROWS_IN_REGS) {
 #pragma unroll
       for (int i = 0; i < C::MB; ++i)

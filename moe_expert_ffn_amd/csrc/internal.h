@@ -23,6 +23,7 @@ struct Sizes {
   int T, k, E, d, dff, beta, P, s;
   int act_bytes;
   int fp8;            // e4m3 weights: the backward requantizes D and dZ
+  int i8;             // int8 weights
   size_t max_slots, max_blocks, max_mt;
 };
 
@@ -32,12 +33,14 @@ struct WsLayout {
   size_t dhat;               // fp8 backward on the stream kernels: requantized D as bf16
   size_t xq, xe;             // fp8 MFMA forward: x as e4m3 codes and row exponents
   size_t hq, he;             // ... and A = SiLU(G) U as e4m3 codes and row exponents
+  size_t sx;                 // int8 layers (codes in xq and hq): the scale of every slot's token
   size_t total;
 };
 
 WsLayout exec_layout(const Sizes& z, bool backward);
 bool use_big_tiles(const Sizes& z);
 bool use_stream(const Sizes& z);
+bool i8_few(const Sizes& z);
 size_t max_tiles(const Sizes& z);
 size_t route_ws_bytes(int T, int k, int E);
 // the routing statistics' scratch array of moe_route_stats_noalloc
@@ -102,6 +105,17 @@ int launch_norm_bwd(const moe_norm& N, bool out, NormRows dn, NormRows dr, NormR
 size_t adamw_ws_bytes(int tensors);
 int launch_adamw_table(const moe_adamw_tensor* t, int count, moe_adamw_list* out, hipStream_t st);
 int launch_adamw(const moe_adamw_list& l, const moe_adamw_hyper& h, hipStream_t st);
+
+int launch_quant_int8_rows(const void* src, int ld, int dtype, int rows, int cols, int8_t* codes, float* scales,
+                           hipStream_t st);
+void launch_quant_int8_tokens(const void* x, int T, int d, const int32_t* row_to_slot, int k, int8_t* codes,
+                              float* slot_scale, hipStream_t st);
+void launch_quant_int8_slots(const void* rows, int slots, int dff, const int32_t* slot_to_row, const int32_t* blocks,
+                             int beta, int8_t* codes, float* gates, hipStream_t st);
+constexpr int kFewRows = 64;           // of a tile of launch_i8_few
+void launch_i8_few(bool fc1, const int8_t* codes, const int8_t* w, const float* w_scale, const float* slot_scale,
+                   const int32_t* slot_to_row, void* out, const int4* mt, const int32_t* mt_cnt, int max_mt, int P, int k,
+                   int K, int N, size_t rows, hipStream_t st);
 
 size_t grads_ws_bytes(int tensors);
 int launch_grads_table(const moe_grad_tensor* t, int count, moe_grad_list* out, hipStream_t st);

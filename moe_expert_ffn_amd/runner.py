@@ -17,6 +17,8 @@ class LayerRunner:
         dev = w1.device
         self.dev = dev
         self.layer = B.make_layer(w1, w2, w1_scale, w2_scale, act_dtype)
+        if with_backward and self.layer.w_dtype == B.MOE_INT8:
+            raise B.MoeError("int8 weights have no backward pass")
         self.keep = (w1, w2, w1_scale, w2_scale)
         self.E, self.d, self.dff = self.layer.E, self.layer.d, self.layer.d_ff
         self.T, self.k, self.beta, self.P, self.s, self.lam = T, k, beta, P, s, lam
