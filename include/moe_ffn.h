@@ -379,7 +379,8 @@ int moe_forward(const moe_layer* L, const void* x, const float* gates,
  * requantized D and dZ live in `ws` (moe_workspace_size counts them): as
  * codes and scales, or, when d and d_ff are multiples of 256, widened back
  * to bf16 (code times scale), which is the value the products use.
- * Errors: as moe_forward, plus MOE_ERR_ARG for s < 0.  On the device, a
+ * Errors: as moe_forward, plus MOE_ERR_UNSUPPORTED for int8 weights and
+ *   MOE_ERR_ARG for s < 0.  On the device, a
  *   plan whose blocks of one expert on one worker are not one contiguous run,
  *   or that gives a worker more than s replica experts, sets
  *   MOE_DEV_BAD_PLAN; an owner outside [0, P) sets MOE_DEV_BAD_OWNER. */

@@ -16,6 +16,7 @@
 //           fp32 reduction of replica partials into the owner slot.
 #include "common.h"
 #include "gemm.h"
+#include "int8.h"
 #include <cstdlib>
 #include <cstring>
 #include <utility>
@@ -45,6 +46,8 @@ struct SchedArgs {
   const float* gate_src;
   float* gate_out;
   size_t gate_n;
+  unsigned gate_wg;    // workgroups that do
+  QuantI8 x;           // int8 layers: x's rows, quantized by the workgroups past those
 };
 
 MOE_DEV int expert_of(int g, const int* boff_s, int E) {
@@ -79,11 +82,19 @@ MOE_DEV int block_rows(int g, int e, int beta, const int* boff_s, const int* cnt
 // (when max_blocks entries fit), so each worker's pass over the blocks reads
 // LDS instead of issuing a global load per 64 blocks.
 constexpr int kSchedThreads = 512;
-template <bool BWL>
+template <bool BWL, bool I8>
 __global__ __launch_bounds__(kSchedThreads) void k_sched(SchedArgs a) {
   extern __shared__ int sm[];
+  if constexpr (I8) {            // x's rows beside both: 21 us of a Qwen3-shaped batch behind 12 of scheduling
+    if (blockIdx.x > a.gate_wg) {
+      const int block = blockIdx.x - 1 - a.gate_wg, blocks = gridDim.x - 1 - a.gate_wg;
+      if (a.x.cols <= kI8WaveCols) quant_i8_rows<uint16_t, 64, 4, kSchedThreads>(a.x, block, blocks);
+      else quant_i8_rows<uint16_t, kSchedThreads, 2, kSchedThreads>(a.x, block, blocks);
+      return;
+    }
+  }
   if (blockIdx.x > 0) {          // the per-slot gates, beside the scheduling workgroup
-    const size_t stride = (size_t)(gridDim.x - 1) * kSchedThreads;
+    const size_t stride = (size_t)a.gate_wg * kSchedThreads;
     for (size_t i = (size_t)(blockIdx.x - 1) * kSchedThreads + threadIdx.x; i < a.gate_n; i += stride) {
       const int row = a.gate_s2r[i];
       a.gate_out[i] = row >= 0 ? a.gate_src[row] : 0.f;
@@ -2367,7 +2378,7 @@ static size_t sched_lds(const Sizes& z, bool bwd, bool bwl) {
 static void launch_sched(const Sizes& z, const int32_t* counts, const int32_t* boff,
                          const int32_t* bw, const int32_t* owner, bool bwd, char* ws,
                          const WsLayout& L, int32_t* status, const int32_t* slot_to_row,
-                         const float* gates, hipStream_t st) {
+                         const float* gates, const QuantI8* x, hipStream_t st) {
   SchedArgs s{};
   unsigned gate_wg = 0;
   if (gates && z.max_slots > 0) {
@@ -2391,18 +2402,22 @@ static void launch_sched(const Sizes& z, const int32_t* counts, const int32_t* b
   s.flags = (int32_t*)(ws + L.flags);
   s.status = status;
   s.max_blocks = (int)z.max_blocks;
+  s.gate_wg = gate_wg;
+  unsigned x_wg = 0;
+  if (x) {
+    s.x = *x;
+    const size_t rpw = x->cols <= kI8WaveCols ? kSchedThreads / 64 : 1;
+    x_wg = (unsigned)std::min<size_t>(((size_t)x->rows + rpw - 1) / rpw, 1 << 22);
+  }
   // block_worker goes through LDS when it fits next to the rest (64 KB)
   const bool bwl = sched_lds(z, true, true) <= 64 * 1024;
-  const size_t lds = sched_lds(z, bwd, bwl);
-  if (bwl) {
-    (void)hipFuncSetAttribute((const void*)k_sched<true>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)sched_lds(z, true, true));
-    hipLaunchKernelGGL(k_sched<true>, dim3(1 + gate_wg), dim3(kSchedThreads), lds, st, s);
-  } else {
-    (void)hipFuncSetAttribute((const void*)k_sched<false>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)sched_lds(z, true, false));
-    hipLaunchKernelGGL(k_sched<false>, dim3(1 + gate_wg), dim3(kSchedThreads), lds, st, s);
-  }
+  const size_t lds = sched_lds(z, bwd, bwl), most = sched_lds(z, true, bwl);
+  auto go = [&](auto kernel) {
+    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    hipLaunchKernelGGL(kernel, dim3(1 + gate_wg + x_wg), dim3(kSchedThreads), lds, st, s);
+  };
+  if (x) bwl ? go(k_sched<true, true>) : go(k_sched<false, true>);
+  else bwl ? go(k_sched<true, false>) : go(k_sched<false, false>);
 }
 
 static ExecArgs make_exec(const Sizes& z, const LayerPtrs& Lp, char* ws, const WsLayout& L) {
@@ -2547,7 +2562,6 @@ static void run_forward_int8(const Sizes& z, ExecArgs& a, const int32_t* row_to_
                              hipStream_t st) {
   const bool few = i8_few(z);
   const size_t rows = (size_t)z.T * z.k;
-  launch_quant_int8_tokens(a.x, z.T, z.d, row_to_slot, z.k, (int8_t*)a.xq, (float*)a.sx, st);
   a.tl_phase = MOE_TL_FC1;
   if (few)
     launch_i8_few(true, (const int8_t*)a.xq, (const int8_t*)a.w1, a.w1s, a.sx, a.slot_to_row, a.bufA, a.mt, a.mt_cnt,
@@ -2588,8 +2602,13 @@ int launch_forward(const Sizes& z, const LayerPtrs& Lp, const void* x, const flo
   const bool stream = Lp.act_dtype == MOE_BF16 &&
                       (((Lp.w_dtype == MOE_BF16 || Lp.w_dtype == MOE_FP8_E4M3) && use_stream(z)) ||
                        Lp.w_dtype == MOE_INT8);
+  QuantI8 xq{};
+  if (z.i8) {
+    xq.src = x; xq.ld = (size_t)z.d; xq.rows = z.T; xq.cols = z.d; xq.codes = (int8_t*)(ws + L.xq);
+    xq.scales = (float*)(ws + L.sx); xq.row_to_slot = row_to_slot; xq.k = z.k;
+  }
   launch_sched(z, counts, boff, block_worker, nullptr, false, ws, L, status,
-               stream ? slot_to_row : nullptr, stream ? gates : nullptr, st);
+               stream ? slot_to_row : nullptr, stream ? gates : nullptr, z.i8 ? &xq : nullptr, st);
   rec(ev, 1, st);
   ExecArgs a = make_exec(z, Lp, ws, L);
   a.x = x; a.gates = gates; a.slot_to_row = slot_to_row; a.row_to_slot = row_to_slot;
@@ -2723,7 +2742,7 @@ int launch_backward(const Sizes& z, const LayerPtrs& Lp, const void* x, const fl
   rec(ev, 0, st);
   const bool stream = Lp.act_dtype != MOE_F32 && use_stream(z);
   launch_sched(z, counts, boff, block_worker, owner, true, ws, L, status,
-               stream ? slot_to_row : nullptr, stream ? gates : nullptr, st);
+               stream ? slot_to_row : nullptr, stream ? gates : nullptr, nullptr, st);
   rec(ev, 1, st);
   ExecArgs a = make_exec(z, Lp, ws, L);
   a.x = x; a.gates = gates; a.slot_to_row = slot_to_row; a.row_to_slot = row_to_slot;

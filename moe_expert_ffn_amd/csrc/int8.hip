@@ -4,138 +4,27 @@
 #include <algorithm>
 
 #include "gemm.h"
+#include "int8.h"
 #include "internal.h"
 #include "lanes.h"
 
 namespace moe {
 
-// ---- rows to codes -------------------------------------------------------------
-struct QuantI8 {
-  const void* src;
-  size_t ld;
-  int rows, cols;
-  int8_t* codes;
-  float* scales;             // [rows]; of slots: the gate before, gate times scale after
-  // the layer's tokens: their scale to each of their slots as well
-  const int32_t* row_to_slot;
-  int k;
-  // the layer's slots: those in use, by the rows they hold and the blocks' number
-  const int32_t* slot_to_row;
-  const int32_t* blocks;
-  int beta;
-};
-
-// The nearest whole number to 127 v / amax, half to even, of the real numbers: c is within one of it, and
-// what is left of 127 v after c amax says which of the three it is.  A bf16 v has 8 bits, c amax 15, and c
-// is 0 where v is far below amax, so in fp32 the rest is exact.
-MOE_DEV int code_of(uint16_t, float v, float inv, float amax) {
-  const float c = rintf(v * inv), rest = __builtin_fmaf(-c, amax, v * 127.f), half = 0.5f * amax;
-  const int n = (int)c;
-  const bool off = fabsf(rest) > half || (fabsf(rest) == half && (n & 1));
-  return n + (off ? (rest > 0.f ? 1 : -1) : 0);
-}
-// A 32-bit v is only looked at again, in 64 bits, where v inv, which is off by 127 2^-23, is near to a half.
-MOE_DEV int code_of(float, float v, float inv, float amax) {
-  const float t = v * inv, c = rintf(t);
-  int n = (int)c;
-  if (fabsf(fabsf(t - c) - 0.5f) < 0x1p-15f) {
-    const double rest = fma(-(double)c, (double)amax, (double)v * 127.0), half = 0.5 * (double)amax;
-    if (fabs(rest) > half || (fabs(rest) == half && (n & 1))) n += rest > 0.0 ? 1 : -1;
-  }
-  return n;
-}
-
-// NT threads take a row; its first KC pieces of 8 elements a thread stay in registers between the maximum
-// and the codes, further ones are read again.
-template <typename T, int NT, int KC>
-__global__ __launch_bounds__(256) void k_quant_i8(QuantI8 a) {
-  constexpr int RPW = 256 / NT;
-  __shared__ uint32_t red[4];
-  const int li = threadIdx.x % NT;
-  size_t rows = a.rows;
-  if (a.blocks) rows = min(rows, (size_t)*a.blocks * a.beta);
-  for (size_t r = (size_t)blockIdx.x * RPW + threadIdx.x / NT; r < rows; r += (size_t)gridDim.x * RPW) {
-    if (a.slot_to_row && a.slot_to_row[r] < 0) continue;               // the whole row's threads
-    const T* src = (const T*)a.src + r * a.ld;
-    int8_t* out = a.codes + r * a.cols;
-    T raw[KC][8];
-#pragma unroll
-    for (int q = 0; q < KC; ++q) {
-      const int c = (li + q * NT) * 8;
-      if (c < a.cols) load_piece<T, 8>(src, c, a.cols, raw[q]);
-    }
-    uint32_t most = 0u;                                  // magnitudes order as their words do
-    auto look = [&](int c, T* v) {
-      settle_piece<T, 8>(c, a.cols, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) most = max(most, __float_as_uint(elem_f(v[i])) & 0x7FFFFFFFu);
-    };
-#pragma unroll
-    for (int q = 0; q < KC; ++q) {
-      const int c = (li + q * NT) * 8;
-      if (c < a.cols) look(c, raw[q]);
-    }
-    for (int c = (li + KC * NT) * 8; c < a.cols; c += NT * 8) {
-      T v[8];
-      load_piece<T, 8>(src, c, a.cols, v);
-      look(c, v);
-    }
-    most = group_all<64>(most, OpMax());
-    if constexpr (NT > 64) {
-      __syncthreads();                                   // the row before has been read
-      if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = most;
-      __syncthreads();
-      most = max(max(red[0], red[1]), max(red[2], red[3]));
-    }
-    // NaN and infinity: a scale of NaN, codes of 0; magnitudes below 2^-100: zeros
-    const bool finite = most < 0x7F800000u;
-    float amax = finite && most >= __float_as_uint(0x1p-100f) ? __uint_as_float(most) : 0.f;
-    const float scale = finite ? amax / 127.f : __builtin_nanf("");
-    const float down = amax >= 0x1p64f ? 0x1p-64f : 1.f; // so that 127 v stays in range
-    amax *= down;
-    const float inv = amax > 0.f ? 127.f / amax : 0.f;
-    auto write = [&](int c, const T* v) {
-      uint32_t w[2] = {0u, 0u};
-      if (amax > 0.f) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          w[i / 4] |= (uint32_t)(code_of(T{}, elem_f(v[i]) * down, inv, amax) & 0xFF) << 8 * (i % 4);
-      }
-      int8_t o[8];
-      __builtin_memcpy(o, w, 8);
-      store_upto<int8_t, 8>(out + c, a.cols - c, o);
-    };
-#pragma unroll
-    for (int q = 0; q < KC; ++q) {
-      const int c = (li + q * NT) * 8;
-      if (c < a.cols) write(c, raw[q]);
-    }
-    for (int c = (li + KC * NT) * 8; c < a.cols; c += NT * 8) {
-      T v[8];
-      load_piece<T, 8>(src, c, a.cols, v);
-      settle_piece<T, 8>(c, a.cols, v);
-      write(c, v);
-    }
-    if (a.row_to_slot) {
-      for (int j = li; j < a.k; j += NT) {
-        const int s = a.row_to_slot[r * a.k + j];
-        if (s >= 0) a.scales[s] = scale;
-      }
-    } else if (li == 0) {
-      a.scales[r] = a.slot_to_row ? a.scales[r] * scale : scale;
-    }
-  }
+template <typename T, int NT, int KC> __global__ __launch_bounds__(256) void k_quant_i8(QuantI8 a) {
+  quant_i8_rows<T, NT, KC, 256>(a, blockIdx.x, gridDim.x);
 }
 
 static void launch_quant(const QuantI8& a, int dtype, hipStream_t st) {
   if (a.rows == 0) return;
   auto go = [&](auto kernel, int rpw) {
+    // a launch holds fewer than 2^32 threads; past that the workgroups take further rows
     const size_t all = ((size_t)a.rows + rpw - 1) / rpw;
-    // slots: one resident round, whatever their capacity
-    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<size_t>(all, a.blocks ? 2048 : 1 << 23)), dim3(256), 0, st, a);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)std::min<size_t>(all, 1 << 23)), dim3(256), 0, st, a);
   };
-  const bool wave = a.cols <= 64 * 8 * 4;
-  if (dtype == MOE_F32) wave ? go(k_quant_i8<float, 64, 4>, 4) : go(k_quant_i8<float, 256, 4>, 1);
+  const bool wave = a.cols <= kI8WaveCols;
+  const bool half = a.cols <= kI8WaveCols / 2;
+  if (half) dtype == MOE_F32 ? go(k_quant_i8<float, 32, 4>, 8) : go(k_quant_i8<uint16_t, 32, 4>, 8);
+  else if (dtype == MOE_F32) wave ? go(k_quant_i8<float, 64, 4>, 4) : go(k_quant_i8<float, 256, 4>, 1);
   else wave ? go(k_quant_i8<uint16_t, 64, 4>, 4) : go(k_quant_i8<uint16_t, 256, 4>, 1);
 }
 int launch_quant_int8_rows(const void* src, int ld, int dtype, int rows, int cols, int8_t* codes, float* scales,
@@ -145,14 +34,7 @@ int launch_quant_int8_rows(const void* src, int ld, int dtype, int rows, int col
   launch_quant(a, dtype, st);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
-// Read no error: they are launches of moe_forward, whose last check sees them all.
-void launch_quant_int8_tokens(const void* x, int T, int d, const int32_t* row_to_slot, int k, int8_t* codes,
-                              float* slot_scale, hipStream_t st) {
-  QuantI8 a{};
-  a.src = x; a.ld = (size_t)d; a.rows = T; a.cols = d; a.codes = codes; a.scales = slot_scale;
-  a.row_to_slot = row_to_slot; a.k = k;
-  launch_quant(a, MOE_BF16, st);
-}
+// Reads no error: it is one of the launches of moe_forward, whose last check sees them all.
 void launch_quant_int8_slots(const void* rows, int slots, int dff, const int32_t* slot_to_row, const int32_t* blocks,
                              int beta, int8_t* codes, float* gates, hipStream_t st) {
   QuantI8 a{};

@@ -108,8 +108,6 @@ int launch_adamw(const moe_adamw_list& l, const moe_adamw_hyper& h, hipStream_t 
 
 int launch_quant_int8_rows(const void* src, int ld, int dtype, int rows, int cols, int8_t* codes, float* scales,
                            hipStream_t st);
-void launch_quant_int8_tokens(const void* x, int T, int d, const int32_t* row_to_slot, int k, int8_t* codes,
-                              float* slot_scale, hipStream_t st);
 void launch_quant_int8_slots(const void* rows, int slots, int dff, const int32_t* slot_to_row, const int32_t* blocks,
                              int beta, int8_t* codes, float* gates, hipStream_t st);
 constexpr int kFewRows = 64;           // of a tile of launch_i8_few
