@@ -2554,9 +2554,12 @@ static void run_forward_stream(const Sizes& z, ExecArgs& a, const int32_t* row_t
   rec(ev, 4, st);
 }
 
-// Where experts have few rows, a 256-row tile of the stream kernels is mostly empty and their items are too few
-// for the chip; sizes off the 256 grid have no others.
-bool i8_few(const Sizes& z) { return !use_stream(z) || (long long)z.T * z.k <= 16ll * z.E; }
+// Where experts have few rows, a 256-row tile of the stream kernels is mostly empty and their items are too few for
+// the chip; where they have more, the rows' codes are what the tiles of few rows read most.  Forward, us, by tiles
+// of few rows and by the stream kernels: 128 experts of 2048 x 768, 4 rows each on average 147 and 164, 6 rows 170
+// and 170, 8 rows 180 and 172; 32 of 7168 x 2048, 4 rows 316 and 324, 6 rows 340 and 337.  (Sizes off the 256 grid
+// have no others.)
+bool i8_few(const Sizes& z) { return !use_stream(z) || (long long)z.T * z.k <= 5ll * z.E; }
 
 static void run_forward_int8(const Sizes& z, ExecArgs& a, const int32_t* row_to_slot, void* y, void* const* ev,
                              hipStream_t st) {

@@ -606,11 +606,11 @@ template <int L> MOE_DEV bool group_any(bool on) {
 }
 constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
 
-// The lane's choices from its scores, each off by `err` at most, the largest smost.  bias: -infinity where
+// The lane's choices from its logits l, the row's largest top, and scores, each off by `err` at most, the largest smost.  bias: -infinity where
 // barred; bmost the largest |bias| of the others.  In LDS: the row's logits and the biases, C places for keys,
 // and a place for every group; gid: the groups of the lane's experts.  Returns whether the choice stays open.
-template <int L, int V>
-MOE_DEV bool choose32(const RouterArgs& a, const float* l, const float* score, float err, float smost, const float* bias,
+template <int L, int V, int SCORE>
+MOE_DEV bool choose32(const RouterArgs& a, const float* l, float top, const float* score, float err, float smost, const float* bias,
                       float bmost, const MOE_LDS float* logits, const MOE_LDS float* sbias, MOE_LDS uint32_t* keys,
                       MOE_LDS uint32_t* worth, const uint32_t* gid, int li, int* where) {
   constexpr int KQ = (kRouterMaxK + L - 1) / L, C = L * V, IB = log2_of(C), UB = 32 - IB < 24 ? 32 - IB : 24;
@@ -626,6 +626,31 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, const float* score, f
     key[i] = ((uint32_t)fmaxf(__builtin_fmaf(v, per, zero), 0.f) << IB | (uint32_t)(C - V - c0)) | (uint32_t)(V - 1 - i);
   }
   bool unsure = !(bmost < 0x1p64f);                      // out of the bounds' range
+  const uint32_t close = far < 0x1p20f ? ((uint32_t)far + 1u) << IB : ~0u - C;
+  auto expert = [&](uint32_t key) { return C - 1 - (int)(key & (C - 1)); };
+  // keys near to each other, but not of an equal logit with an equal bias (which have an equal value, and the
+  // keys' order is the indexes')
+  auto nearby = [&](uint32_t a, uint32_t b) {
+    const int e = expert(a), f = expert(b);
+    return b >= C && a - b <= close && !(logits[e] == logits[f] && sbias[e] == sbias[f]);
+  };
+  // values in 64 bits
+  auto sum64 = [&]() {
+    double sum = SCORE == MOE_SCORE_SOFTMAX ? 0.0 : 1.0;
+    if constexpr (SCORE == MOE_SCORE_SOFTMAX) {
+#pragma unroll 2
+      for (int i = 0; i < V; ++i) sum += score64<SCORE>(logits[c0 + i], top);
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) sum += __shfl_xor(sum, o, 64);
+    }
+    return sum;
+  };
+  auto value64 = [&](uint32_t key, double sum) {
+    const int e = expert(key);
+    double v = score64<SCORE>(logits[e], top);
+    if constexpr (SCORE == MOE_SCORE_SOFTMAX) v /= sum;
+    return key >= C ? v + (double)sbias[e] : -HUGE_VAL;
+  };
   if (top_groups < groups) {
     const int glog = fresh(a.glog), two = fresh(a.two);
     // in units; a second that is not there has the value 0
@@ -633,8 +658,9 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, const float* score, f
       return t.a >= C ? (t.a >> IB) + (two ? (t.b >= C ? t.b >> IB : (uint32_t)zero) : 0u) : 0u;
     };
     wave_lds_order();
+    TwoBest t{0u, 0u};
     if (glog >= 0) {                                     // a group is 2^glog whole lanes
-      TwoBest t{key[0], 0u};
+      t = {key[0], 0u};
 #pragma unroll
       for (int i = 1; i < V; ++i) t.join(key[i], 0u);
       t = lanes_two_best(t, glog);
@@ -676,8 +702,33 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, const float* score, f
     least = group_all<L>(least, OpMin());
     most = group_all<L>(most, OpMax());
     // a group's value has two values' errors; equals are all open
-    unsure |= __popc(open[0]) + __popc(open[1]) != top_groups;
-    unsure |= most > 0u && (float)(least - most) <= 2.f * far + 1.f;
+    bool doubt = __popc(open[0]) + __popc(open[1]) != top_groups || (most > 0u && (float)(least - most) <= 2.f * far + 1.f);
+    if (doubt && !unsure && glog >= 0) {                 // the whole group of lanes
+      // Rare: the groups' values in 64 bits, as far as it is sure which members make them.
+      uint32_t after = 0u;
+      const uint32_t end = two ? t.b : t.a;
+#pragma unroll
+      for (int i = 0; i < V; ++i) after = max(after, key[i] < end ? key[i] : 0u);
+      after = lanes_two_best({after, 0u}, glog).a;
+      if (!group_any<L>(end >= C && nearby(end, after))) {
+        const double sum = sum64();
+        double w = value64(t.a, sum);
+        if (two && t.b >= C) w += value64(t.b, sum);
+        MOE_LDS double* worth64 = (MOE_LDS double*)keys;
+        wave_lds_order();
+        worth64[li >> glog] = w;
+        wave_lds_order();
+        const double own = worth64[min(li, groups - 1)];               // a group has a lane at least
+        int above = 0;
+#pragma unroll 4
+        for (int j = 0; j < groups; ++j) above += worth64[j] > own || (worth64[j] == own && j < li);
+        const bool in = li < groups && above < top_groups;
+        open[0] = group_all<L>(in && li < 32 ? 1u << li : 0u, OpOr());
+        open[1] = group_all<L>(in && li >= 32 ? 1u << (li & 31) : 0u, OpOr());
+        doubt = false;
+      }
+    }
+    unsure |= doubt;
     if (glog >= 0) {
       const int m = li >> glog;
       const bool in = (m & 32 ? open[1] : open[0]) >> (m & 31) & 1u;
@@ -691,11 +742,9 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, const float* score, f
       }
     }
   }
-  const uint32_t close = far < 0x1p20f ? ((uint32_t)far + 1u) << IB : ~0u - C;
 #pragma unroll
   for (int q = 0; q < KQ; ++q) where[q] = -1;
   bool near = false;
-  auto expert = [&](uint32_t key) { return C - 1 - (int)(key & (C - 1)); };
   if (k <= 8) {
     // Lists of the lanes' eight largest, merged over the lanes: 32 instructions a step.  (A maximum over the
     // lanes for each place: 40.)
@@ -730,9 +779,31 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, const float* score, f
     next = (li & 7) == 7 ? ninth : next;
     const bool on = li < k && mine >= C;
     where[0] = on ? expert(mine) : -1;
-    // (an equal logit with an equal bias has an equal value, and the keys' order is the indexes')
-    const int e = expert(mine), f = expert(next);
-    near = on && next >= C && mine - next <= close && !(logits[e] == logits[f] && sbias[e] == sbias[f]);
+    near = on && nearby(mine, next);
+    if (!unsure && group_any<L>(near)) {                 // the whole group
+      // Rare: the list's values in 64 bits, a lane each, as far as none behind it is near to the last place's.
+      const int many = L >= 16 && k == 8 ? 9 : 8;
+      const uint32_t held = li < 8 ? mine : li == 8 && many == 9 ? ninth : 0u, end = many == 9 ? ninth : list[7];
+      uint32_t behind = 0u;
+#pragma unroll
+      for (int i = 0; i < V; ++i) behind = max(behind, key[i] < end ? key[i] : 0u);
+      behind = group_all<L>(behind, OpMax());
+      const uint32_t last = group_all<L>(on ? mine : ~0u, OpMin());
+      if (behind >= C && last - behind <= close) return true;
+      const int own = expert(held);
+      const double v = value64(held, sum64());
+      int rank = 0;
+#pragma unroll 3
+      for (int i = 0; i < many; ++i) {
+        const double o = __shfl(v, i, L);
+        rank += o > v || (o == v && __shfl(own, i, L) < own);
+      }
+      wave_lds_order();
+      if (li < many) worth[rank] = held >= C ? (uint32_t)own : ~0u;
+      wave_lds_order();
+      where[0] = li < k ? (int)worth[li] : -1;
+      near = false;
+    }
   } else {
     uint32_t lane[V];
 #pragma unroll
@@ -884,7 +955,7 @@ __global__ __launch_bounds__(kRouterThreads, kChoiceWaves) void k_choice(RouterA
       MOE_LDS float* row = (MOE_LDS float*)rows[g];
       row_to_lds<V>(v, row, li);
       int where[KQ];
-      if (choose32<L, V>(a, v, w, err, smost, bias, bmost, row, (MOE_LDS float*)sbias, (MOE_LDS uint32_t*)row + C,
+      if (choose32<L, V, SCORE>(a, v, sc_.top, w, err, smost, bias, bmost, row, (MOE_LDS float*)sbias, (MOE_LDS uint32_t*)row + C,
                          (MOE_LDS uint32_t*)worths[g], gid, li, where))
         open |= 1u << r;
       else
