@@ -142,7 +142,8 @@ template <int SCORE> struct Score {
 
 // The logarithm of a score, up to the softmax's sum.
 template <int SCORE> MOE_DEV float log_score(float l) {
-  return SCORE == MOE_SCORE_SOFTMAX ? l : fminf(l, 0.f) - log1pf(exp_of(-fabsf(l)));
+  // log2 of a number from 1 to 2: off by 2^-24, and so is the share
+  return SCORE == MOE_SCORE_SOFTMAX ? l : fminf(l, 0.f) - __builtin_amdgcn_logf(1.f + exp_of(-fabsf(l))) * 0.69314718f;
 }
 
 template <int L, int V> MOE_DEV float row_top(const float* v) {
@@ -1185,7 +1186,9 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
       Q = group_all<L>(Q, OpAdd());
       pg = group_all<L>(pg, OpAdd());
       float hq = a.renorm ? (Q > 0.f ? H / Q : 0.f) : (SCORE == MOE_SCORE_SOFTMAX ? H : 0.f);
-      if (a.renorm && Q < kFewShares && H != 0.f) {      // the whole group: shares of next to nothing
+      if (__any(a.renorm && Q < kFewShares && H != 0.f)) {             // rare, whole waves: shares of next to nothing
+        asm volatile("");                                // keeps the branch
+        const bool few = Q < kFewShares && H != 0.f;
         float most = -INFINITY, all = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) most = fmaxf(most, flag[i] ? log_score<SCORE>(v[i]) : -INFINITY);
@@ -1194,8 +1197,8 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
         for (int i = 0; i < V; ++i) all += flag[i] ? exp_of(log_score<SCORE>(v[i]) - most) : 0.f;
         all = group_all<L>(all, OpAdd());
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] -= flag[i] && all > 0.f ? H / all * exp_of(log_score<SCORE>(v[i]) - most) : 0.f;
-        hq = 0.f;
+        for (int i = 0; i < V; ++i) d[i] -= few && flag[i] && all > 0.f ? H / all * exp_of(log_score<SCORE>(v[i]) - most) : 0.f;
+        hq = few ? 0.f : hq;
       }
       const float rest = a.renorm ? 0.f : hq;            // of the experts not chosen
       float zs = 0.f;
