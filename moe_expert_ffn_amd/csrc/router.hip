@@ -1174,6 +1174,7 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
     T* out = (T*)a.dlogits + t * a.ld_out;
     T o[V];
     float x[V];
+    bool few = false;                                    // the chosen shares are next to nothing
     if (row_live(sc.top, sum)) {                         // the whole group
       const float inv = inverse(sum);
       float Q = 0.f, pg = 0.f;
@@ -1185,21 +1186,8 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
       }
       Q = group_all<L>(Q, OpAdd());
       pg = group_all<L>(pg, OpAdd());
-      float hq = a.renorm ? (Q > 0.f ? H / Q : 0.f) : (SCORE == MOE_SCORE_SOFTMAX ? H : 0.f);
-      if (__any(a.renorm && Q < kFewShares && H != 0.f)) {             // rare, whole waves: shares of next to nothing
-        asm volatile("");                                // keeps the branch
-        const bool few = Q < kFewShares && H != 0.f;
-        float most = -INFINITY, all = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) most = fmaxf(most, flag[i] ? log_score<SCORE>(v[i]) : -INFINITY);
-        most = group_all<L>(most, OpMaxF());
-#pragma unroll
-        for (int i = 0; i < V; ++i) all += flag[i] ? exp_of(log_score<SCORE>(v[i]) - most) : 0.f;
-        all = group_all<L>(all, OpAdd());
-#pragma unroll
-        for (int i = 0; i < V; ++i) d[i] -= few && flag[i] && all > 0.f ? H / all * exp_of(log_score<SCORE>(v[i]) - most) : 0.f;
-        hq = few ? 0.f : hq;
-      }
+      const float hq = a.renorm ? (Q >= kFewShares ? H / Q : 0.f) : (SCORE == MOE_SCORE_SOFTMAX ? H : 0.f);
+      few = a.renorm && Q < kFewShares && H != 0.f;
       const float rest = a.renorm ? 0.f : hq;            // of the experts not chosen
       float zs = 0.f;
       if (zmul != 0.f) {
@@ -1223,6 +1211,25 @@ __global__ __launch_bounds__(kRouterThreads) void k_router_bwd(RouterArgs a) {
     }
     to_elems<V>(x, o);
     store_upto<T, V>(out + c0, a.E - c0, o);
+    if (few) {                                           // rare, the whole group: again, with shares from their logarithms
+      asm volatile("");
+      float most = -INFINITY, all = 0.f, ls[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        ls[i] = flag[i] ? log_score<SCORE>(v[i]) : -INFINITY;
+        most = fmaxf(most, ls[i]);
+      }
+      most = group_all<L>(most, OpMaxF());
+#pragma unroll
+      for (int i = 0; i < V; ++i) all += flag[i] ? exp_of(ls[i] - most) : 0.f;
+      all = group_all<L>(all, OpAdd());
+      const float each = H / all;                          // a choice at least: H is not 0
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (flag[i]) x[i] -= each * exp_of(ls[i] - most) * (SCORE == MOE_SCORE_SIGMOID ? away[i] : 1.f);
+      to_elems<V>(x, o);
+      store_upto<T, V>(out + c0, a.E - c0, o);
+    }
   }
 }
 
