@@ -127,7 +127,7 @@ typedef enum { MOE_PLAN_FWD = 0, MOE_PLAN_BWD = 1, MOE_PLAN_QUOTA = 2 } moe_plan
  *   w1_scale [E][2*d_ff/128][d/128], w2_scale [E][d/128][d_ff/128];
  * or MOE_INT8 (codes of -127..127, act MOE_BF16; forward only, to answer with), with one
  * fp32 scale per weight row (moe_quantize_int8_rows makes both):
- *   w1_scale [E][2*d_ff], w2_scale [E][d].
+ *   w1_scale [E][2*d_ff], w2_scale [E][d];  w1 and w2 lie at multiples of 16 bytes.
  * Requires d % 128 == 0 and d_ff % 64 == 0 (fp8: d_ff % 128 == 0). */
 typedef struct {
   int E, d, d_ff;
@@ -724,6 +724,7 @@ size_t moe_grad_workspace_size(int tensors);
 /* Writes the list's table into ws on `stream`; *out (host) is what the calls below take.  Tensors may
  * share memory (each counts in the norm) where they are not scaled in place.  The norm keeps its partial
  * sums in ws: calls on one list must not overlap in time.
+ * A call on another stream has to be ordered after it by the caller.
  * Errors: MOE_ERR_ARG for a count outside [0, MOE_GRAD_MAX_TENSORS], n < 0, an unknown dtype or a null
  *   or misaligned pointer of a tensor with n > 0; MOE_ERR_UNSUPPORTED for a list of 2^24 items of 8192
  *   elements and more; MOE_ERR_WORKSPACE. */

@@ -44,7 +44,10 @@ int check_layer(const moe_layer* L, bool backward) {
   if (!f32 && !bf && !f8 && !i8)
     return L->act_dtype > MOE_BF16 || L->w_dtype > MOE_INT8 ? MOE_ERR_ARG : MOE_ERR_UNSUPPORTED;
   if (i8) {
-    if (!L->w1_scale || !L->w2_scale) return MOE_ERR_ARG;
+    // read in pieces of 16 bytes, straight into LDS: a byte's address need not be one
+    if (!L->w1_scale || !L->w2_scale || (((uintptr_t)L->w1 | (uintptr_t)L->w2) & 15) ||
+        (((uintptr_t)L->w1_scale | (uintptr_t)L->w2_scale) & 3))
+      return MOE_ERR_ARG;
     if (backward || L->d > kI8MaxK || L->d_ff > kI8MaxK) return MOE_ERR_UNSUPPORTED;
   }
   if (f8) {

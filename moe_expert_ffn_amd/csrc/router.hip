@@ -800,7 +800,9 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, float top, const floa
         rank += o > v || (o == v && __shfl(own, i, L) < own);
       }
       wave_lds_order();
-      if (li < many) worth[rank] = held >= C ? (uint32_t)own : ~0u;
+      if (li < many) worth[li] = ~0u;                    // places that nothing is left for
+      wave_lds_order();
+      if (li < many && held >= C) worth[rank] = (uint32_t)own;
       wave_lds_order();
       where[0] = li < k ? (int)worth[li] : -1;
       near = false;

@@ -110,6 +110,51 @@ def test_values_that_32_bits_cannot_tell_apart(E, groups, top, score):
                "top2" if seed % 4 < 2 else "max")
 
 
+@pytest.mark.parametrize("E", [8, 64, 100, 256, 600])
+@pytest.mark.parametrize("left", [1, 2, 3, 7, 8])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_values_next_to_each_other_with_few_to_choose(E, left, score):
+    """Fewer experts left than places, their values within 32 bits' rounding: the other places are -1."""
+    for seed in range(6):
+        rng = np.random.default_rng(100 * left + seed)
+        row = np.full(E, -np.inf, dtype=np.float32)
+        at = rng.choice(E, left, replace=False)
+        row[at] = rng.standard_normal(left).astype(np.float32)
+        l = row[at].astype(np.float64)
+        s = 1 / (1 + np.exp(-l)) if score == "sigmoid" else np.exp(l - l.max()) / np.exp(l - l.max()).sum()
+        bias = np.zeros(E, dtype=np.float32)
+        bias[at] = (1.25 - s).astype(np.float32)
+        logits = torch.from_numpy(np.stack([row, row + np.float32(0.0), row])).to(DEV)
+        groups = 1 if E % 4 else 4
+        _check(logits, min(E, 8), score, True, torch.from_numpy(bias).to(DEV))
+        _check(logits, min(E // groups, 8), score, False, torch.from_numpy(bias).to(DEV), groups, max(1, groups - 1))
+
+
+@pytest.mark.parametrize("E,groups,top", [(64, 8, 4), (64, 2, 1), (128, 4, 2), (256, 8, 4), (60, 4, 2), (512, 16, 5), (1024, 8, 3)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_that_32_bits_cannot_tell_apart(E, groups, top, score):
+    """Groups whose values, of two members or one, lie within 32 bits' rounding of each other, members that do not;
+    and with a third member next to the second."""
+    for seed in range(16):
+        rng = np.random.default_rng(seed)
+        size = E // groups
+        row = rng.standard_normal(E).astype(np.float32)
+        l = row.astype(np.float64)
+        s = 1 / (1 + np.exp(-l)) if score == "sigmoid" else np.exp(l - l.max()) / np.exp(l - l.max()).sum()
+        bias = (-3 + 0.5 * rng.random(E)).astype(np.float32)
+        rank = "top2" if seed % 2 else "max"
+        for g in range(groups):
+            a, b, c = g * size + rng.choice(size, 3, replace=False)
+            first = 1.7 + 0.1 * rng.random() if rank == "top2" else 2.0
+            bias[a] = np.float32(first - s[a])
+            second = 3.0 - (s[a] + float(bias[a])) if rank == "top2" else 1.0 + 0.3 * rng.random()
+            bias[b] = np.float32(second - s[b])
+            if seed % 4 >= 2 and g % 2:
+                bias[c] = np.float32(second - s[c])
+        _check(torch.from_numpy(np.stack([row] * 3)).to(DEV), min(8, top * size), score, True, torch.from_numpy(bias).to(DEV),
+               groups, top, rank)
+
+
 @pytest.mark.parametrize("E,groups,top", [(8, 2, 1), (100, 4, 2), (256, 8, 4), (700, 7, 3)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("dtype", [F32, BF16])

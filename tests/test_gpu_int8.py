@@ -128,7 +128,7 @@ class Layer8:
 LAYERS = [(1, 1, 1, 128, 64, 16, 1), (1, 8, 16, 256, 256, 16, 1), (3, 2, 5, 384, 192, 1, 2), (17, 4, 8, 256, 64, 16, 4),
           (64, 8, 32, 512, 256, 16, 1), (150, 3, 6, 384, 192, 32, 2), (300, 2, 4, 128, 320, 50, 8), (333, 3, 10, 384, 192, 300, 2),
           (40, 2, 2, 512, 512, 128, 1), (700, 4, 8, 512, 256, 128, 8), (600, 2, 4, 256, 512, 16, 4), (900, 3, 5, 768, 256, 300, 2),
-          (130, 1, 1, 256, 256, 128, 1), (257, 2, 3, 1024, 768, 50, 1)]
+          (130, 1, 1, 256, 256, 128, 1), (257, 2, 3, 1024, 768, 50, 1), (3, 1, 2, 8320, 64, 16, 1), (20, 2, 3, 2176, 2112, 16, 2)]
 
 
 @pytest.mark.parametrize("T,k,E,d,f,beta,P", LAYERS)

@@ -38,6 +38,10 @@ def test_layer_refusals():
     assert _forward(_layer(d=192)) == UNSUP and _forward(_layer(f=96)) == UNSUP and _forward(_layer(E=513)) == UNSUP
     assert _forward(_layer(d=131072 + 128, f=64)) == UNSUP and _forward(_layer(f=131072 + 64, d=128)) == UNSUP
     assert _forward(_layer(), ws=None) == WS and _forward(_layer(), n=4096) == WS
+    for i, at in ((5, 264), (6, 264), (7, 258), (8, 257)):                       # weights off 16 bytes, scales off 4
+        f = [8, 256, 128, B.MOE_BF16, B.MOE_INT8, 256, 256, 256, 256]
+        f[i] = at
+        assert _forward(B.Layer(*f)) == ARG, i
     L = _layer()
     assert B.load().moe_backward(ctypes.byref(L), P, P, P, P, P, 40, 2, 16, 2, 1, *([P] * 9), P, P, 1 << 40, 0, None, None,
                                  None) == UNSUP
