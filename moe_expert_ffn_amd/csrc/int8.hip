@@ -49,7 +49,8 @@ void launch_quant_int8_slots(const void* rows, int slots, int dff, const int32_t
 // v_mfma_i32_16x16x64_i8, 16 rows of 64 bytes a load; the rows' codes, which few items share, come out of
 // the caches the same way.  The waves' sums are joined in LDS.  Lane l of a fragment holds row l % 16, codes
 // 16 (l / 16) to + 15 of the chunk; with the weights first, lane l of a product holds weight rows 4 (l / 16)
-// to + 3 of row l % 16.
+// to + 3 of row l % 16.  Bound by HBM: 512 rows over 125 experts of 2048 x 768, FC1 393 MB of weights in 69 us
+// (5.7 TB/s), FC2 197 MB in 45; one token, 25 MB of FC1 in 7 us, the latency of a launch, a read and the join.
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 struct FewI8 {
   const int8_t* codes;       // FC1: [T][K] by token, FC2: [slots][K]
