@@ -108,8 +108,8 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_INT8 = 3 } moe_d
  * after the workgroup's last item and all its memory operations).  Workgroup g
  * belongs to worker (g % 8) * P / 8.  Written by the persistent 256 x 256
  * stream kernels (bf16 activations, d and d_ff multiples of 256, operands
- * below 2 GiB); other shapes and workgroups beyond the launch leave their
- * entries untouched.  Writing it changes no result. */
+ * below 2 GiB); other shapes, int8 layers of few rows and workgroups beyond the
+ * launch leave their entries untouched.  Writing it changes no result. */
 #define MOE_TIMELINE_MAX_WG 1024
 enum { MOE_TL_FC1 = 0, MOE_TL_FC2 = 1, MOE_TL_DA = 2, MOE_TL_DX = 3, MOE_TL_DW = 4,
        MOE_TL_PHASES = 5 };
@@ -745,7 +745,9 @@ int moe_grad_scale(const moe_grad_list* list, const float* scale, void* stream);
  * in [-127, 127].  A row whose magnitudes are all below 2^-100 is stored as zeros with a scale of 0; one with
  * NaN or an infinity gets a scale of NaN and codes of 0.
  *   src [rows][cols], rows ld apart, MOE_F32 or MOE_BF16; codes [rows][cols]; scales [rows].
- * Errors: MOE_ERR_ARG for rows < 0, cols < 1, ld < cols, an unknown dtype or a null pointer. */
+ *   The three share no memory (ld's gaps count as src's).
+ * Errors: MOE_ERR_ARG for rows < 0, cols < 1, ld < cols, an unknown dtype, a null pointer or shared memory;
+ *   MOE_ERR_UNSUPPORTED for cols > 2^30. */
 int moe_quantize_int8_rows(const void* src, int ld, int dtype, int rows, int cols, int8_t* codes, float* scales,
                            void* stream);
 

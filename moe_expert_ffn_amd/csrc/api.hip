@@ -25,6 +25,14 @@ bool ws_ok(const void* ws, size_t have, size_t need) {
   return have >= need;
 }
 
+struct Extent {
+  const void* at;
+  size_t bytes;
+  bool meets(const Extent& o) const {
+    return (uintptr_t)at < (uintptr_t)o.at + o.bytes && (uintptr_t)o.at < (uintptr_t)at + bytes;
+  }
+};
+
 bool dtype_ok(int d) { return d == MOE_F32 || d == MOE_BF16; }
 
 // 127 * 127 * K stays below 2^31
@@ -228,6 +236,12 @@ int moe_quantize_int8_rows(const void* src, int ld, int dtype, int rows, int col
                            void* stream) {
   if (rows < 0 || cols < 1 || ld < cols || !dtype_ok(dtype) || (rows > 0 && (!src || !codes || !scales)))
     return MOE_ERR_ARG;
+  if (cols > (1 << 30)) return MOE_ERR_UNSUPPORTED;        // a lane's next piece is counted in 32 bits
+  if (rows == 0) return MOE_OK;
+  const size_t eb = dtype == MOE_F32 ? 4 : 2;
+  const Extent all[3] = {{src, ((size_t)(rows - 1) * ld + cols) * eb}, {codes, (size_t)rows * cols},
+                         {scales, (size_t)rows * sizeof(float)}};
+  if (all[0].meets(all[1]) || all[0].meets(all[2]) || all[1].meets(all[2])) return MOE_ERR_ARG;
   return launch_quant_int8_rows(src, ld, dtype, rows, cols, codes, scales, (hipStream_t)stream);
 }
 

@@ -22,6 +22,18 @@ def test_quantizer_refusals():
         B.quantize_int8_rows(x, torch.zeros(4, 8, dtype=torch.int8), torch.zeros(4))
 
 
+def test_quantizer_refuses_shared_memory_and_rows_past_32_bits():
+    """Rows are taken in any order: codes over a row that is still to be read would be its own input."""
+    def q(src, codes, scales, cols=64, ld=64, dt=B.MOE_BF16):
+        return B.load().moe_quantize_int8_rows(ctypes.c_void_p(src), ld, dt, 4, cols, ctypes.c_void_p(codes),
+                                               ctypes.c_void_p(scales), None)
+    at = 1 << 20                                  # src is 4 rows of 128 bytes there
+    assert q(at, at, 1 << 22) == ARG and q(at, at + 511, 1 << 22) == ARG and q(at, at - 255, 1 << 22) == ARG
+    assert q(at, 1 << 22, at + 508) == ARG and q(at, 1 << 22, at - 12) == ARG
+    assert q(at, 1 << 22, (1 << 22) + 252) == ARG and q(at, 1 << 22, (1 << 22) - 12) == ARG
+    assert q(at, 1 << 45, 1 << 46, cols=(1 << 30) + 1, ld=(1 << 30) + 1) == UNSUP
+
+
 def _layer(E=8, d=256, f=128, act=B.MOE_BF16, s1=256, s2=256):
     return B.Layer(E, d, f, act, B.MOE_INT8, 256, 256, s1, s2)
 

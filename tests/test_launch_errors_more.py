@@ -26,7 +26,8 @@ calls = {
     "choice": (lambda: lib.moe_router_forward_choice(ctypes.byref(R), ctypes.byref(C), P, 64, None, 500, P, P, P, P, P, P, P, P,
                                                      1 << 30, None), 2),
     "bias": (lambda: lib.moe_router_bias_update(P, 64, 0.1, P, None), 1),
-    "rows": (lambda: lib.moe_quantize_int8_rows(P, 64, 0, 5, 64, P, P, None), 1),
+    "rows": (lambda: lib.moe_quantize_int8_rows(P, 64, 0, 5, 64, ctypes.c_void_p(1 << 16),
+                                                ctypes.c_void_p(1 << 20), None), 1),
     "prepare": (lambda: lib.moe_grad_prepare(many, 200, ctypes.byref(B.GradList()), P, 1 << 20, None), 3),
     "norm": (lambda: lib.moe_grad_norm(ctypes.byref(G), ctypes.byref(B.Clip(1.0, 1.0, None)), P, P, P, None), 1),
     "scale": (lambda: lib.moe_grad_scale(ctypes.byref(G), P, None), 1)}
