@@ -618,11 +618,20 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, float top, const floa
   bool unsure = !(bmost < 0x1p64f);                      // out of the bounds' range
   const uint32_t close = far < 0x1p20f ? ((uint32_t)far + 1u) << IB : ~0u - C;
   auto expert = [&](uint32_t key) { return C - 1 - (int)(key & (C - 1)); };
-  // keys near to each other, but not of an equal logit with an equal bias (which have an equal value, and the
-  // keys' order is the indexes')
-  auto nearby = [&](uint32_t a, uint32_t b) {
+  auto nearby = [&](uint32_t a, uint32_t b) { return b >= C && a - b <= close; };
+  // An equal logit with an equal bias: an equal value, and the keys' order is the indexes'.  It says nothing of
+  // the keys behind it, which may be near to both and larger.
+  auto equal = [&](uint32_t a, uint32_t b) {
     const int e = expert(a), f = expert(b);
-    return b >= C && a - b <= close && !(logits[e] == logits[f] && sbias[e] == sbias[f]);
+    return logits[e] == logits[f] && sbias[e] == sbias[f];
+  };
+  // the largest of the lane's keys below `end` that is not its equal (by LDS: l and bias kept for it would be
+  // registers of every row's)
+  auto unlike = [&](uint32_t end) {
+    uint32_t most = 0u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) most = max(most, key[i] < end && !equal(key[i], end) ? key[i] : 0u);
+    return most;
   };
   // values in 64 bits
   auto sum64 = [&]() {
@@ -695,11 +704,7 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, float top, const floa
     bool doubt = __popc(open[0]) + __popc(open[1]) != top_groups || (most > 0u && (float)(least - most) <= 2.f * far + 1.f);
     if (doubt && !unsure && glog >= 0) {                 // the whole group of lanes
       // Rare: the groups' values in 64 bits, as far as it is sure which members make them.
-      uint32_t after = 0u;
-      const uint32_t end = two ? t.b : t.a;
-#pragma unroll
-      for (int i = 0; i < V; ++i) after = max(after, key[i] < end ? key[i] : 0u);
-      after = lanes_two_best({after, 0u}, glog).a;
+      const uint32_t end = two ? t.b : t.a, after = lanes_two_best({unlike(end), 0u}, glog).a;
       if (!group_any<L>(end >= C && nearby(end, after))) {
         const double sum = sum64();
         double w = value64(t.a, sum);
@@ -770,6 +775,12 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, float top, const floa
     const bool on = li < k && mine >= C;
     where[0] = on ? expert(mine) : -1;
     near = on && nearby(mine, next);
+    const bool same = near && equal(mine, next);
+    near = near && !same;
+    if (group_any<L>(same && li == k - 1)) {             // the whole group: what comes behind the last place's equals
+      const uint32_t last = group_all<L>(on ? mine : ~0u, OpMin());
+      near |= nearby(last, group_all<L>(unlike(last), OpMax()));
+    }
     if (!unsure && group_any<L>(near)) {                 // the whole group
       // Rare: the list's values in 64 bits, a lane each, as far as none behind it is near to the last place's.
       const int many = L >= 16 && k == 8 ? 9 : 8;
@@ -779,7 +790,7 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, float top, const floa
       for (int i = 0; i < V; ++i) behind = max(behind, key[i] < end ? key[i] : 0u);
       behind = group_all<L>(behind, OpMax());
       const uint32_t last = group_all<L>(on ? mine : ~0u, OpMin());
-      if (behind >= C && last - behind <= close) return true;
+      if (nearby(last, behind)) return true;
       const int own = expert(held);
       const double v = value64(held, sum64());
       int rank = 0;
