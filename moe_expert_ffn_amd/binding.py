@@ -713,10 +713,11 @@ def _router_args(router, logits, mask):
 
 def router_forward(router: Router, logits, out: dict, ws, status, mask=None, choice=None):
     """Routes logits [T][E] into out (alloc_router): ids, gates, counts, prob_sum, live, losses.  choice
-    (make_choice): by values instead of logits."""
-    st = _here(logits, mask, ws, status, *out.values())
+    (make_choice, for a router of as many experts): by values instead of logits."""
     if choice is not None and choice.tensor is not None:
+        _vector(choice.tensor, router.E, torch.float32, "bias")
         _here(choice.tensor)
+    st = _here(logits, mask, ws, status, *out.values())
     T, ld, _ = _router_args(router, logits, mask)
     _vector(out["topk_ids"], T * router.k, torch.int32, "topk_ids")
     _vector(out["gates"], T * router.k, torch.float32, "gates")
