@@ -8,7 +8,9 @@ library must have been built (``python moe_expert_ffn_amd/build.py`` or
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
+from bisect import bisect_left
 
 import torch
 
@@ -972,6 +974,14 @@ class PreparedGrads:
 
     def __init__(self, c_list, ws, keep):
         self.list, self.ws, self.keep = c_list, ws, keep
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in (*keep, ws) if t.numel())
+        self.begins = [b for b, _ in spans]
+        self.ends = list(itertools.accumulate((e for _, e in spans), max))    # the furthest of those up to each
+
+    def holds(self, at):
+        """Whether the 4 bytes at an address lie in a gradient or the workspace, or a part of them."""
+        i = bisect_left(self.begins, at + 4)
+        return i > 0 and self.ends[i - 1] > at
 
 
 def make_grads(grads) -> PreparedGrads:
@@ -1014,10 +1024,13 @@ def grad_norm(prepared: PreparedGrads, max_norm, norm, scale, status, mult=1.0):
 
 
 def grad_scale(prepared: PreparedGrads, scale):
-    """Every gradient of the list times scale [1], in place."""
+    """Every gradient of the list times scale [1], which lies in none of them, in place."""
+    at = scale.data_ptr()
+    if prepared.holds(at):
+        raise MoeError("scale: lies in the list's memory")
     st = _here(prepared.ws, scale)
     _vector(scale, 1, torch.float32, "scale")
-    _check(load().moe_grad_scale(ctypes.byref(prepared.list), _at(scale), st))
+    _check(load().moe_grad_scale(ctypes.byref(prepared.list), at, st))
 
 
 class Events:
