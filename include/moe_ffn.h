@@ -736,8 +736,9 @@ int moe_grad_prepare(const moe_grad_tensor* tensors, int count, moe_grad_list* o
 int moe_grad_norm(const moe_grad_list* list, const moe_clip* clip, float* norm, float* scale,
                   int32_t* status_dev, void* stream);
 
-/* Every element of the list times *scale (device), rounded to nearest; untouched where it is 1.  *scale lies in
- * no tensor of the list: it is read while they are written.
+/* Every element of the list times *scale (device), a product in fp32, rounded to nearest, and again to bf16 where
+ * the tensor is; untouched where *scale is 1.  *scale lies in no tensor of the list: it is read while they are
+ * written.
  * Errors: MOE_ERR_ARG for a null pointer or a list whose tensors share memory. */
 int moe_grad_scale(const moe_grad_list* list, const float* scale, void* stream);
 

@@ -154,8 +154,9 @@ __global__ __launch_bounds__(kGradThreads) void k_grad_norm(GradArgs a) {
   *a.scale = (float)(norm <= a.max_norm ? mult : mult * (a.max_norm / norm));
 }
 
-// g = g * scale, a workgroup an item; nothing is read or written where the scale is 1.  25M bf16 elements,
-// 100 MB, in 16 us out of the caches that the norm has filled.
+// g = g * scale, a workgroup an item; nothing is read or written where the scale is 1.  A bf16 element is the fp32
+// product rounded again, as the plain product of a bf16 tensor and an fp32 scale is: half a step and 2^-24.
+// 25M bf16 elements, 100 MB, in 16 us out of the caches that the norm has filled.
 template <typename T> MOE_DEV void scale_item(T* g, int n, float scale) {
   constexpr int N = 16 / sizeof(T), R = kGradItem / (kGradThreads * N);
   const int tid = threadIdx.x;
