@@ -244,15 +244,19 @@ class BlockRunner(LayerRunner):
         return self.optimizer
 
     def optimizer_step(self, lr, step, max_norm=None, grad_scale=None, **hyper):
-        """One AdamW step (binding.adamw's arguments) on the block's weights, in place.  max_norm: the
-        gradients, times grad_scale (a number or a tensor), are first scaled down to this norm where theirs,
-        which self.grad_norm receives, is above it."""
+        """One AdamW step (binding.adamw's arguments) on the block's weights, in place.  The gradients are
+        taken times grad_scale, a number or a tensor.  max_norm: they are then scaled down to this norm where
+        theirs, which self.grad_norm receives, is above it."""
         if self.optimizer is None:
             raise B.MoeError("make_optimizer first")
         if max_norm is not None:
             B.grad_norm(self.grads, max_norm, self.grad_norm, self.grad_scale, self.status,
                         1.0 if grad_scale is None else grad_scale)
             grad_scale = self.grad_scale
+        elif grad_scale is not None and not isinstance(grad_scale, torch.Tensor):
+            if not abs(grad_scale) <= torch.finfo(torch.float32).max:
+                raise B.MoeError(f"grad_scale={grad_scale} is not finite in fp32")
+            grad_scale = self.grad_scale.fill_(grad_scale)
         B.adamw(self.optimizer, lr, step=step, grad_scale=grad_scale, **hyper)
 
     def update_bias(self, rate):
