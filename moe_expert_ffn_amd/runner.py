@@ -168,6 +168,7 @@ class BlockRunner(LayerRunner):
         self.logits = torch.empty((T, self.E), **rows)
         self.rstd_in, self.rstd_out = torch.empty(T, **f32), torch.empty(T, **f32)
         self.optimizer = self.x = None
+        self.has_routed = False
         if self.with_backward:
             self.norm_ws = B.norm_workspace(T, d, dev)
             self.dy, self.dn = torch.empty((T, d), **rows), torch.empty((T, d), **rows)
@@ -190,6 +191,7 @@ class BlockRunner(LayerRunner):
         B.norm_in(x, self.w_in, self.eps, self.n, self.rstd_in, mask=mask)
         torch.mm(self.n, self.w_router.t(), out=self.logits)
         r = B.router_forward(self.router, self.logits, self.routed, self.router_ws, self.status, mask, self.choice)
+        self.has_routed = True
         self.route(r["topk_ids"])
         if self.with_backward:
             self.plan_bwd_async()
@@ -263,4 +265,6 @@ class BlockRunner(LayerRunner):
         """The balancing step of the router's bias by the last routing's counts, in place."""
         if self.choice is None or self.choice.tensor is None:
             raise B.MoeError("the runner's router has no bias")
+        if not self.has_routed:
+            raise B.MoeError("update_bias takes the counts of a block_forward")
         B.router_bias_update(self.choice.tensor, self.routed["counts"], rate)
