@@ -625,12 +625,12 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, float top, const floa
     const int e = expert(a), f = expert(b);
     return logits[e] == logits[f] && sbias[e] == sbias[f];
   };
-  // the largest of the lane's keys below `end` that is not its equal (by LDS: l and bias kept for it would be
-  // registers of every row's)
-  auto unlike = [&](uint32_t end) {
+  // the largest of the lane's keys below `end` that is not its equal, or any (by LDS: l and bias kept for it
+  // would be registers of every row's)
+  auto behind_of = [&](uint32_t end, bool any) {
     uint32_t most = 0u;
 #pragma unroll
-    for (int i = 0; i < V; ++i) most = max(most, key[i] < end && !equal(key[i], end) ? key[i] : 0u);
+    for (int i = 0; i < V; ++i) most = max(most, key[i] < end && (any || !equal(key[i], end)) ? key[i] : 0u);
     return most;
   };
   // values in 64 bits
@@ -704,7 +704,10 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, float top, const floa
     bool doubt = __popc(open[0]) + __popc(open[1]) != top_groups || (most > 0u && (float)(least - most) <= 2.f * far + 1.f);
     if (doubt && !unsure && glog >= 0) {                 // the whole group of lanes
       // Rare: the groups' values in 64 bits, as far as it is sure which members make them.
-      const uint32_t end = two ? t.b : t.a, after = lanes_two_best({unlike(end), 0u}, glog).a;
+      // A second member's equal is no more than the first only where the second is.
+      const uint32_t end = two ? t.b : t.a;
+      const bool mixed = two && nearby(t.a, t.b) && !equal(t.a, t.b);
+      const uint32_t after = lanes_two_best({behind_of(end, mixed), 0u}, glog).a;
       if (!group_any<L>(end >= C && nearby(end, after))) {
         const double sum = sum64();
         double w = value64(t.a, sum);
@@ -779,7 +782,7 @@ MOE_DEV bool choose32(const RouterArgs& a, const float* l, float top, const floa
     near = near && !same;
     if (group_any<L>(same && li == k - 1)) {             // the whole group: what comes behind the last place's equals
       const uint32_t last = group_all<L>(on ? mine : ~0u, OpMin());
-      near |= nearby(last, group_all<L>(unlike(last), OpMax()));
+      near |= nearby(last, group_all<L>(behind_of(last, false), OpMax()));
     }
     if (!unsure && group_any<L>(near)) {                 // the whole group
       // Rare: the list's values in 64 bits, a lane each, as far as none behind it is near to the last place's.

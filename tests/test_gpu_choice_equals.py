@@ -4,6 +4,8 @@ Scores of sigmoid logits around 20 differ by 10^-9 and less, those of neighbouri
 to nothing in 32 bits, where the lower index leads, and apart in 64.  Two of the lower logit first, then the higher one:
 the last place (or the member that makes a group's value) is followed by its equal, and the expert that belongs there
 comes behind both."""
+import itertools
+
 import numpy as np
 import pytest
 import torch
@@ -76,3 +78,25 @@ def test_members_before_equals(score, dtype, E, groups, top, rank, with_bias):
     logits = torch.from_numpy(np.stack(rows)).to(dtype).to(DEV)
     bias = torch.full((E,), 0.25, device=DEV) if with_bias else None
     _check(logits, min(8, top * size), score, True, bias, groups, top, rank)
+
+
+@pytest.mark.parametrize("score,dtype", KINDS)
+@pytest.mark.parametrize("E,groups,top", [(16, 2, 1), (32, 4, 2), (64, 4, 1), (256, 8, 4), (12, 3, 1), (1024, 32, 5)])
+@pytest.mark.parametrize("rank", ["max", "top2"])
+def test_every_order_of_near_members(score, dtype, E, groups, top, rank):
+    """Two to four members of a group on three near levels, in every order: the two that make its value may be a lower
+    one and a higher one whose equal is left out."""
+    say(f"[orders] {score} {dtype} E={E} groups={groups}/{top} {rank}")
+    rng = np.random.default_rng(E + 7 * groups)
+    near, far = _levels(score, dtype)
+    size = E // groups
+    orders = [o for n in (2, 3, 4) for o in itertools.product(near, repeat=n)]
+    rows = []
+    for o in orders:
+        row = np.full(E, far, dtype=np.float32)
+        for g in range(groups):
+            members = o if g == 0 else orders[rng.integers(len(orders))]
+            row[g * size + np.sort(rng.choice(size, len(members), replace=False))] = members
+        rows.append(row)
+    logits = torch.from_numpy(np.stack(rows)).to(dtype).to(DEV)
+    _check(logits, min(3, top * size), score, True, None, groups, top, rank)
