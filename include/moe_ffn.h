@@ -489,8 +489,8 @@ int moe_router_forward(const moe_router* R, const void* logits, int ld,
  * balances the experts with it) and enters no gate.  The E experts form `groups` groups of E / groups
  * consecutive ones; a group's value is its best member's, or the sum of its two best (of one where only
  * one can be chosen).  The top_groups best groups are open, and the chosen experts are the k largest
- * values in them, in descending order; the lower index among equals, groups and experts alike.  Values are
- * compared as 64-bit numbers.  An expert whose bias is NaN or -infinity is never chosen. */
+ * values in them, in descending order; the lower index among equals, groups and experts alike.  Values, and sums
+ * of two, are compared as 64-bit numbers.  An expert whose bias is NaN or -infinity is never chosen. */
 typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
 typedef struct {
   const float* bias;     /* [E] device, nullable */

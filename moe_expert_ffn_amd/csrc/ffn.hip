@@ -1507,9 +1507,12 @@ struct SrcFc2F8 : SrcFc2T<true> {
 // item slot of LDS: rows' at 1024 (FC1 reads its slot map at 0), weight rows' in a slot of their own behind
 // the scratch.  A step moves the bytes of a bf16 one and has its MFMAs, of twice the products.  The Qwen3-shaped
 // batch of 8192 tokens: FC1 412 G operations in 240 to 270 us (1.5 to 1.7 P/s; the matrix units are busy 47% of
-// the CUs' cycles), bound as the bf16 one by the load path of a CU; FC2 206 G in 169 to 178 us (33%), by that and
-// the 268 MB of O that it writes in epilogues which nothing overlaps.  (An 8192^3 product of the installed
-// library: 2.1 P/s.)
+// the CUs' cycles), FC2 206 G in 169 to 178 us (33%).  Neither a CU's load path nor HBM is full alone: FC1 reads
+// 795 MB, its 403 MB of weights about once for each of an expert's two row tiles, and writes 101, 3.7 TB/s in all;
+// FC2 reads 317 MB and writes the 268 of O in epilogues that nothing overlaps, 3.5 TB/s (a large copy: 6.3).
+// Which of the two costs more was not separated.  (An 8192^3 product of the installed library: 2.1 P/s.)
+// A contribution p O is rounded to bf16 as every layer's of bf16 activations is, and the k of a token are added in
+// fp32: the output is 0.0026 of its norm off where sums kept in fp32 would be 0.0019 off, and O is half as large.
 constexpr size_t kI8ScaleOff = kStreamLds;
 constexpr size_t kStreamLdsI8 = kStreamLds + kItemSlots * 1024;
 using RowI8 = RowKI8<256, kWNW>;
@@ -2562,8 +2565,11 @@ static void run_forward_stream(const Sizes& z, ExecArgs& a, const int32_t* row_t
 // Where experts have few rows, a 256-row tile of the stream kernels is mostly empty and their items are too few for
 // the chip; where they have more, the rows' codes are what the tiles of few rows read most.  Forward, us, by tiles
 // of few rows and by the stream kernels: 128 experts of 2048 x 768, 4 rows each on average 147 and 164, 6 rows 170
-// and 170, 8 rows 180 and 172; 32 of 7168 x 2048, 4 rows 316 and 324, 6 rows 340 and 337.  (Sizes off the 256 grid
-// have no others.)
+// and 170, 8 rows 180 and 172; 32 of 7168 x 2048, 4 rows 316 and 324, 6 rows 340 and 337.  All slots were routed
+// there.  Slots of other ranks' experts count here too, since the host knows no others: 32 such experts with one
+// slot of eight routed take 119 us for 16 tokens (16 rows) and, by the stream kernels, 242 for 24 (27 rows).
+// Sizes off the 256 grid have no other form, and where their rows are many it is far from its operations: 8192
+// tokens, 6 of 64 experts of 2048 x 1408, 2834 us for 850 G operations (0.3 P/s).
 bool i8_few(const Sizes& z) { return !use_stream(z) || (long long)z.T * z.k <= 5ll * z.E; }
 
 static void run_forward_int8(const Sizes& z, ExecArgs& a, const int32_t* row_to_slot, void* y, void* const* ev,

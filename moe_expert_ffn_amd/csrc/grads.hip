@@ -93,9 +93,9 @@ MOE_DEV double sum_doubles(double s) {
 
 // Squares and sums in 64 bits: no gradient is too small or too large for its square, and the order of
 // the sum, which the sizes alone fix, does not show in the 24 bits of the result.  The last workgroup to
-// finish joins the partial sums.  Bound by HBM, which reads faster than it copies: 604M fp32 elements in
-// 385 us (6.3 TB/s; a 1 GiB copy reaches 5.1), two 64-bit instructions an element being 50 us of the VALU; a
-// few small tensors take 6 us, the latency of the search, a read and the join.
+// finish joins the partial sums.  Bound by HBM: 604M fp32 elements in 385 us (6.3 TB/s, as fast as an
+// elementwise kernel copies 1 GiB; the runtime's own copy reaches 5.2), two 64-bit instructions an element
+// being 50 us of the VALU; a few small tensors take 6 us, the latency of the search, a read and the join.
 __global__ __launch_bounds__(kGradThreads) void k_grad_norm(GradArgs a) {
   __shared__ double red[kGradThreads / 64];
   __shared__ int last;
@@ -124,7 +124,8 @@ __global__ __launch_bounds__(kGradThreads) void k_grad_norm(GradArgs a) {
     s = red[0] + red[1] + red[2] + red[3];
     // The partial sums are device-scope stores and loads, which pass the XCD's own L2, so the wait alone
     // orders them with the counters: a release at device scope writes that L2 back, and one counter takes
-    // its workgroups one by one (25M bf16: 60 us with both, 31 with one counter and no release, 11 so).
+    // its workgroups one by one (25M bf16: 60 us with both, 31 with one counter and no release, 11 so).  It
+    // relies on gfx950 acknowledging a device-scope store once it is past the XCD's L2.
     __hip_atomic_store(a.tab.part + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");
     __builtin_amdgcn_s_waitcnt(0);

@@ -72,8 +72,9 @@ struct MostBf16 {
 // NT threads take a row; its first KC pieces of 8 elements a thread stay in registers between the maximum
 // and the codes, further ones are read again.
 // WG threads a workgroup, which is number `block` of `blocks`.  65536 rows of 768 bf16: 151 MB in 34 us
-// (4.5 TB/s, some 13 VALU instructions an element).  Short pieces' masks, made before the loop, of whose rows a
-// lane has one or two, and codes by comparison took 45.
+// (4.5 TB/s, some 13 VALU instructions an element).  With short pieces' masks made before the loop, of whose rows a
+// lane has one or two, 42, and with codes by comparison as well 45.  196608 rows of 2048 fp32, a layer's weights:
+// 2.01 GB in 367 us (5.5 TB/s).
 template <typename T, int NT, int KC, int WG> MOE_DEV void quant_i8_rows(const QuantI8& a, int block, int blocks) {
   constexpr int RPW = WG / NT;
   __shared__ uint32_t red[WG / 64];

@@ -160,7 +160,7 @@ template <typename T, int N> MOE_DEV void store_upto(T* p, int n, const T* v) {
 }
 
 // A wave-uniform number that the compiler forgets: its comparisons are made where they are used.  (Kept over
-// k_choice's loop of rows as masks, they took 160 scalar registers to VGPRs and back: 65521 x 256 87 us, now 61.)
+// k_choice's loop of rows as masks, they took 160 scalar registers to VGPRs and back: 65521 x 256 87 us, now 62.)
 MOE_DEV int fresh(int v) {
   asm volatile("" : "+s"(v));
   return v;

@@ -248,7 +248,9 @@ class BlockRunner(LayerRunner):
     def optimizer_step(self, lr, step, max_norm=None, grad_scale=None, **hyper):
         """One AdamW step (binding.adamw's arguments) on the block's weights, in place.  The gradients are
         taken times grad_scale, a number or a tensor.  max_norm: they are then scaled down to this norm where
-        theirs, which self.grad_norm receives, is above it."""
+        theirs, which self.grad_norm receives, is above it.  That norm is this block's alone; one over several
+        blocks' gradients is binding.grad_norm's of a list of all (binding.make_grads), whose scale goes here
+        as grad_scale.  A gradient that is not finite sets DEV_BAD_GRAD in self.status."""
         if self.optimizer is None:
             raise B.MoeError("make_optimizer first")
         if max_norm is not None:
