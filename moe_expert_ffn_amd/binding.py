@@ -974,7 +974,8 @@ class PreparedGrads:
 
     def __init__(self, c_list, ws, keep):
         self.list, self.ws, self.keep = c_list, ws, keep
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in (*keep, ws) if t.numel())
+        sizes = [(t.data_ptr(), t.nbytes) for t in (*keep, ws)]
+        spans = sorted((at, at + n) for at, n in sizes if n)
         self.begins = [b for b, _ in spans]
         self.ends = list(itertools.accumulate((e for _, e in spans), max))    # the furthest of those up to each
 

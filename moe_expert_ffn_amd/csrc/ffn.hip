@@ -1507,12 +1507,12 @@ struct SrcFc2F8 : SrcFc2T<true> {
 // item slot of LDS: rows' at 1024 (FC1 reads its slot map at 0), weight rows' in a slot of their own behind
 // the scratch.  A step moves the bytes of a bf16 one and has its MFMAs, of twice the products.  The Qwen3-shaped
 // batch of 8192 tokens: FC1 412 G operations in 240 to 270 us (1.5 to 1.7 P/s; the matrix units are busy 47% of
-// the CUs' cycles), FC2 206 G in 169 to 178 us (33%).  Neither a CU's load path nor HBM is full alone: FC1 reads
-// 795 MB, its 403 MB of weights about once for each of an expert's two row tiles, and writes 101, 3.7 TB/s in all;
-// FC2 reads 317 MB and writes the 268 of O in epilogues that nothing overlaps, 3.5 TB/s (a large copy: 6.3).
-// Which of the two costs more was not separated.  (An 8192^3 product of the installed library: 2.1 P/s.)
+// the CUs' cycles), FC2 206 G in 169 to 178 us (33%).  What bounds them, a CU's load path as in bf16 or HBM, was not
+// separated: FC1 reads 793 MB, its 403 MB of weights about once for each of an expert's two row tiles, and writes
+// 101, 3.7 TB/s in all; FC2 reads 316 MB and writes the 268 of O in epilogues that nothing overlaps, 3.5 TB/s (a
+// large copy: 6.3).  (An 8192^3 product of the installed library: 2.1 P/s.)
 // A contribution p O is rounded to bf16 as every layer's of bf16 activations is, and the k of a token are added in
-// fp32: the output is 0.0026 of its norm off where sums kept in fp32 would be 0.0019 off, and O is half as large.
+// fp32: the output is 0.0025 of its norm off (0.0018 with contributions in fp32), and O is half as large.
 constexpr size_t kI8ScaleOff = kStreamLds;
 constexpr size_t kStreamLdsI8 = kStreamLds + kItemSlots * 1024;
 using RowI8 = RowKI8<256, kWNW>;
