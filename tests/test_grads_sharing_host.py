@@ -9,12 +9,12 @@ FULL = torch.zeros(4096)                       # one allocation, so that places 
 
 def _list():
     grads = [FULL[100:200], FULL[0:0], FULL[300:1300].view(10, 100), FULL[500:600], FULL[1400:1401]]
-    ws = FULL[2048:3072].view(torch.uint8)
+    ws = FULL[2048:2560].view(torch.uint8)
     return B.PreparedGrads(B.GradList(ws.data_ptr(), len(grads), 4, 0), ws, grads)
 
 
-INSIDE = [100, 150, 199, 300, 500, 599, 600, 1299, 1400, 2048, 3071]
-OUTSIDE = [0, 99, 200, 299, 1300, 1399, 1401, 2047, 3072, 4095]
+INSIDE = [100, 150, 199, 300, 500, 599, 600, 1299, 1400, 2048, 2559]
+OUTSIDE = [0, 99, 200, 299, 1300, 1399, 1401, 2047, 2560, 4095]
 
 
 @pytest.mark.parametrize("at", INSIDE)
